@@ -301,6 +301,117 @@ SAGA_API int saga_key_head_merge(const saga_merge_shape* s, const void* x, const
                                  size_t ws_bytes, void* stream);
 SAGA_API const char* saga_merge_last_error(void);
 
+/* ---------------------------------------------------------------------------
+ * Serving operators around the caches: many new tokens per call, batch rows of
+ * different lengths, caches of 8-bit rows.  (The paper's evaluation decodes one
+ * token at a time from bf16 caches; these calls have no counterpart in it.)
+ *
+ * A cache is described by saga_cache.  SAGA_CACHE_BF16: k and v as everywhere
+ * above, the scales unused.  SAGA_CACHE_E4M3: k [B, h_k, l_cap, d] and
+ * v [B, h_v, l_cap, d] hold one e4m3 code per element, k_scale
+ * [B, h_k, l_cap] and v_scale [B, h_v, l_cap] one fp32 scale per row:
+ *   amax  = max(max |x|, 2^-100) over the row's d elements,
+ *   scale = amax / 448,  code = e4m3(x * (448 / amax))  (nearest even),
+ *   and the row stands for code * scale.
+ * k and v 16-byte aligned, the scales 4-byte aligned.
+ *
+ * Per-batch lengths are device int32 arrays of B entries, read when the kernels
+ * run; with them the calls can be captured into CUDA graphs and replayed at
+ * other lengths.  Batch row b holds counts[b] of the `tokens` new tokens
+ * (counts NULL: all of them; values outside [0, tokens] are clamped); nothing
+ * of the others is read or written.  Inputs must be finite. */
+#define SAGA_CACHE_BF16 0
+#define SAGA_CACHE_E4M3 1
+
+typedef struct saga_cache {
+  void* k;        /* bf16 or e4m3 [B, h_k, l_cap, d] */
+  void* v;        /* bf16 or e4m3 [B, h_v, l_cap, d] */
+  float* k_scale; /* fp32 [B, h_k, l_cap] (SAGA_CACHE_E4M3) */
+  float* v_scale; /* fp32 [B, h_v, l_cap] */
+  int format;     /* SAGA_CACHE_* */
+} saga_cache;
+
+/* New tokens' rows of one kind: bf16, element (b, t, head, i) at
+ * data[b * batch_stride + t * token_stride + head * head_stride + i].  Strides
+ * in elements, non-negative multiples of 8 (0 repeats a row); data 16-byte
+ * aligned.  (A packed projection output is three of these into one buffer; a
+ * bf16 cache [B, h, l_cap, d] is one with its rows as tokens.) */
+typedef struct saga_rows {
+  const void* data;
+  long long batch_stride;
+  long long token_stride;
+  long long head_stride;
+} saga_rows;
+
+typedef struct saga_norm_rope {
+  int norm;               /* nonzero: x * w / sqrt(mean(x^2) + eps) over each head of q and k, before the rotation */
+  float eps;              /* >= 0, finite */
+  const void* q_weight;   /* bf16 [d], 16-byte aligned (NULL: ones) */
+  const void* k_weight;   /* bf16 [d], 16-byte aligned (NULL: ones) */
+  const float* inv_freq;  /* fp32 [rot_dim / 2]; NULL: no rotation */
+  int rot_dim;            /* rotated elements of each head, from its first on: a multiple of 16 up to d */
+  int interleaved;        /* pairs (2i, 2i + 1); 0: pairs (i, i + rot_dim / 2) */
+} saga_norm_rope;
+
+/* Norm and position rotation of every query and key head in one pass over a
+ * projection's rows, with the append: for every present token (b, t),
+ *   q_out[b, t] = rot(norm(q[b, t]))  (bf16 [B, tokens, h_q, d], dense),
+ *   cache row starts[b] + t of the key heads   = rot(norm(k[b, t])),
+ *   cache row starts[b] + t of the value heads = v[b, t].
+ * The rotation turns pair i = (x, y) by a = position * inv_freq[i] into
+ * (x cos a - y sin a, y cos a + x sin a); position = positions[b * tokens + t],
+ * or the cache row where positions is NULL.  Norm sums and products are fp32,
+ * the angle is reduced in fp64, each output is rounded once.  A token whose
+ * cache row lies outside [0, l_cap) is not appended (its q_out is written) and
+ * SAGA_STATUS_LEN_CLAMPED is ORed into *status (nullable device word).
+ * q_out may be q itself when q is dense; it overlaps no other argument. */
+SAGA_API int saga_norm_rope_append(const saga_shape* s, int tokens, const saga_rows* q, const saga_rows* k,
+                                   const saga_rows* v, const saga_norm_rope* op, const int* starts,
+                                   const int* positions, const int* counts, void* q_out, const saga_cache* cache,
+                                   unsigned* status, void* stream);
+
+/* The append alone: cache rows starts[b] + t of present tokens = k[b, t],
+ * v[b, t], into either format. */
+SAGA_API int saga_kv_store(const saga_shape* s, int tokens, const saga_rows* k, const saga_rows* v,
+                           const int* starts, const int* counts, const saga_cache* cache, unsigned* status,
+                           void* stream);
+
+/* Rows [start, start + rows) of an 8-bit cache as bf16 (code * scale, rounded
+ * once): k_out [B, h_k, rows, d], v_out [B, h_v, rows, d], either NULL.  With
+ * lens, batch row b's rows at or past lens[b] are left as they are.  (An exact
+ * threshold refresh of an 8-bit cache reads such keys.) */
+SAGA_API int saga_kv_load(const saga_shape* s, const saga_cache* cache, int start, int rows, const int* lens,
+                          void* k_out, void* v_out, void* stream);
+
+/* Attention of drafted tokens over a cache, for verifying several candidate
+ * continuations at once (tokens = 1: a decode step over either format).
+ * Batch row b has prefix_lens[b] cached tokens that every drafted token sees,
+ * and its drafted tokens' own keys and values already at cache rows
+ * prefix_lens[b] + u (saga_norm_rope_append or saga_kv_store puts them there).
+ * Drafted token t sees drafted token u where bit u of tree_mask[b * tokens + t]
+ * is set (its ancestors and itself, for a tree); tree_mask NULL: u <= t.
+ *   A[i] = q[b, t, j] . K[i] / sqrt(d) over the visible rows i,
+ *   kept: all of them, or with tau (fp32 [B, h_q], the thresholds of the last
+ *         refresh) those with A[i] >= tau[b, j], as a reuse step keeps them,
+ *   out[b, t, j] = softmax(A)[kept] V[kept];  0 where nothing is kept.
+ *   q    bf16 [B, tokens, h_q, d], out fp32 or bf16 [B, tokens, h_q, d], dense;
+ *   tree_mask uint64 [B, tokens]; bits at or past counts[b] are ignored;
+ *   1 <= tokens <= SAGA_TREE_MAX_TOKENS.
+ * Scores, softmax statistics and sums are fp32; the softmax weights are rounded
+ * to 16 bits before the product with the values.  Rows of absent tokens of out
+ * are left as they are.  Cache rows that no present token sees may hold
+ * anything; a row that some token sees must be finite.  A prefix outside
+ * [0, l_cap - counts[b]] is clamped and flagged in the status word (word 0 of
+ * the workspace, saga_get_status).  workspace: saga_tree_workspace_bytes(s,
+ * tokens) bytes of device memory, 256-byte aligned, zero-filled once before
+ * first use; calls on one workspace must not overlap in time. */
+#define SAGA_TREE_MAX_TOKENS 64
+SAGA_API size_t saga_tree_workspace_bytes(const saga_shape* s, int tokens);
+SAGA_API int saga_tree_attn(const saga_shape* s, int tokens, const void* q, const saga_cache* cache,
+                            const int* prefix_lens, const int* counts, const unsigned long long* tree_mask,
+                            const float* tau, void* out, int out_dtype, void* workspace, size_t ws_bytes,
+                            void* stream);
+
 /* Measurement aid (no counterpart in the paper): one streaming read of
  * `bytes` of device memory at buf (16-byte aligned; the last bytes % 16 are
  * not read), 16-byte loads with four in flight per thread over a grid of up

@@ -12,6 +12,7 @@
 
 #include "saga.h"
 #include "saga_internal.h"
+#include "saga_serve.h"
 
 namespace saga {
 cudaError_t launch_split(int D, int NP, int mode, const CUtensorMap& tf, const CUtensorMap& tp, const SplitParams& p,
@@ -382,6 +383,21 @@ int run_refresh(const saga_shape* s, const Prepared& pr, const void* q, const vo
 }
 
 }  // namespace
+
+namespace saga {
+// The error text and the shared checks, for the entry points in other files.
+int api_fail(int code, const char* fmt, ...) {
+  va_list ap;
+  va_start(ap, fmt);
+  vsnprintf(g_err, sizeof(g_err), fmt, ap);
+  va_end(ap);
+  return code;
+}
+int api_ok() { return ok(); }
+int api_cuda_fail(cudaError_t e, const char* what) { return cuda_fail(e, what); }
+int api_validate_shape(const saga_shape* s) { return validate_shape(s); }
+int api_device_sms(int* sms) { return device_sms(sms); }
+}  // namespace saga
 
 extern "C" {
 

@@ -26,13 +26,17 @@ SAGA_OUT_F32 = 0
 SAGA_OUT_BF16 = 1
 SAGA_STATUS_LEN_CLAMPED = 0x1
 SAGA_STATUS_TIMEOUT = 0x2
+SAGA_CACHE_BF16 = 0
+SAGA_CACHE_E4M3 = 1
+SAGA_TREE_MAX_TOKENS = 64
 
 EXPORTED = ("saga_workspace_bytes", "saga_kv_append", "atopn_refresh_threshold", "atopn_select_workspace_bytes",
             "atopn_select_threshold", "saga_decode_attn", "saga_trace_next_attention", "saga_get_status", "saga_last_error", "saga_abi_version",
             "saga_noalloc_scratch_bytes", "saga_decode_attn_noalloc", "saga_noalloc_get_status",
             "saga_noalloc_last_error", "saga_decode_step", "saga_test_expire_next_wait", "saga_read_probe_sink_words",
             "saga_read_probe", "saga_merge_workspace_bytes", "saga_key_head_merge", "saga_merge_last_error",
-            "saga_qkv_project", "saga_qkv_workspace_bytes")
+            "saga_qkv_project", "saga_qkv_workspace_bytes", "saga_norm_rope_append", "saga_kv_store", "saga_kv_load",
+            "saga_tree_workspace_bytes", "saga_tree_attn")
 
 
 class SagaError(RuntimeError):
@@ -56,6 +60,22 @@ class SagaShape(ctypes.Structure):
 class SagaMergeShape(ctypes.Structure):
     _fields_ = [("tokens", ctypes.c_int), ("hidden", ctypes.c_int), ("d", ctypes.c_int), ("h_q", ctypes.c_int),
                 ("h_k", ctypes.c_int)]
+
+
+class _Cache(ctypes.Structure):
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("k_scale", ctypes.c_void_p),
+                ("v_scale", ctypes.c_void_p), ("format", ctypes.c_int)]
+
+
+class _Rows(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p), ("batch_stride", ctypes.c_longlong), ("token_stride", ctypes.c_longlong),
+                ("head_stride", ctypes.c_longlong)]
+
+
+class _NormRope(ctypes.Structure):
+    _fields_ = [("norm", ctypes.c_int), ("eps", ctypes.c_float), ("q_weight", ctypes.c_void_p),
+                ("k_weight", ctypes.c_void_p), ("inv_freq", ctypes.c_void_p), ("rot_dim", ctypes.c_int),
+                ("interleaved", ctypes.c_int)]
 
 
 _lib = None
@@ -123,6 +143,17 @@ def load(path: Optional[str] = None):
     lib.saga_read_probe.restype = _I
     lib.saga_noalloc_last_error.argtypes = []
     lib.saga_noalloc_last_error.restype = ctypes.c_char_p
+    cp, rp, np_ = ctypes.POINTER(_Cache), ctypes.POINTER(_Rows), ctypes.POINTER(_NormRope)
+    lib.saga_norm_rope_append.argtypes = [sp, _I, rp, rp, rp, np_, _P, _P, _P, _P, cp, _P, _P]
+    lib.saga_norm_rope_append.restype = _I
+    lib.saga_kv_store.argtypes = [sp, _I, rp, rp, _P, _P, cp, _P, _P]
+    lib.saga_kv_store.restype = _I
+    lib.saga_kv_load.argtypes = [sp, cp, _I, _I, _P, _P, _P, _P]
+    lib.saga_kv_load.restype = _I
+    lib.saga_tree_workspace_bytes.argtypes = [sp, _I]
+    lib.saga_tree_workspace_bytes.restype = ctypes.c_size_t
+    lib.saga_tree_attn.argtypes = [sp, _I, _P, cp, _P, _P, _P, _P, _P, _I, _P, ctypes.c_size_t, _P]
+    lib.saga_tree_attn.restype = _I
     _lib = lib
     return lib
 
@@ -388,6 +419,206 @@ def key_head_merge(x, q, w_k, h_k: int, workspace=None, stream=None):
     if rc != SAGA_OK:
         raise SagaError(rc, lib.saga_merge_last_error().decode(errors="replace"))
     return loss, pairing, merged, workspace
+
+
+class KVCache:
+    """One layer's caches in either format: bf16 k [B, h_k, l_cap, d] and v [B, h_v, l_cap, d], or e4m3 codes of the
+    same shapes (float8_e4m3fn or uint8) with one fp32 scale per row, k_scale [B, h_k, l_cap] and v_scale."""
+
+    def __init__(self, k, v, k_scale=None, v_scale=None):
+        if (k_scale is None) != (v_scale is None):
+            raise ValueError("pass both scales (an 8-bit cache) or neither (bf16)")
+        self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
+        self.format = SAGA_CACHE_BF16 if k_scale is None else SAGA_CACHE_E4M3
+
+    def _struct(self, shape: SagaShape) -> "_Cache":
+        B, hq, hk, hv, d, lc = shape.astuple()
+        for name, t, h in (("cache.k", self.k, hk), ("cache.v", self.v, hv)):
+            if self.format == SAGA_CACHE_BF16:
+                _expect(t, name, torch.bfloat16, (B, h, lc, d))
+            else:
+                _expect(t, name, torch.uint8 if t.dtype == torch.uint8 else torch.float8_e4m3fn, (B, h, lc, d))
+        if self.format == SAGA_CACHE_E4M3:
+            _expect(self.k_scale, "cache.k_scale", torch.float32, (B, hk, lc))
+            _expect(self.v_scale, "cache.v_scale", torch.float32, (B, hv, lc))
+        return _Cache(self.k.data_ptr(), self.v.data_ptr(),
+                      None if self.k_scale is None else self.k_scale.data_ptr(),
+                      None if self.v_scale is None else self.v_scale.data_ptr(), self.format)
+
+    def _tensors(self):
+        return (self.k, self.v, self.k_scale, self.v_scale)
+
+
+def alloc_cache(shape: SagaShape, format: int = SAGA_CACHE_BF16, device=None) -> KVCache:
+    """Zero-filled caches of either format on `device`."""
+    B, hq, hk, hv, d, lc = shape.astuple()
+    device = device or "cuda"
+    if format == SAGA_CACHE_BF16:
+        return KVCache(torch.zeros((B, hk, lc, d), dtype=torch.bfloat16, device=device),
+                       torch.zeros((B, hv, lc, d), dtype=torch.bfloat16, device=device))
+    if format != SAGA_CACHE_E4M3:
+        raise ValueError(f"unknown cache format {format}")
+    return KVCache(torch.zeros((B, hk, lc, d), dtype=torch.float8_e4m3fn, device=device),
+                   torch.zeros((B, hv, lc, d), dtype=torch.float8_e4m3fn, device=device),
+                   torch.zeros((B, hk, lc), dtype=torch.float32, device=device),
+                   torch.zeros((B, hv, lc), dtype=torch.float32, device=device))
+
+
+def _rows(t, name: str, B: int, T: int, heads: int, d: int) -> "_Rows":
+    """A [B, T, heads, d] tensor or view whose last dimension is dense."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dtype != torch.bfloat16:
+        raise TypeError(f"{name} must be torch.bfloat16, got {t.dtype}")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if tuple(t.shape) != (B, T, heads, d):
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {(B, T, heads, d)}")
+    if t.stride(3) != 1:
+        raise ValueError(f"{name}: the elements of a head must be dense (strides {t.stride()})")
+    # a dimension of one element has no stride that matters
+    return _Rows(t.data_ptr(), t.stride(0) if B > 1 else 0, t.stride(1) if T > 1 else 0,
+                 t.stride(2) if heads > 1 else 0)
+
+
+def _tokens(t, name: str) -> int:
+    if not isinstance(t, torch.Tensor) or t.dim() != 4:
+        raise ValueError(f"{name} must be a 4-D tensor [batch, tokens, heads, d]")
+    return int(t.shape[1])
+
+
+class _on_device:
+    """Makes the tensors' device current for a call; they must all be on one device."""
+
+    def __init__(self, *tensors):
+        devices = {t.device for t in tensors if t is not None}
+        if len(devices) != 1:
+            raise ValueError(f"tensors on different devices: {sorted(map(str, devices))}")
+        self._guard = torch.cuda.device(devices.pop())
+
+    def __enter__(self):
+        return self._guard.__enter__()
+
+    def __exit__(self, *exc):
+        return self._guard.__exit__(*exc)
+
+
+def saga_norm_rope_append(shape: SagaShape, q, k, v, cache: KVCache, starts, q_out, positions=None, counts=None,
+                          norm: bool = False, q_weight=None, k_weight=None, eps: float = 1e-6, inv_freq=None,
+                          interleaved: bool = False, status=None, stream=None):
+    """Per-head norm (norm=True) and position rotation (inv_freq fp32 [rot_dim / 2]) of the new tokens' queries and
+    keys, with the append of keys and values at cache rows starts[b] + t.  q, k, v: bf16 [B, T, heads, d], strided
+    views allowed; q_out: bf16 [B, T, h_q, d]; starts, counts: int32 [B]; positions: int32 [B, T] (the
+    cache row where None); status: a workspace tensor whose word 0 takes SAGA_STATUS_LEN_CLAMPED."""
+    B, hq, hk, hv, d, lc = shape.astuple()
+    T = _tokens(q, "q")
+    rq, rk, rv = _rows(q, "q", B, T, hq, d), _rows(k, "k", B, T, hk, d), _rows(v, "v", B, T, hv, d)
+    _expect(q_out, "q_out", torch.bfloat16, (B, T, hq, d))
+    _expect(starts, "starts", torch.int32, (B,))
+    if positions is not None:
+        _expect(positions, "positions", torch.int32, (B, T))
+    if counts is not None:
+        _expect(counts, "counts", torch.int32, (B,))
+    if not norm and (q_weight is not None or k_weight is not None):
+        raise ValueError("norm weights without norm=True")
+    for name, w in (("q_weight", q_weight), ("k_weight", k_weight)):
+        if w is not None:
+            _expect(w, name, torch.bfloat16, (d,))
+    rot = 0
+    if inv_freq is not None:
+        _expect(inv_freq, "inv_freq", torch.float32)
+        if inv_freq.dim() != 1:
+            raise ValueError("inv_freq must be 1-D [rot_dim / 2]")
+        rot = 2 * int(inv_freq.shape[0])
+    if status is not None:
+        _expect(status, "status", torch.uint8)
+        if status.numel() < 4:
+            raise ValueError("status must hold 4 bytes")
+    op = _NormRope(1 if norm else 0, float(eps), None if q_weight is None else q_weight.data_ptr(),
+                   None if k_weight is None else k_weight.data_ptr(),
+                   None if inv_freq is None else inv_freq.data_ptr(), rot, 1 if interleaved else 0)
+    c = cache._struct(shape)
+    with _on_device(q, k, v, q_out, starts, positions, counts, q_weight, k_weight, inv_freq, status,
+                    *cache._tensors()):
+        _check(load().saga_norm_rope_append(ctypes.byref(shape), T, ctypes.byref(rq), ctypes.byref(rk),
+                                            ctypes.byref(rv), ctypes.byref(op), _ptr(starts), _ptr(positions),
+                                            _ptr(counts), _ptr(q_out), ctypes.byref(c), _ptr(status),
+                                            _stream(stream)))
+
+
+def saga_kv_store(shape: SagaShape, k, v, cache: KVCache, starts, counts=None, status=None, stream=None):
+    """Appends the new tokens' keys and values (bf16 [B, T, heads, d], strided views allowed) at cache rows
+    starts[b] + t, in the cache's format."""
+    B, hq, hk, hv, d, lc = shape.astuple()
+    T = _tokens(k, "k")
+    rk, rv = _rows(k, "k", B, T, hk, d), _rows(v, "v", B, T, hv, d)
+    _expect(starts, "starts", torch.int32, (B,))
+    if counts is not None:
+        _expect(counts, "counts", torch.int32, (B,))
+    if status is not None:
+        _expect(status, "status", torch.uint8)
+        if status.numel() < 4:
+            raise ValueError("status must hold 4 bytes")
+    c = cache._struct(shape)
+    with _on_device(k, v, starts, counts, status, *cache._tensors()):
+        _check(load().saga_kv_store(ctypes.byref(shape), T, ctypes.byref(rk), ctypes.byref(rv), _ptr(starts),
+                                    _ptr(counts), ctypes.byref(c), _ptr(status), _stream(stream)))
+
+
+def saga_kv_load(shape: SagaShape, cache: KVCache, start: int, rows: int, k_out=None, v_out=None, lens=None,
+                 stream=None):
+    """Rows [start, start + rows) of an 8-bit cache as bf16 into k_out [B, h_k, rows, d] and v_out [B, h_v, rows, d]
+    (either may be None); with lens (int32 [B]) rows at or past lens[b] are left as they are."""
+    B, hq, hk, hv, d, lc = shape.astuple()
+    if k_out is not None:
+        _expect(k_out, "k_out", torch.bfloat16, (B, hk, int(rows), d))
+    if v_out is not None:
+        _expect(v_out, "v_out", torch.bfloat16, (B, hv, int(rows), d))
+    if lens is not None:
+        _expect(lens, "lens", torch.int32, (B,))
+    c = cache._struct(shape)
+    with _on_device(k_out, v_out, lens, *cache._tensors()):
+        _check(load().saga_kv_load(ctypes.byref(shape), ctypes.byref(c), int(start), int(rows), _ptr(lens),
+                                   _ptr(k_out), _ptr(v_out), _stream(stream)))
+
+
+def saga_tree_workspace_bytes(shape: SagaShape, tokens: int) -> int:
+    n = load().saga_tree_workspace_bytes(ctypes.byref(shape), int(tokens))
+    if n == 0:
+        raise SagaError(SAGA_ERR_ARG, load().saga_last_error().decode(errors="replace"))
+    return int(n)
+
+
+def alloc_tree_workspace(shape: SagaShape, tokens: int, device=None) -> torch.Tensor:
+    """Zero-filled workspace of saga_tree_workspace_bytes(shape, tokens) bytes on `device`."""
+    return torch.zeros(saga_tree_workspace_bytes(shape, tokens), dtype=torch.uint8, device=device or "cuda")
+
+
+def saga_tree_attn(shape: SagaShape, q, cache: KVCache, prefix_lens, out, workspace, tree_mask=None, counts=None,
+                   tau=None, stream=None):
+    """Attention of drafted tokens: q bf16 [B, T, h_q, d] over prefix_lens[b] cached rows and the drafted rows at
+    prefix_lens[b] + u that tree_mask (int64 or uint64 words [B, T]; None: u <= t) shows; tau fp32 [B, h_q] keeps
+    scores at or above the thresholds.  out: fp32 or bf16 [B, T, h_q, d]."""
+    B, hq, hk, hv, d, lc = shape.astuple()
+    T = _tokens(q, "q")
+    _expect(q, "q", torch.bfloat16, (B, T, hq, d))
+    _expect(prefix_lens, "prefix_lens", torch.int32, (B,))
+    if not isinstance(out, torch.Tensor) or out.dtype not in (torch.float32, torch.bfloat16):
+        raise TypeError("out must be float32 or bfloat16")
+    _expect(out, "out", out.dtype, (B, T, hq, d))
+    _expect(workspace, "workspace", torch.uint8)
+    if tree_mask is not None:
+        _expect(tree_mask, "tree_mask", torch.uint64 if tree_mask.dtype == torch.uint64 else torch.int64, (B, T))
+    if counts is not None:
+        _expect(counts, "counts", torch.int32, (B,))
+    if tau is not None:
+        _expect(tau, "tau", torch.float32, (B, hq))
+    c = cache._struct(shape)
+    with _on_device(q, prefix_lens, out, workspace, tree_mask, counts, tau, *cache._tensors()):
+        _check(load().saga_tree_attn(ctypes.byref(shape), T, _ptr(q), ctypes.byref(c), _ptr(prefix_lens),
+                                     _ptr(counts), _ptr(tree_mask), _ptr(tau), _ptr(out),
+                                     SAGA_OUT_BF16 if out.dtype == torch.bfloat16 else SAGA_OUT_F32, _ptr(workspace),
+                                     workspace.numel(), _stream(stream)))
 
 
 def read_probe(buf: torch.Tensor, sink: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
