@@ -15,7 +15,7 @@ BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libsaga.so")
 SOURCES = ["saga_kernels.cu", "saga_api.cu", "saga_noalloc.cu", "saga_probe.cu", "saga_merge.cu", "saga_cache.cu",
            "saga_tree.cu"]
-HEADERS = ["saga_device.cuh", "saga_internal.h", "saga_serve.h", "saga_launch.cuh"]
+HEADERS = ["saga_device.cuh", "saga_internal.h", "saga_serve.h", "saga_launch.cuh", "saga_tree.h"]
 
 NVCC_FLAGS = [
     "-O3", "-std=c++17", "-gencode", "arch=compute_100a,code=sm_100a", "-lineinfo",

@@ -3,10 +3,12 @@
 // store and load, and attention of drafted tokens.  Not part of the public ABI.
 #pragma once
 
+#include <cuda.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
 
 #include "saga.h"
+#include "saga_tree.h"
 
 namespace saga {
 
@@ -17,6 +19,9 @@ int api_ok();
 int api_cuda_fail(cudaError_t e, const char* what);
 int api_validate_shape(const saga_shape* s);
 int api_device_sms(int* sms);
+// Tensor map over `rows` rows of d bf16 elements: boxes of 64 columns (one
+// 128-byte swizzle row) by kTreeTile rows.
+int api_rows_map(CUtensorMap* m, const void* base, long long rows, int d);
 
 // A quantised row: value = code * scale with scale = amax / kE4m3Max over the
 // row's d elements.  Rows whose largest magnitude is below kAmaxFloor use it
@@ -80,6 +85,12 @@ struct TreeParams {
   float scale;  // fp32(1 / sqrt(d))
   int out_bf16;
   int batch, tokens, h_q, h_k, h_v, l_cap;
+  TreePlan plan;
+  TreeSmem smem;
+  int ctas;        // of the attention kernel
+  float* part_o;   // [slots, cols, d]: sums of weights times values
+  float* part_m;   // [slots, cols]: the power of two that the weights are relative to
+  float* part_l;   // [slots, cols]: sums of weights
 };
 
 int api_check_cache(const saga_shape* s, const saga_cache* c);

@@ -1,0 +1,227 @@
+// saga_tree.h - how attention of drafted tokens is laid out over columns,
+// tiles and CTAs.  Host and device; not part of the public ABI.
+#pragma once
+
+#include <stddef.h>
+#include <stdint.h>
+
+namespace saga {
+
+constexpr int kTreeTile = 128;     // cache rows per tile (the M of the score product)
+constexpr int kTreeMaxCols = 128;  // query columns of one CTA's products
+constexpr int kTreeMaxStages = 12;
+
+// The query rows of one (batch row, key head) are its G = h_q / h_k heads by T
+// tokens, one column of the products each.  Columns that share a value head
+// are neighbours and padded to the product's column unit; a chunk is as many
+// value heads as fit 128 columns, or a part of one value head's columns.
+// Column r of a value head is head r / T, token r % T.
+struct TreePlan {
+  int nvh;     // value heads of a key head's group (1 where several key heads share a value head)
+  int hpv;     // query heads of the group per value head
+  int rows;    // hpv * T columns of a value head, before padding
+  int nv;      // value heads per chunk (the last chunk of a group may have fewer)
+  int rsplit;  // chunks that one value head is cut into (nv == 1), else 1
+  int rpc;     // columns of a value head per chunk, before padding
+  int nvp;     // the same, padded
+  int chunks;  // chunks per key head
+  int cols;    // columns of a chunk: nv * nvp, padded to 16
+  int groups;  // 8-column groups with a live column, per chunk
+};
+
+__host__ __device__ inline TreePlan tree_plan(int h_q, int h_k, int h_v, int d, int T) {
+  TreePlan p;
+  const int G = h_q / h_k, per_v = h_q / h_v;
+  p.hpv = per_v < G ? per_v : G;
+  p.nvh = G / p.hpv;
+  p.rows = p.hpv * T;
+  const int unit = d == 64 ? 8 : 16;  // columns of the value product: M = 64 takes 8, M = 128 takes 16
+  const int padded = (p.rows + unit - 1) / unit * unit;
+  if (padded <= kTreeMaxCols) {
+    const int per = kTreeMaxCols / padded;
+    p.chunks = (p.nvh + per - 1) / per;
+    p.nv = (p.nvh + p.chunks - 1) / p.chunks;
+    p.chunks = (p.nvh + p.nv - 1) / p.nv;
+    p.rsplit = 1;
+    p.rpc = p.rows;
+    p.nvp = padded;
+  } else {
+    p.rsplit = (p.rows + kTreeMaxCols - 1) / kTreeMaxCols;
+    p.rpc = (p.rows + p.rsplit - 1) / p.rsplit;
+    p.rsplit = (p.rows + p.rpc - 1) / p.rpc;
+    p.nvp = (p.rpc + unit - 1) / unit * unit;
+    p.nv = 1;
+    p.chunks = p.nvh * p.rsplit;
+  }
+  p.cols = (p.nv * p.nvp + 15) / 16 * 16;
+  p.groups = p.nv * ((p.rpc + 7) / 8);
+  return p;
+}
+
+// The work is a line of tiles: batch rows in order, in each its `items`
+// (key head, chunk) items in order, in each its tiles.  CTA i of `ctas` takes
+// tiles [i W / ctas, (i + 1) W / ctas) of the W; an item that several CTAs
+// share is joined from their partials.  No more CTAs work than there are
+// tiles, so each of them has one at least.  CTA i's partial of item k lies in
+// slot i + k: along the line one of the two grows from one partial to the
+// next, so no two share a slot.
+struct TreeLine {
+  const int* prefix;
+  const int* counts;  // nullable
+  int tokens, l_cap;
+  int items;  // of each batch row
+};
+
+// The prefix and the tokens of batch row b; false if the prefix was clamped.
+__host__ __device__ inline bool tree_lens(const TreeLine& l, int b, int* P, int* n) {
+  int c = l.counts != nullptr ? l.counts[b] : l.tokens;
+  c = c < 0 ? 0 : c > l.tokens ? l.tokens : c;
+  const int given = l.prefix[b];
+  *n = c;
+  *P = given < 0 ? 0 : given > l.l_cap - c ? l.l_cap - c : given;
+  return *P == given;
+}
+__host__ __device__ inline int tree_tiles(int prefix, int n) { return n > 0 ? (prefix + n + kTreeTile - 1) / kTreeTile : 0; }
+__host__ __device__ inline int tree_ctas(long long total, int most) { return total < most ? (int)total : most; }
+__host__ __device__ inline long long tree_first_tile(long long total, int ctas, int i) { return (long long)i * total / ctas; }
+// The CTA that tile x of the line belongs to.
+__host__ __device__ inline int tree_cta_of(long long total, int ctas, long long x) { return (int)(((x + 1) * ctas - 1) / total); }
+
+// One segment of a CTA's share of the line: tiles [t0, t1) of item `hc` of
+// batch row b.
+struct TreeWalk {
+  int b, hc, t0, t1, tiles, P, n;
+  long long left;  // tiles of the share from t0 on
+  int item;
+};
+
+// share: the batch row of the first tile, that tile's place among the batch
+// row's, the tiles of the share.
+__host__ __device__ inline bool tree_walk_begin(const TreeLine& l, const long long* share, TreeWalk& w) {
+  w.left = share[2];
+  if (w.left == 0) return false;
+  w.b = (int)share[0];
+  tree_lens(l, w.b, &w.P, &w.n);
+  w.tiles = tree_tiles(w.P, w.n);
+  w.hc = (int)(share[1] / w.tiles);
+  w.t0 = (int)(share[1] - (long long)w.hc * w.tiles);
+  w.t1 = w.tiles - w.t0 < w.left ? w.tiles : w.t0 + (int)w.left;
+  w.item = w.b * l.items + w.hc;
+  return true;
+}
+
+__host__ __device__ inline bool tree_walk_next(const TreeLine& l, TreeWalk& w) {
+  w.left -= w.t1 - w.t0;
+  if (w.left == 0) return false;
+  w.t0 = 0;
+  if (++w.hc == l.items) {
+    w.hc = 0;
+    do {  // ends: tiles of the share are left, so a later batch row has some
+      ++w.b;
+      tree_lens(l, w.b, &w.P, &w.n);
+      w.tiles = tree_tiles(w.P, w.n);
+    } while (w.tiles == 0);
+  }
+  w.t1 = w.tiles < w.left ? w.tiles : (int)w.left;
+  w.item = w.b * l.items + w.hc;
+  return true;
+}
+
+// The order of a segment's loads: K(t0), then for every t: K(t + 1) if there
+// is one, V(t, 0), V(t, 1), ...  v = -1 stands for the keys.
+struct TreeFeed {
+  int t, v;
+};
+__host__ __device__ inline TreeFeed tree_feed(const TreeWalk& w) { return TreeFeed{w.t0, -1}; }
+__host__ __device__ inline bool tree_feed_next(const TreeWalk& w, int nv, TreeFeed& f) {
+  if (f.v < 0) {
+    if (f.t == w.t0 && f.t + 1 < w.t1) {
+      ++f.t;
+    } else {
+      if (f.t > w.t0) --f.t;
+      f.v = 0;
+    }
+    return true;
+  }
+  if (++f.v < nv) return true;
+  if (f.t + 2 < w.t1) {
+    f.t += 2;
+    f.v = -1;
+    return true;
+  }
+  if (f.t + 1 < w.t1) {
+    ++f.t;
+    f.v = 0;
+    return true;
+  }
+  return false;
+}
+// Where V(t0 + i, 0) stands in that order.
+__host__ __device__ inline int tree_value_place(int i, int tiles, int nv) { return 1 + i * nv + (i + 1 < tiles ? i + 1 : tiles - 1); }
+
+// Where a query row (head jj of its key head's group, token t) sits.
+struct TreeSpot {
+  int chunk, col;
+};
+__host__ __device__ inline TreeSpot tree_spot(const TreePlan& p, int T, int jj, int t) {
+  const int v = jj / p.hpv, r = (jj - v * p.hpv) * T + t;
+  TreeSpot s;
+  if (p.rsplit == 1) {
+    s.chunk = v / p.nv;
+    s.col = (v - s.chunk * p.nv) * p.nvp + r;
+  } else {
+    s.chunk = v * p.rsplit + r / p.rpc;
+    s.col = r % p.rpc;
+  }
+  return s;
+}
+
+// The query row of a chunk's column: false for padding.
+__host__ __device__ inline bool tree_row(const TreePlan& p, int T, int chunk, int col, int* jj, int* t) {
+  const int vl = col / p.nvp, c = col - vl * p.nvp;
+  int v, r;
+  if (p.rsplit == 1) {
+    v = chunk * p.nv + vl;
+    r = c;
+  } else {
+    v = chunk / p.rsplit;
+    r = (chunk - v * p.rsplit) * p.rpc + c;
+  }
+  if (vl >= p.nv || v >= p.nvh || c >= p.rpc || r >= p.rows) return false;
+  *jj = v * p.hpv + r / T;
+  *t = r - r / T * T;
+  return true;
+}
+
+// Shared memory of the kernel: the tile ring, Q, two P buffers, per-column
+// words, the scales of two tiles (8-bit caches), barriers.
+struct TreeSmem {
+  int stages, stage_bytes;
+  int q, p, p_bytes, m, tau, cs, f, mask, scales, bars, total;
+};
+__host__ __device__ inline TreeSmem tree_smem(const TreePlan& p, int d, bool e4m3) {
+  TreeSmem s;
+  s.stage_bytes = kTreeTile * d * 2;
+  const int budget = 227 * 1024 - 1024;  // less the slack that aligns the base to 1024 bytes
+  const int q_bytes = p.cols * d * 2;
+  s.p_bytes = p.cols * kTreeTile * 2;
+  const int words = p.cols * (4 + 4 + 4 + 4 + 8);
+  const int scale_bytes = e4m3 ? 2 * 2 * (1 + p.nv) * kTreeTile * 4 : 0;
+  const int bar_bytes = 8 * (3 * kTreeMaxStages + 16) + 64;
+  const int fixed = q_bytes + 2 * s.p_bytes + words + scale_bytes + bar_bytes;
+  s.stages = (budget - fixed) / s.stage_bytes;
+  if (s.stages > kTreeMaxStages) s.stages = kTreeMaxStages;
+  s.q = s.stages * s.stage_bytes;
+  s.p = s.q + q_bytes;
+  s.mask = s.p + 2 * s.p_bytes;
+  s.m = s.mask + p.cols * 8;
+  s.tau = s.m + p.cols * 4;
+  s.cs = s.tau + p.cols * 4;
+  s.f = s.cs + p.cols * 4;
+  s.scales = s.f + p.cols * 4;
+  s.bars = s.scales + scale_bytes;
+  s.total = s.bars + bar_bytes + 1024;
+  return s;
+}
+
+}  // namespace saga

@@ -1,0 +1,148 @@
+"""Host-side index logic of the drafted-token attention, compiled with g++ and run on the CPU: every query row has
+one column of one chunk and back, columns and shared memory stay within their limits, the CTAs' shares cover every
+tile of every item once and in order, partials never share a slot and are all written, and the loads of a segment come
+in the order in which the products take them."""
+import os
+import shutil
+import subprocess
+
+import pytest
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+CSRC = os.path.join(ROOT, "long_context_decoding_saga_b200", "csrc")
+
+PROGRAM = r"""
+#define __host__
+#define __device__
+#include <cstdio>
+#include <cstdlib>
+#include <map>
+#include <set>
+#include <vector>
+#include "saga_tree.h"
+using namespace saga;
+
+static int fails = 0;
+#define CHECK(c, ...) do { if (!(c)) { ++fails; if (fails < 20) { std::printf(__VA_ARGS__); std::printf("\n"); } } } while (0)
+
+static const int Ts[] = {1, 2, 3, 4, 5, 7, 8, 12, 16, 31, 32, 33, 48, 63, 64};
+static void plans() {
+  for (int h_k = 1; h_k <= 8; ++h_k) for (int h_v = 1; h_v <= 32; ++h_v) for (int d = 64; d <= 128; d += 64)
+    for (int h_q = 1; h_q <= 64; ++h_q) {
+      if (h_q % h_k || h_q % h_v || (h_v % h_k && h_k % h_v) || h_q / h_k > (d == 64 ? 64 : 32)) continue;
+      if (h_v > h_k && h_v / h_k > 32) continue;
+      for (int T : Ts) {
+        const TreePlan p = tree_plan(h_q, h_k, h_v, d, T);
+        const int G = h_q / h_k, unit = d == 64 ? 8 : 16;
+        CHECK(p.cols <= kTreeMaxCols && p.cols % 16 == 0 && p.nvp % unit == 0 && p.nv * p.nvp <= p.cols, "cols");
+        CHECK(p.groups <= 16 && p.groups >= 1, "groups");
+        CHECK(p.hpv * p.nvh == G, "heads");
+        std::map<std::pair<int, int>, int> seen;
+        for (int jj = 0; jj < G; ++jj) for (int t = 0; t < T; ++t) {
+          const TreeSpot s = tree_spot(p, T, jj, t);
+          CHECK(s.chunk >= 0 && s.chunk < p.chunks && s.col >= 0 && s.col < p.nv * p.nvp, "spot of %d %d", jj, t);
+          const int uses = ++seen[std::make_pair(s.chunk, s.col)];
+          CHECK(uses == 1, "two rows in one column");
+          int j2 = -1, t2 = -1;
+          CHECK(tree_row(p, T, s.chunk, s.col, &j2, &t2) && j2 == jj && t2 == t, "row of column");
+          // its value head is the one whose columns these are
+          const int kh = 0, j = kh * G + jj;
+          const int vl = s.col / p.nvp, v0 = p.rsplit == 1 ? s.chunk * p.nv : s.chunk / p.rsplit;
+          CHECK((kh * G + (v0 + vl) * p.hpv) / (h_q / h_v) == j / (h_q / h_v), "value head");
+        }
+        int live = 0;
+        for (int c = 0; c < p.chunks; ++c) for (int col = 0; col < p.cols; ++col) {
+          int a, b;
+          live += tree_row(p, T, c, col, &a, &b);
+        }
+        CHECK(live == G * T, "live columns %d of %d", live, G * T);
+        for (int e = 0; e < 2; ++e) {
+          const TreeSmem s = tree_smem(p, d, e);
+          CHECK(s.stages >= 3 && s.stages <= kTreeMaxStages && s.total <= 227 * 1024, "smem %d stages %d", s.total, s.stages);
+          CHECK(s.q % 1024 == 0 && s.p % 1024 == 0 && s.m % 16 == 0 && s.f % 16 == 0 && s.bars % 8 == 0, "smem alignment");
+        }
+      }
+    }
+}
+
+static void lines() {
+  std::srand(1);
+  for (int round = 0; round < 3000; ++round) {
+    const int B = 1 + std::rand() % 40, items = 1 + std::rand() % 9, T = 1 + std::rand() % 64, cap = 64 + std::rand() % 3000;
+    const int most = (round % 3 == 0) ? 148 : 1 + std::rand() % 20, nv = 1 + std::rand() % 5;
+    std::vector<int> prefix(B), counts(B);
+    for (int b = 0; b < B; ++b) {
+      prefix[b] = std::rand() % 5 == 0 ? 0 : std::rand() % (cap + 50) - 20;
+      counts[b] = std::rand() % 4 == 0 ? 0 : std::rand() % (T + 3) - 1;
+    }
+    const TreeLine line{prefix.data(), round % 2 ? counts.data() : nullptr, T, cap, items};
+    long long total = 0;
+    std::vector<long long> before(B);
+    for (int b = 0; b < B; ++b) {
+      int P, n;
+      tree_lens(line, b, &P, &n);
+      CHECK(P >= 0 && n >= 0 && P + n <= cap, "lens");
+      before[b] = total;
+      total += (long long)items * tree_tiles(P, n);
+    }
+    const int ctas = tree_ctas(total, most);
+    long long x = 0;
+    std::set<long long> slots;
+    std::map<int, std::pair<int, int>> held;  // item -> first and last CTA
+    for (int i = 0; i < ctas; ++i) {
+      const long long first = tree_first_tile(total, ctas, i), count = tree_first_tile(total, ctas, i + 1) - first;
+      CHECK(first == x && count >= 1, "share of CTA %d", i);
+      int b = 0;
+      while (b + 1 < B && before[b + 1] <= first) ++b;
+      { int P, n; tree_lens(line, b, &P, &n); while (tree_tiles(P, n) == 0) { --b; tree_lens(line, b, &P, &n); } }
+      const long long share[3] = {b, first - before[b], count};
+      TreeWalk w;
+      bool more = tree_walk_begin(line, share, w);
+      while (more) {
+        CHECK(w.t0 < w.t1 && w.t1 <= w.tiles && w.hc < items, "segment");
+        CHECK(w.item == w.b * items + w.hc, "item");
+        CHECK(slots.insert((long long)i + w.item).second, "slot used twice");
+        CHECK(i + w.item < ctas + (long long)B * items, "slot out of range");
+        if (!held.count(w.item)) held[w.item] = {i, i};
+        CHECK(held[w.item].second >= i - 1, "a CTA between has no partial");
+        held[w.item].second = i;
+        for (int t = w.t0; t < w.t1; ++t, ++x) {
+          CHECK(x == before[w.b] + (long long)w.hc * w.tiles + t, "tile order");
+          CHECK(tree_cta_of(total, ctas, x) == i, "CTA of tile");
+        }
+        // the feed: K(t0), then K(t + 1), V(t, ...)
+        std::vector<std::pair<int, int>> want, got;
+        want.push_back({w.t0, -1});
+        for (int t = w.t0; t < w.t1; ++t) {
+          if (t + 1 < w.t1) want.push_back({t + 1, -1});
+          CHECK((int)want.size() == tree_value_place(t - w.t0, w.t1 - w.t0, nv), "place of the values");
+          for (int v = 0; v < nv; ++v) want.push_back({t, v});
+        }
+        TreeFeed f = tree_feed(w);
+        do got.push_back({f.t, f.v}); while (tree_feed_next(w, nv, f));
+        CHECK(got == want, "feed order");
+        more = tree_walk_next(line, w);
+      }
+    }
+    CHECK(x == total, "tiles covered %lld of %lld", x, total);
+  }
+}
+
+int main() {
+  plans();
+  lines();
+  std::printf(fails ? "%d failures\n" : "ok\n", fails);
+  return fails != 0;
+}
+"""
+
+
+def test_plan_shares_and_feed(tmp_path):
+    if shutil.which("g++") is None:
+        pytest.skip("no g++")
+    src = tmp_path / "t.cpp"
+    src.write_text(PROGRAM)
+    exe = tmp_path / "t"
+    subprocess.run(["g++", "-O1", "-std=c++17", "-I" + CSRC, str(src), "-o", str(exe)], check=True)
+    r = subprocess.run([str(exe)], capture_output=True, text=True)
+    assert r.returncode == 0, r.stdout
