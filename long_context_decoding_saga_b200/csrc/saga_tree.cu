@@ -13,18 +13,19 @@
 // transposed operand, so nothing is transposed.
 //
 // P = 2^(x - m) with x the score in powers of two and m a reference per column.
-// The softmax needs no exact maximum: any m within the range of the 16-bit
-// weights gives the same quotient.  So m is taken from the first tile's maximum
-// and moved only when a score rises above what the weights can hold, which one
-// comparison per score and one vote per tile watch for; then sums and
-// accumulators are rescaled and the tile is done again.  Sums of weights are
-// kept per thread and column in registers and added across rows once at the
-// end of a segment.
+// The softmax needs no exact maximum: any m within the range of bf16's exponent
+// gives the same quotient.  So m is taken from the first tile's maximum and
+// moved only when a score rises 2^32 above it, which one comparison per score
+// and one vote per tile watch for; then the accumulators are rescaled and the
+// tile is done again.  The weights are rounded to bf16, and what they are
+// divided by is the sum of the rounded weights: a row of ones beside V in the
+// second product adds them up in fp32.
 //
-// 8-bit caches: the codes are widened to half precision (exactly) on their way
-// into the same tile ring; a key row's scale multiplies its scores and a value
-// row's scale its weights, in fp32, before the rounding of P.  q goes to half
-// precision scaled by a power of two, exact for all that matters of bf16.
+// 8-bit caches: codes are widened on their way into the same tile ring.  Keys
+// become half precision, exactly, and a key row's scale multiplies its scores
+// in fp32 (q goes to half precision scaled by a power of two, exact for all
+// that matters of bf16).  Values are multiplied by their row's scale in fp32
+// and rounded to bf16, which is finer than their own 4 bits.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>
@@ -41,12 +42,12 @@ namespace {
 
 constexpr float kUnset = -1e37f;      // a column's reference before any kept score
 constexpr float kLog2e = 1.4426950408889634f;
-constexpr float kMinScale = 8.271806125530277e-25f;  // 2^-80: value scales below it do not lower the reference
-constexpr int kEpiWarp0 = 4, kConvWarp0 = 12;
+constexpr float kOver = 32.f;         // a score this far (in powers of two) above its reference moves the reference
+constexpr int kEpiWarp0 = 4, kConvWarp0 = 12, kConvWarps = 8;
 constexpr int kEpiAll = 256;
 
 template <bool E4M3>
-constexpr int kTreeThreads = E4M3 ? 512 : 384;
+constexpr int kTreeThreads = E4M3 ? (kConvWarp0 + kConvWarps) * 32 : kConvWarp0 * 32;
 
 // ------------------------------------------------------------------ the line of tiles
 __device__ __forceinline__ TreeLine line_of(const TreeParams& p) {
@@ -55,22 +56,19 @@ __device__ __forceinline__ TreeLine line_of(const TreeParams& p) {
 
 // Heads of a segment.
 struct Heads {
-  int kh, chunk, v0, nv;  // first value head of the group, value heads here
+  int kh, chunk, nv;  // key head, chunk, value heads here
+  size_t key, value;  // cache row 0 of the key head and of the first value head (the others follow, l_cap rows apart)
 };
 __device__ __forceinline__ Heads heads_of(const TreeParams& p, const TreeWalk& w) {
   Heads h;
   h.kh = w.hc / p.plan.chunks;
   h.chunk = w.hc - h.kh * p.plan.chunks;
-  h.v0 = p.plan.rsplit == 1 ? h.chunk * p.plan.nv : h.chunk / p.plan.rsplit;
-  h.nv = p.plan.rsplit == 1 ? min(p.plan.nv, p.plan.nvh - h.v0) : 1;
+  const int v0 = p.plan.rsplit == 1 ? h.chunk * p.plan.nv : h.chunk / p.plan.rsplit;  // of the group
+  h.nv = p.plan.rsplit == 1 ? min(p.plan.nv, p.plan.nvh - v0) : 1;
+  h.key = ((size_t)w.b * p.h_k + h.kh) * p.l_cap;
+  const int vh = p.h_v > p.h_k ? h.kh * p.plan.nvh + v0 : h.kh * p.h_v / p.h_k;
+  h.value = ((size_t)w.b * p.h_v + vh) * p.l_cap;
   return h;
-}
-__device__ __forceinline__ size_t key_row(const TreeParams& p, const TreeWalk& w, const Heads& h) {
-  return ((size_t)w.b * p.h_k + h.kh) * p.l_cap;
-}
-__device__ __forceinline__ size_t value_row(const TreeParams& p, const TreeWalk& w, const Heads& h, int v) {
-  const int j = h.kh * (p.h_q / p.h_k) + (h.v0 + v) * p.plan.hpv;  // the value head's first query head
-  return ((size_t)w.b * p.h_v + j / (p.h_q / p.h_v)) * p.l_cap;
 }
 
 // Drafted tokens that any present token sees (the whole warp calls).
@@ -90,7 +88,8 @@ __device__ __forceinline__ bool row_seen(const TreeWalk& w, unsigned long long s
 
 // ------------------------------------------------------------------ tcgen05 pieces beyond saga_device.cuh
 // Matrix descriptors.  V tile: 128-byte swizzle, the product's M (d) dense:
-// 64-element blocks `block` bytes apart, 8-row groups 1024 bytes apart.
+// 64-element blocks `block` bytes apart, 8-row groups 1024 bytes apart.  For
+// d = 64 the second block of the M = 128 product is the ones.
 __device__ __forceinline__ uint64_t desc_v(uint32_t addr, uint32_t block) {
   return (uint64_t)((addr >> 4) & 0x3FFFu) | ((uint64_t)(block >> 4) << 16) | ((uint64_t)(1024u >> 4) << 32) |
          ((uint64_t)1u << 46) | ((uint64_t)2u << 61);
@@ -107,16 +106,22 @@ __host__ __device__ constexpr uint32_t idesc16(bool half, int M, int N, bool tra
          ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
 }
 
-__device__ __forceinline__ void tmem_ld8(uint32_t taddr, float* v) {
-  uint32_t r[8];
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];\n\t"
-      "tcgen05.wait::ld.sync.aligned;"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
-      : "r"(taddr)
-      : "memory");
+// 8 columns of this thread's lane: the load, and the wait after which they may be read.
+__device__ __forceinline__ void tmem_ld8_start(uint32_t taddr, uint32_t* r) {
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+               : "r"(taddr));
+}
+__device__ __forceinline__ void tmem_ld8_end(uint32_t* r, float* v) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]));
 #pragma unroll
   for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(r[i]);
+}
+__device__ __forceinline__ void tmem_ld8(uint32_t taddr, float* v) {
+  uint32_t r[8];
+  tmem_ld8_start(taddr, r);
+  tmem_ld8_end(r, v);
 }
 __device__ __forceinline__ void tmem_st8(uint32_t taddr, const float* v) {
   asm volatile(
@@ -127,26 +132,28 @@ __device__ __forceinline__ void tmem_st8(uint32_t taddr, const float* v) {
       : "memory");
 }
 
+// One lane of a converged warp.  Code under it issues tensor-core and copy
+// instructions from uniform registers: under a test of the lane number each
+// product took about 150 clocks to issue, under this about 40.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile("{\n\t.reg .pred P;\n\telect.sync _|P, 0xffffffff;\n\tselp.u32 %0, 1, 0, P;\n\t}" : "=r"(p));
+  return p != 0;
+}
+
 __device__ __forceinline__ float ex2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
 
-template <bool E4M3>
-__device__ __forceinline__ uint32_t pack2(float a, float b) {
-  if (E4M3) {
-    const __half2 h = __floats2half2_rn(a, b);
-    return reinterpret_cast<const uint32_t&>(h);
-  }
-  const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+__device__ __forceinline__ uint32_t pack_half(float a, float b) {
+  const __half2 h = __floats2half2_rn(a, b);
   return reinterpret_cast<const uint32_t&>(h);
 }
-
-__device__ __forceinline__ void cp_async4_zfill(void* smem_dst, const void* gsrc, bool valid) {
-  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(smem_u32(smem_dst)),
-               "l"(reinterpret_cast<uint64_t>(gsrc)), "r"(valid ? 4 : 0)
-               : "memory");
+__device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
+  const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+  return reinterpret_cast<const uint32_t&>(h);
 }
 
 // A position in the tile ring.
@@ -173,119 +180,104 @@ struct Bars {
   uint64_t *q_full, *drain;
 };
 
-template <int M>
-struct Mode {
-  static constexpr int value = M;
-};
-
-// The epilogue's view of one tile.
-template <int D, bool E4M3>
-struct Tile {
-  uint32_t s_tmem;      // scores of this warp's lanes
-  uint8_t* p_buf;       // the P buffer
-  uint8_t* p_row;       // this thread's 16 bytes of column group 0 in it
-  const float* sc;      // 8-bit: this row's scales, [0] key, [1 + v - v_first] value (stride kTreeTile)
-  bool all;             // every column sees the row
-  unsigned long long bit;  // else the drafted token of the row (0: none)
-  float scale;
-};
-
-enum { kAccumulate, kUndo, kMax };
-
 // Words for exchanging a column group's values between the four warps of its
 // warpgroup: the group's part of a P buffer while that holds no weights.
 __device__ __forceinline__ float* column_words(uint8_t* p_buf, int col) {
   return reinterpret_cast<float*>(p_buf + (col >> 3) * 2048);
 }
 
-// One pass over this warpgroup's columns of a tile.  kAccumulate: weights into
-// P and the sums, true if a score is above what its column's reference allows.
-// kUndo: takes the same weights out of the sums again.  kMax: the columns'
-// maxima over the warp's rows into column_words.
-template <int D, bool E4M3, int MAXG, bool MASKED, int MODE>
-__device__ __forceinline__ bool tile_pass(const TreeParams& p, const Tile<D, E4M3>& t, int g0, int ng, int gpv,
-                                          const float* m, const float* tau, const float* cs,
-                                          const unsigned long long* mask, float* l) {
-  bool over = false;
-  const float ks = E4M3 ? t.sc[0] : t.scale;
-  const int v_first = E4M3 ? g0 / gpv : 0;
-#pragma unroll
-  for (int g = 0; g < MAXG; ++g) {
-    if (g < ng) {
-      const int vl = (g0 + g) / gpv, col = vl * p.plan.nvp + (g0 + g - vl * gpv) * 8;
-      float s[8];
-      tmem_ld8(t.s_tmem + col, s);
-      float vs = 1.f, lv = 0.f, lim = 32.f;
-      if (E4M3) {
-        vs = t.sc[(1 + vl - v_first) * kTreeTile];
-        lv = __log2f(fmaxf(vs, kMinScale));
-        lim = 15.f - lv;
-      }
-      float e[8], mm[8];
-      *reinterpret_cast<float4*>(mm) = *reinterpret_cast<const float4*>(m + col);
-      *reinterpret_cast<float4*>(mm + 4) = *reinterpret_cast<const float4*>(m + col + 4);
-      if (!MASKED) {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const float f = (E4M3 ? ks * cs[col + i] : ks) * kLog2e;
-          e[i] = MODE == kMax ? s[i] * f : fmaf(s[i], f, -mm[i]);
-        }
-      } else {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const float a = s[i] * (E4M3 ? ks * cs[col + i] : ks);
-          const bool keep = (t.all || (mask[col + i] & t.bit) != 0ull) && a >= tau[col + i];
-          e[i] = keep ? (MODE == kMax ? a * kLog2e : fmaf(a, kLog2e, -mm[i])) : -INFINITY;
-        }
-      }
-      if (MODE == kMax) {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const uint32_t k = __reduce_max_sync(0xffffffffu, float_key(e[i] + lv));
-          if (lane_id() == 0) column_words(t.p_buf, col)[(threadIdx.x >> 5 & 3) * 8 + i] = key_float(k);
-        }
-      } else {
-        uint32_t w[4];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          over |= e[i] > lim;
-          e[i] = ex2(fminf(e[i], lim));
-          if (MODE == kAccumulate) l[g * 8 + i] += e[i];
-          else l[g * 8 + i] -= e[i];
-        }
-        if (MODE == kAccumulate) {
-#pragma unroll
-          for (int i = 0; i < 4; ++i)
-            w[i] = E4M3 ? pack2<E4M3>(e[2 * i] * vs, e[2 * i + 1] * vs) : pack2<E4M3>(e[2 * i], e[2 * i + 1]);
-          *reinterpret_cast<uint4*>(t.p_row + (col >> 3) * 2048) = make_uint4(w[0], w[1], w[2], w[3]);
-        }
-      }
+// The column groups (8 live columns or fewer, the rest padding) of a
+// warpgroup: `count` of them from `col` on, `groups` to a value head of `nvp`
+// columns, the first of them the `at`-th of its value head.
+struct Groups {
+  int col, at, count, groups, nvp;
+  __device__ __forceinline__ void step() {
+    col += 8;
+    if (++at == groups) {
+      at = 0;
+      col += nvp - groups * 8;
     }
   }
-  return over;
+};
+
+// What a thread's cache row is to the columns of a tile.
+struct Row {
+  float f;                 // score factor, without the columns'
+  bool all;                // every column sees the row
+  unsigned long long bit;  // else the drafted token in it (0: none)
+};
+
+// Scores of 8 columns in powers of two, less the columns' references with
+// RELATIVE; -inf where hidden or below the threshold.
+template <bool E4M3, bool MASKED, bool RELATIVE>
+__device__ __forceinline__ void exponents(float* s, const Row& r, int col, const float* m, const float* tau,
+                                          const float* cs, const unsigned long long* mask) {
+  float mm[8], cc[8];
+  if (RELATIVE) {
+    *reinterpret_cast<float4*>(mm) = *reinterpret_cast<const float4*>(m + col);
+    *reinterpret_cast<float4*>(mm + 4) = *reinterpret_cast<const float4*>(m + col + 4);
+  }
+  if (E4M3) {
+    *reinterpret_cast<float4*>(cc) = *reinterpret_cast<const float4*>(cs + col);
+    *reinterpret_cast<float4*>(cc + 4) = *reinterpret_cast<const float4*>(cs + col + 4);
+  }
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const float f = E4M3 ? r.f * cc[i] : r.f;
+    if (!MASKED) {
+      s[i] = RELATIVE ? fmaf(s[i], f * kLog2e, -mm[i]) : s[i] * (f * kLog2e);
+    } else {
+      const float a = s[i] * f;
+      const bool keep = (r.all || (mask[col + i] & r.bit) != 0ull) && a >= tau[col + i];
+      s[i] = keep ? (RELATIVE ? fmaf(a, kLog2e, -mm[i]) : a * kLog2e) : -INFINITY;
+    }
+  }
 }
 
-// 8 columns' sums over the 32 lanes: lane 4 c holds column
-// (bit 2 of c) * 4 + (bit 1) * 2 + bit 0 of its octet.
-__device__ __forceinline__ float octet_sum(const float* v, int lane) {
-  float a[4], b[2], c;
+// Weights of a tile into P; returns the largest exponent of the thread's.
+template <bool E4M3, bool MASKED>
+__device__ __forceinline__ float weigh(uint32_t s_tmem, uint8_t* p_row, Groups g, const Row& r, const float* m,
+                                       const float* tau, const float* cs, const unsigned long long* mask) {
+  float top = -INFINITY;
+  uint32_t raw[8];
+  if (g.count > 0) tmem_ld8_start(s_tmem + g.col, raw);
+#pragma unroll 1
+  for (int n = g.count; n > 0; --n) {
+    float s[8];
+    tmem_ld8_end(raw, s);
+    const int col = g.col;
+    g.step();
+    if (n > 1) tmem_ld8_start(s_tmem + g.col, raw);  // the next group's scores, while this one's are weighed
+    exponents<E4M3, MASKED, true>(s, r, col, m, tau, cs, mask);
+    uint32_t w[4];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const float mine = lane & 16 ? v[4 + i] : v[i], other = lane & 16 ? v[i] : v[4 + i];
-    a[i] = mine + __shfl_xor_sync(0xffffffffu, other, 16);
-  }
+    for (int i = 0; i < 8; ++i) {
+      top = fmaxf(top, s[i]);
+      s[i] = ex2(s[i]);
+    }
 #pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const float mine = lane & 8 ? a[2 + i] : a[i], other = lane & 8 ? a[i] : a[2 + i];
-    b[i] = mine + __shfl_xor_sync(0xffffffffu, other, 8);
+    for (int i = 0; i < 4; ++i) w[i] = pack_bf16(s[2 * i], s[2 * i + 1]);
+    *reinterpret_cast<uint4*>(p_row + (col >> 3) * 2048) = make_uint4(w[0], w[1], w[2], w[3]);
   }
-  {
-    const float mine = lane & 4 ? b[1] : b[0], other = lane & 4 ? b[0] : b[1];
-    c = mine + __shfl_xor_sync(0xffffffffu, other, 4);
+  return top;
+}
+
+// The columns' largest scores over the warp's rows, into the column words.
+template <bool E4M3, bool MASKED>
+__device__ __forceinline__ void maxima(uint32_t s_tmem, uint8_t* p_buf, Groups g, const Row& r, const float* m,
+                                       const float* tau, const float* cs, const unsigned long long* mask) {
+#pragma unroll 1
+  for (int n = g.count; n > 0; --n, g.step()) {
+    float s[8];
+    tmem_ld8(s_tmem + g.col, s);
+    exponents<E4M3, MASKED, false>(s, r, g.col, m, tau, cs, mask);
+    float* words = column_words(p_buf, g.col) + (threadIdx.x >> 5 & 3) * 8;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const uint32_t k = __reduce_max_sync(0xffffffffu, float_key(s[i]));
+      if (lane_id() == 0) words[i] = key_float(k);
+    }
   }
-  c += __shfl_xor_sync(0xffffffffu, c, 2);
-  c += __shfl_xor_sync(0xffffffffu, c, 1);
-  return c;
 }
 
 // ------------------------------------------------------------------ 8-bit tiles into the ring
@@ -307,88 +299,144 @@ struct Feed {
     live = tree_walk_next(line_of(p), w);
     if (live) segment(p);
   }
+  __device__ __forceinline__ size_t row(const TreeParams& p) const {  // the tile's first, of the cache array
+    return (at.v < 0 ? h.key : h.value + (size_t)at.v * p.l_cap) + (size_t)at.t * kTreeTile;
+  }
   __device__ __forceinline__ const uint8_t* base(const TreeParams& p) const {
-    return static_cast<const uint8_t*>(at.v < 0 ? p.k : p.v) +
-           ((at.v < 0 ? key_row(p, w, h) : value_row(p, w, h, at.v)) + (size_t)at.t * kTreeTile) * D;
+    return static_cast<const uint8_t*>(at.v < 0 ? p.k : p.v) + row(p) * D;
+  }
+  __device__ __forceinline__ const float* scales(const TreeParams& p) const {
+    return (at.v < 0 ? p.k_scale : p.v_scale) + row(p);
   }
   __device__ __forceinline__ int rows() const {  // rows of the tile that hold anything
     return min(kTreeTile, w.P + w.n - at.t * kTreeTile);
   }
 };
 
-// 16 codes as 16 half-precision values.
-__device__ __forceinline__ void widen16(const uint4& u, uint4* a, uint4* b) {
+__device__ __forceinline__ float2 mul2(float2 a, float b) {
+  unsigned long long x, y, z;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(x) : "f"(a.x), "f"(a.y));
+  asm("mov.b64 %0, {%1, %1};" : "=l"(y) : "f"(b));
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(z) : "l"(x), "l"(y));
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(a.x), "=f"(a.y) : "l"(z));
+  return a;
+}
+
+// 16 codes as half precision (keys: exact), or times the row's scale as bf16.
+__device__ __forceinline__ void widen16(const uint4& u, bool value, float scale, uint4* a, uint4* b) {
   const uint32_t w[4] = {u.x, u.y, u.z, u.w};
   uint32_t y[8];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const __half2_raw lo = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(w[i] & 0xffffu), __NV_E4M3);
-    const __half2_raw hi = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(w[i] >> 16), __NV_E4M3);
-    y[2 * i] = reinterpret_cast<const uint32_t&>(lo);
-    y[2 * i + 1] = reinterpret_cast<const uint32_t&>(hi);
+  for (int i = 0; i < 8; ++i) {
+    const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(w[i >> 1] >> (16 * (i & 1))), __NV_E4M3);
+    y[i] = reinterpret_cast<const uint32_t&>(h);
+  }
+  if (value) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      float2 f = __half22float2(reinterpret_cast<const __half2&>(y[i]));
+      f = mul2(f, scale);
+      y[i] = pack_bf16(f.x, f.y);
+    }
   }
   *a = make_uint4(y[0], y[1], y[2], y[3]);
   *b = make_uint4(y[4], y[5], y[6], y[7]);
 }
 
-// 128 threads: 16-byte pieces of the tile's codes, loaded one tile ahead into
-// registers, widened into the 128-byte swizzle that the products read.  Rows
-// that no token sees become zeros.  One lane asks L2 for the tiles further on.
-constexpr int kFeedAhead = 6;
+// Two groups of 128 threads take the tiles in turn: 16-byte pieces of the
+// codes are loaded into registers as soon as the group's last tile is out of
+// them, widened, and stored in the 128-byte swizzle that the products read.
+// Rows that no token sees become zeros.  Another warp asks L2 for the tiles
+// further on: `progress` tells it how many tiles the first group has done.
+constexpr int kFeedAhead = 8;
 
 template <int D>
-__device__ void widen_tiles(const TreeParams& p, const TreeWalk& w0, uint8_t* smem, const Bars& bar, volatile int* abort_flag) {
-  constexpr int CPR = D / 16;                      // pieces per row
-  constexpr int PER = kTreeTile * CPR / 128;       // pieces per thread
-  constexpr int RSTEP = 128 / CPR;                 // rows between a thread's pieces
-  const int tid = threadIdx.x - kConvWarp0 * 32, lane = threadIdx.x & 31;
-  const int c = tid % CPR, r0 = tid / CPR;
-  const TreeSmem& L = p.smem;
-  Feed<D> f, far;
+__device__ void prefetch_tiles(const TreeParams& p, const TreeWalk& w0, volatile int* progress, volatile int* abort_flag) {
+  Feed<D> f;
   f.w = w0;
   f.live = true;
   f.segment(p);
-  far = f;
-  auto ask = [&]() {
-    if (!far.live) return;
-    const int rows = far.rows();
-    if (tid == 0 && rows > 0) prefetch_l2_bulk(far.base(p), (uint32_t)rows * D);
-    far.next(p);
-  };
+  const int lane = lane_id();
+  int asked = 0;
+  while (f.live) {
+    const unsigned long long t0 = global_ns();
+    while (asked >= 2 * *progress + kFeedAhead) {  // ends: the first group goes on, or gives up and sets the flag
+      if (*abort_flag != 0 || global_ns() - t0 > kWaitLimitNs) return;
+      __nanosleep(100);
+    }
+    const int rows = f.rows();
+    if (lane == 0) prefetch_l2_bulk(f.base(p), (uint32_t)rows * D);
+    if (lane * 32 < rows) prefetch_l2_line(f.scales(p) + lane * 32);
+    f.next(p);
+    ++asked;
+  }
+}
+
+template <int D>
+__device__ void widen_tiles(const TreeParams& p, const TreeWalk& w0, uint8_t* smem, const Bars& bar,
+                            volatile int* progress, volatile int* abort_flag) {
+  constexpr int CPR = D / 16;                  // pieces per row
+  constexpr int PER = kTreeTile * CPR / 128;   // pieces per thread
+  constexpr int RSTEP = 128 / CPR;             // rows between a thread's pieces
+  const int group = (threadIdx.x - kConvWarp0 * 32) >> 7;
+  const int tid = threadIdx.x & 127, lane = threadIdx.x & 31;
+  const int c = tid % CPR, r0 = tid / CPR;
+  const TreeSmem& L = p.smem;
+  Feed<D> f;
+  f.w = w0;
+  f.live = true;
+  f.segment(p);
   uint4 x[PER];
+  float sc[PER];
   auto fetch = [&]() {
     const uint8_t* src = f.base(p) + (size_t)r0 * D + c * 16;
+    const float* scale = f.scales(p) + r0;
     const int row0 = f.at.t * kTreeTile + r0;
+    const bool value = f.at.v >= 0;
+    if ((f.at.t + 1) * kTreeTile <= f.w.P) {
 #pragma unroll
-    for (int i = 0; i < PER; ++i)
-      x[i] = row_seen(f.w, f.seen, row0 + i * RSTEP)
-                 ? __ldg(reinterpret_cast<const uint4*>(src + (size_t)i * RSTEP * D))
-                 : make_uint4(0u, 0u, 0u, 0u);
+      for (int i = 0; i < PER; ++i) {
+        x[i] = __ldg(reinterpret_cast<const uint4*>(src + (size_t)i * RSTEP * D));
+        if (value) sc[i] = __ldg(scale + i * RSTEP);
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < PER; ++i) {
+        const bool there = row_seen(f.w, f.seen, row0 + i * RSTEP);
+        x[i] = there ? __ldg(reinterpret_cast<const uint4*>(src + (size_t)i * RSTEP * D)) : make_uint4(0u, 0u, 0u, 0u);
+        sc[i] = there && value ? __ldg(scale + i * RSTEP) : 0.f;
+      }
+    }
   };
-  if (tid < 32)
-    for (int i = 0; i < kFeedAhead; ++i) ask();
-  fetch();
   Ring r;
+  if (group == 1) {
+    f.next(p);  // a share has a key tile and a value tile at least
+    r.step(L.stages);
+  }
+  fetch();
   while (true) {
-    if (tid < 32) ask();
-    bool ok = r.round == 0 || mbar_wait(&bar.empty[r.st], (r.round - 1) & 1, abort_flag);
+    const bool ok = r.round == 0 || mbar_wait(&bar.empty[r.st], (r.round - 1) & 1, abort_flag);
     if (!__all_sync(0xffffffffu, ok)) break;
     uint8_t* dst = smem + r.st * L.stage_bytes + ((c * 16) >> 6) * (kTreeTile * 128);
-    const int j = (c & 3) * 2;
+    const int j = (c & 3) * 2, flip = c >> 2;  // the two halves of a row start with different chunks: other banks
+    const bool value = f.at.v >= 0;
 #pragma unroll
     for (int i = 0; i < PER; ++i) {
       uint4 a, b;
-      widen16(x[i], &a, &b);
+      widen16(x[i], value, sc[i], &a, &b);
       const int row = r0 + i * RSTEP;
       uint8_t* at = dst + row * 128;
-      *reinterpret_cast<uint4*>(at + ((j ^ (row & 7)) << 4)) = a;
-      *reinterpret_cast<uint4*>(at + (((j + 1) ^ (row & 7)) << 4)) = b;
+      *reinterpret_cast<uint4*>(at + (((j + flip) ^ (row & 7)) << 4)) = flip ? b : a;
+      *reinterpret_cast<uint4*>(at + (((j + 1 - flip) ^ (row & 7)) << 4)) = flip ? a : b;
     }
     f.next(p);
+    if (f.live) f.next(p);
     if (f.live) fetch();
     fence_proxy_async_shared();
     __syncwarp();
     if (lane == 0) mbar_arrive(&bar.full[r.st]);
+    if (group == 0 && tid == 0) *progress = *progress + 1;
+    r.step(L.stages);
     r.step(L.stages);
     if (!f.live) break;
   }
@@ -397,11 +445,11 @@ __device__ void widen_tiles(const TreeParams& p, const TreeWalk& w0, uint8_t* sm
 // ------------------------------------------------------------------ the kernel
 // Warp 0: TMA loads of the tiles (bf16 caches).  Warp 1: the products, issued
 // by one lane.  Warps 4 .. 11: two warpgroups, each half of the column groups
-// of every tile.  Warps 12 .. 15: widening of 8-bit tiles into the ring.
+// of every tile.  Warps 12 .. 19: widening of 8-bit tiles into the ring.
 // Ring order: K of tile 0, then for each tile K of the next one and its own
 // value heads, so that the next tile's scores are there while a tile's weights
 // are computed.
-template <int D, bool E4M3, int MAXG>
+template <int D, bool E4M3>
 __global__ void __launch_bounds__(kTreeThreads<E4M3>, 1)
     saga_tree_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
                      const TreeParams p) {
@@ -418,18 +466,22 @@ __global__ void __launch_bounds__(kTreeThreads<E4M3>, 1)
   bar.pv_done = bar.p_full + 2;
   bar.q_full = bar.pv_done + 2;
   bar.drain = bar.q_full + 1;
-  long long* share = reinterpret_cast<long long*>(bar.drain + 1);
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(share + 3);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bar.drain + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  TreeWalk* share = reinterpret_cast<TreeWalk*>(tmem_slot + 2);  // left == 0: this CTA has no tiles
+  volatile int* progress = reinterpret_cast<volatile int*>(share + 1);
+  const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   const int stages = L.stages;
   const int cols = p.plan.cols;
-  const uint32_t tmem_cols = 3 * cols <= 64 ? 64u : 3 * cols <= 128 ? 128u : 3 * cols <= 256 ? 256u : 512u;
+  // two score buffers, the accumulators, and the sums of weights (d = 64: lanes 64 .. 127 of the accumulators)
+  const int used = (D == 64 ? 3 : 4) * cols;
+  const uint32_t tmem_cols = used <= 64 ? 64u : used <= 128 ? 128u : used <= 256 ? 256u : 512u;
 
   if (threadIdx.x == 0) {
     *abort_flag = 0;
+    *progress = 0;
     for (int i = 0; i < stages; ++i) {
-      mbar_init(&bar.full[i], E4M3 ? 4 : 1);
+      mbar_init(&bar.full[i], E4M3 ? kConvWarps / 2 : 1);
       mbar_init(&bar.empty[i], 1);
       mbar_init(&bar.vfix[i], 4);
     }
@@ -440,7 +492,7 @@ __global__ void __launch_bounds__(kTreeThreads<E4M3>, 1)
       mbar_init(&bar.pv_done[i], 1);
     }
     mbar_init(bar.q_full, 8);
-    mbar_init(bar.drain, 1);
+    mbar_init(bar.drain, 32);
     mbar_init_fence();
     if (!E4M3) {
       tma_prefetch_desc(&kmap);
@@ -450,6 +502,11 @@ __global__ void __launch_bounds__(kTreeThreads<E4M3>, 1)
   if (warp == 1) {
     tmem_alloc(tmem_slot, tmem_cols);
     tmem_relinquish();
+  }
+  if (warp == 2 || warp == 3) {
+    for (int i = threadIdx.x - 64; i < 2048 / 16; i += 64)
+      *reinterpret_cast<uint4*>(smem + L.ones + i * 16) = make_uint4(0x3f803f80u, 0x3f803f80u, 0x3f803f80u, 0x3f803f80u);
+    fence_proxy_async_shared();
   }
   pdl_trigger();
   pdl_wait();
@@ -472,7 +529,8 @@ __global__ void __launch_bounds__(kTreeThreads<E4M3>, 1)
     const long long first = working ? tree_first_tile(total, ctas, blockIdx.x) : 0;
     const long long count = working ? tree_first_tile(total, ctas, blockIdx.x + 1) - first : 0;
     long long base = 0;
-    if (lane == 0) share[2] = count;
+    if (lane == 0) share->left = 0;
+    __syncwarp();
     for (int b0 = 0; b0 < p.batch && count > 0; b0 += 32) {
       long long mine = 0;
       if (b0 + lane < p.batch) {
@@ -488,10 +546,7 @@ __global__ void __launch_bounds__(kTreeThreads<E4M3>, 1)
       }
       const unsigned hit = __ballot_sync(0xffffffffu, base + incl > first);
       if (hit != 0u) {
-        if (lane == __ffs(hit) - 1) {
-          share[0] = b0 + lane;
-          share[1] = first - (base + incl - mine);
-        }
+        if (lane == __ffs(hit) - 1) *share = tree_walk_begin(line, b0 + lane, first - (base + incl - mine), count);
         break;
       }
       base += __shfl_sync(0xffffffffu, incl, 31);
@@ -501,153 +556,188 @@ __global__ void __launch_bounds__(kTreeThreads<E4M3>, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
-  const uint32_t o_tmem = tmem + 2 * cols;
-  int issued = 0;  // TMA loads (warp 0, lane 0)
-  TreeWalk w;
-  const bool any = tree_walk_begin(line_of(p), share, w);
+  const uint32_t o_tmem = tmem + 2 * cols, l_tmem = tmem + 3 * cols;
+  int issued = 0;  // TMA loads (warp 0)
+  TreeWalk w = *share;
+  const bool any = w.left > 0;
 
   if (warp == 0 && !E4M3) {
-    if (lane == 0 && any) {
+    if (any) {
       Ring r;
       bool ok = true;
       auto load = [&](const CUtensorMap* map, size_t row) {
         if (!ok) return;
-        if (r.round > 0 && !mbar_wait(&bar.empty[r.st], (r.round - 1) & 1, abort_flag)) {
-          ok = false;
-          return;
-        }
-        mbar_arrive_expect_tx(&bar.full[r.st], (uint32_t)L.stage_bytes);
+        if (r.round > 0) ok = __all_sync(0xffffffffu, mbar_wait(&bar.empty[r.st], (r.round - 1) & 1, abort_flag));
+        if (!ok) return;
+        if (elect_one()) {
+          mbar_arrive_expect_tx(&bar.full[r.st], (uint32_t)L.stage_bytes);
 #pragma unroll
-        for (int h = 0; h < D / 64; ++h)
-          tma_load_2d(smem + r.st * L.stage_bytes + h * (kTreeTile * 128), map, &bar.full[r.st], h * 64, (int)row);
+          for (int h = 0; h < D / 64; ++h)
+            tma_load_2d(smem + r.st * L.stage_bytes + h * (kTreeTile * 128), map, &bar.full[r.st], h * 64, (int)row);
+        }
+        __syncwarp();
         r.step(stages);
         ++issued;
       };
       do {
         const Heads h = heads_of(p, w);
-        const size_t kr = key_row(p, w, h);
-        load(&kmap, kr + (size_t)w.t0 * kTreeTile);
+        load(&kmap, h.key + (size_t)w.t0 * kTreeTile);
         for (int t = w.t0; t < w.t1; ++t) {
-          if (t + 1 < w.t1) load(&kmap, kr + (size_t)(t + 1) * kTreeTile);
-          for (int v = 0; v < h.nv; ++v) load(&vmap, value_row(p, w, h, v) + (size_t)t * kTreeTile);
+          if (t + 1 < w.t1) load(&kmap, h.key + (size_t)(t + 1) * kTreeTile);
+          for (int v = 0; v < h.nv; ++v) load(&vmap, h.value + (size_t)v * p.l_cap + (size_t)t * kTreeTile);
         }
       } while (ok && tree_walk_next(line_of(p), w));
     }
-    __syncwarp();
   } else if (warp == 1) {
-    if (lane == 0 && any) {
+    if (any) {
       const uint32_t idesc_s = idesc16(E4M3, kTreeTile, cols, false);
-      const uint32_t idesc_o = idesc16(E4M3, D, p.plan.nvp, true);
-      const uint32_t q0 = smem_u32(smem + L.q);
+      const uint32_t idesc_o = idesc16(false, 128, p.plan.nvp, true), idesc_l = idesc16(false, 64, cols, true);
+      const uint32_t ones = smem_u32(smem + L.ones), ring0 = smem_u32(smem);
+      const uint64_t q_desc = umma_sdesc_sw128(smem_u32(smem + L.q));
+      const uint64_t l_desc = desc_v(ones, 0);
       Ring r;
       uint32_t fixed = 0;  // parity of each stage's vfix barrier
       int gs = 0, gp = 0, seg = 0;  // score products, value products, segments so far
       bool ok = true;
+      auto wait = [&](uint64_t* b, uint32_t parity) { return __all_sync(0xffffffffu, mbar_wait(b, parity, abort_flag)); };
       auto scores = [&]() {
-        if (!mbar_wait(&bar.full[r.st], r.round & 1, abort_flag)) return false;
-        if (gs >= 2 && !mbar_wait(&bar.s_empty[gs & 1], ((gs >> 1) - 1) & 1, abort_flag)) return false;
+        if (!wait(&bar.full[r.st], r.round & 1)) return false;
+        if (gs >= 2 && !wait(&bar.s_empty[gs & 1], ((gs >> 1) - 1) & 1)) return false;
         tc_fence_after();
-        const uint32_t a0 = smem_u32(smem + r.st * L.stage_bytes);
+        const uint64_t k_desc = umma_sdesc_sw128(ring0 + r.st * L.stage_bytes);
+        const uint32_t d = tmem + (gs & 1) * cols;
+        if (elect_one()) {
 #pragma unroll
-        for (int k = 0; k < D / 16; ++k) {
-          // 64-column halves: K of the tile 16 KB apart, Q cols * 128 bytes
-          const uint32_t a = a0 + (k >> 2) * (kTreeTile * 128) + (k & 3) * 32;
-          const uint32_t b = q0 + (k >> 2) * (cols * 128) + (k & 3) * 32;
-          umma_bf16(tmem + (gs & 1) * cols, umma_sdesc_sw128(a), umma_sdesc_sw128(b), idesc_s, k > 0);
+          for (int k = 0; k < D / 16; ++k)  // 64-column halves: K of the tile 16 KB apart, Q cols * 128 bytes
+            umma_bf16(d, k_desc + (k >> 2) * (kTreeTile * 128 / 16) + (k & 3) * 2,
+                      q_desc + (k >> 2) * (cols * 8) + (k & 3) * 2, idesc_s, k > 0);
+          umma_commit(&bar.empty[r.st]);
+          umma_commit(&bar.s_full[gs & 1]);
         }
-        umma_commit(&bar.empty[r.st]);
-        umma_commit(&bar.s_full[gs & 1]);
+        __syncwarp();
         r.step(stages);
         ++gs;
         return true;
       };
       do {
         const Heads h = heads_of(p, w);
-        ok = mbar_wait(bar.q_full, seg & 1, abort_flag);
+        ok = wait(bar.q_full, seg & 1);
         ++seg;
         tc_fence_after();
         ok = ok && scores();
         for (int t = w.t0; ok && t < w.t1; ++t) {
           if (t + 1 < w.t1) ok = scores();
-          if (!ok || !mbar_wait(&bar.p_full[gp & 1], (gp >> 1) & 1, abort_flag)) {
-            ok = false;
-            break;
-          }
-          const uint32_t b0 = smem_u32(smem + L.p + (gp & 1) * L.p_bytes);
+          ok = ok && wait(&bar.p_full[gp & 1], (gp >> 1) & 1);
+          const uint64_t p_desc = desc_p(smem_u32(smem + L.p + (gp & 1) * L.p_bytes));
           const bool fix = !E4M3 && (t + 1) * kTreeTile > w.P;
+          const uint32_t first = t > w.t0 ? 1u : 0u;
           for (int v = 0; ok && v < h.nv; ++v) {
-            ok = mbar_wait(&bar.full[r.st], r.round & 1, abort_flag);
+            ok = wait(&bar.full[r.st], r.round & 1);
             if (ok && fix) {
-              ok = mbar_wait(&bar.vfix[r.st], fixed >> r.st & 1, abort_flag);
+              ok = wait(&bar.vfix[r.st], fixed >> r.st & 1);
               fixed ^= 1u << r.st;
             }
             if (!ok) break;
             tc_fence_after();
-            const uint32_t a0 = smem_u32(smem + r.st * L.stage_bytes);
+            const uint32_t a0 = ring0 + r.st * L.stage_bytes, d = o_tmem + v * p.plan.nvp;
+            // d = 64: the block of ones stays where it is while the tile's rows go by
+            const uint64_t a = desc_v(a0, D == 64 ? ones - a0 : kTreeTile * 128);
+            const uint64_t b = p_desc + v * (p.plan.nvp * 16);
+            constexpr uint64_t kStep = D == 64 ? 128ull - (128ull << 16) : 128ull;
+            if (elect_one()) {
 #pragma unroll
-            for (int k = 0; k < kTreeTile / 16; ++k)
-              umma_bf16(o_tmem + v * p.plan.nvp, desc_v(a0 + k * 2048, kTreeTile * 128),
-                        desc_p(b0 + v * (p.plan.nvp >> 3) * 2048 + k * 256), idesc_o, (t > w.t0 || k > 0) ? 1u : 0u);
-            umma_commit(&bar.empty[r.st]);
+              for (int k = 0; k < kTreeTile / 16; ++k)
+                umma_bf16(d, a + k * kStep, b + k * 16, idesc_o, k > 0 ? 1u : first);
+              umma_commit(&bar.empty[r.st]);
+            }
+            __syncwarp();
             r.step(stages);
           }
-          if (ok) umma_commit(&bar.pv_done[gp & 1]);
+          if (!ok) break;
+          if (elect_one()) {
+            if (D == 128) {  // the sums of weights, which d = 64 has beside the values
+#pragma unroll
+              for (int k = 0; k < kTreeTile / 16; ++k) umma_bf16(l_tmem, l_desc, p_desc + k * 16, idesc_l, k > 0 ? 1u : first);
+            }
+            umma_commit(&bar.pv_done[gp & 1]);
+          }
+          __syncwarp();
           ++gp;
         }
       } while (ok && tree_walk_next(line_of(p), w));
     }
-    __syncwarp();
   } else if (warp >= kEpiWarp0 && warp < kEpiWarp0 + 8) {
     const int wg = (warp - kEpiWarp0) >> 2, quarter = warp & 3;
     const int r = quarter * 32 + lane;        // cache row of the tile
     const int et = threadIdx.x - kEpiWarp0 * 32;  // 0 .. 255
-    const int gpv = (p.plan.rpc + 7) >> 3;    // column groups of a value head
     float* m = reinterpret_cast<float*>(smem + L.m);
     float* tau = reinterpret_cast<float*>(smem + L.tau);
     float* cs = reinterpret_cast<float*>(smem + L.cs);
     float* fac = reinterpret_cast<float*>(smem + L.f);
+    int* out_row = reinterpret_cast<int*>(smem + L.row);
     unsigned long long* mask = reinterpret_cast<unsigned long long*>(smem + L.mask);
     const uint32_t lanes = (uint32_t)(quarter * 32) << 16;
     const int G = p.h_q / p.h_k;
     int gt = 0;  // tiles so far
     Ring seg_ring;  // ring position of the segment's first load
-    float l[MAXG * 8];
     bool ok = true;
     if (any) do {
       const Heads h = heads_of(p, w);
-      // column groups of this warpgroup
-      const int live = h.nv * gpv, g0 = wg == 0 ? 0 : (live + 1) >> 1, ng = wg == 0 ? (live + 1) >> 1 : live >> 1;
-      const int v_first = g0 / gpv, v_last = ng > 0 ? (g0 + ng - 1) / gpv : v_first - 1;
+      // column groups of this warpgroup: half of the live ones
+      Groups mine;
+      mine.groups = p.plan.groups;
+      mine.nvp = p.plan.nvp;
+      const int live = h.nv * mine.groups, g0 = wg == 0 ? 0 : (live + 1) >> 1;
+      mine.count = wg == 0 ? (live + 1) >> 1 : live >> 1;
+      mine.at = g0 % mine.groups;
+      mine.col = g0 / mine.groups * mine.nvp + mine.at * 8;
       const int nt = w.t1 - w.t0;
-      float* scales = reinterpret_cast<float*>(smem + L.scales) + wg * (1 + p.plan.nv) * kTreeTile + r;
-      const size_t kr = key_row(p, w, h);
-      unsigned long long seen = 0;
-      if (w.t1 * kTreeTile > w.P) seen = seen_by_any(p, w);
-      auto fetch_scales = [&](int i) {  // of the segment's tile i
-        if (!E4M3) return;
-        float* dst = scales + (i & 1) * 2 * (1 + p.plan.nv) * kTreeTile;
+      auto fetch_scale = [&](int i) {  // of the row in the segment's tile i
         const int row = (w.t0 + i) * kTreeTile + r;
-        const bool there = row_seen(w, seen, row);
-        const size_t safe = there ? row : 0;
-        cp_async4_zfill(dst, p.k_scale + kr + safe, there);
-        for (int v = v_first; v <= v_last; ++v)
-          cp_async4_zfill(dst + (1 + v - v_first) * kTreeTile, p.v_scale + value_row(p, w, h, v) + safe, there);
-        cp_async_commit();
+        return row < w.P + w.n ? __ldg(p.k_scale + h.key + row) : 0.f;
       };
-      fetch_scales(0);
-      // Q and the columns' words
+      float key_scale = 0.f;
+      if (E4M3) key_scale = fetch_scale(0);
+      // the columns' words, then Q with every load in flight before the first is used
+      int my_row = -1;  // of the output: thread et's column
+      float my_tau = INFINITY;
+      unsigned long long my_mask = 0ull;
+      if (et < cols) {
+        int jj, t;
+        if (tree_row(p.plan, p.tokens, h.chunk, et, &jj, &t) && t < w.n) {
+          my_row = (w.b * p.tokens + t) * p.h_q + h.kh * G + jj;
+          my_tau = p.tau != nullptr ? p.tau[w.b * p.h_q + h.kh * G + jj] : -INFINITY;
+          my_mask = p.mask != nullptr ? p.mask[(size_t)w.b * p.tokens + t] : (2ull << t) - 1ull;
+        }
+      }
       named_bar_sync(3, kEpiAll);  // the last segment's words and Q are no longer read
-      constexpr int LPR = D / 8;
-      for (int i = et; i < cols * LPR; i += kEpiAll) {  // whole warps: cols * LPR is a multiple of 128
-        const int col = i / LPR, c = i % LPR;
-        int jj = 0, t = 0;
-        const bool there = tree_row(p.plan, p.tokens, h.chunk, col, &jj, &t) && t < w.n;
-        uint4 x = make_uint4(0u, 0u, 0u, 0u);
-        if (there)
-          x = *reinterpret_cast<const uint4*>(p.q + (((size_t)w.b * p.tokens + t) * p.h_q + h.kh * G + jj) * D + c * 8);
+      if (et < cols) {
+        m[et] = my_row >= 0 ? kUnset : -kUnset;  // padding: weights of zero whatever its scores
+        out_row[et] = my_row;
+      }
+      named_bar_sync(3, kEpiAll);
+      constexpr int LPR = D / 8, STEP = kEpiAll / LPR, PER = kTreeMaxCols / STEP;
+      uint4 x[PER];
+      const int c = et % LPR;
+#pragma unroll
+      for (int i = 0; i < PER; ++i) {
+        const int col = et / LPR + i * STEP;
+        const int row = col < cols ? out_row[col] : -1;
+        x[i] = make_uint4(0u, 0u, 0u, 0u);
+        if (row >= 0) x[i] = __ldg(reinterpret_cast<const uint4*>(p.q + (size_t)row * D + c * 8));
+      }
+      if (et < cols) {
+        tau[et] = my_tau;
+        mask[et] = my_mask;
+      }
+      unsigned long long seen = 0;
+      if (!E4M3 && w.t1 * kTreeTile > w.P) seen = seen_by_any(p, w);
+#pragma unroll
+      for (int i = 0; i < PER; ++i) {
+        const int col = et / LPR + i * STEP;
         if (E4M3) {
           float f[8];
-          const uint32_t u[4] = {x.x, x.y, x.z, x.w};
+          const uint32_t u[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
           float amax = 0.f;
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
@@ -662,97 +752,96 @@ __global__ void __launch_bounds__(kTreeThreads<E4M3>, 1)
           const float down = __uint_as_float((uint32_t)(127 - ex) << 23);
           uint32_t y[4];
 #pragma unroll
-          for (int k = 0; k < 4; ++k) y[k] = pack2<true>(f[2 * k] * down, f[2 * k + 1] * down);
-          x = make_uint4(y[0], y[1], y[2], y[3]);
-          if (c == 0) cs[col] = __uint_as_float((uint32_t)(127 + ex) << 23) * p.scale;
+          for (int k = 0; k < 4; ++k) y[k] = pack_half(f[2 * k] * down, f[2 * k + 1] * down);
+          x[i] = make_uint4(y[0], y[1], y[2], y[3]);
+          if (c == 0 && col < cols) cs[col] = __uint_as_float((uint32_t)(127 + ex) << 23) * p.scale;
         }
-        *reinterpret_cast<uint4*>(smem + L.q + (c >> 3) * (cols * 128) + col * 128 + (((c & 7) ^ (col & 7)) << 4)) = x;
-        if (c == 0) {
-          m[col] = there ? kUnset : -kUnset;  // padding: weights of zero whatever its scores
-          tau[col] = !there ? INFINITY : p.tau != nullptr ? p.tau[w.b * p.h_q + h.kh * G + jj] : -INFINITY;
-          mask[col] = !there ? 0ull : p.mask != nullptr ? p.mask[(size_t)w.b * p.tokens + t] : (2ull << t) - 1ull;
-        }
+        if (col < cols)
+          *reinterpret_cast<uint4*>(smem + L.q + (c >> 3) * (cols * 128) + col * 128 + (((c & 7) ^ (col & 7)) << 4)) = x[i];
       }
       fence_proxy_async_shared();
       named_bar_sync(3, kEpiAll);
       if (lane == 0) mbar_arrive(bar.q_full);
-#pragma unroll
-      for (int i = 0; i < MAXG * 8; ++i) l[i] = 0.f;
 
       for (int i = 0; i < nt; ++i, ++gt) {
         const int buf = gt & 1;
-        Tile<D, E4M3> t;
-        t.s_tmem = tmem + buf * cols + lanes;
-        t.p_buf = smem + L.p + buf * L.p_bytes;
-        t.p_row = t.p_buf + r * 16;
-        t.sc = scales + (i & 1) * 2 * (1 + p.plan.nv) * kTreeTile;
-        t.scale = p.scale;
+        const uint32_t s_tmem = tmem + buf * cols + lanes;
+        uint8_t* p_buf = smem + L.p + buf * L.p_bytes;
         const int row = (w.t0 + i) * kTreeTile + r;
-        t.all = row < w.P;
-        t.bit = !t.all && row < w.P + w.n ? 1ull << (row - w.P) : 0ull;
+        Row rw;
+        rw.f = E4M3 ? key_scale : p.scale;
+        rw.all = row < w.P;
+        rw.bit = !rw.all && row < w.P + w.n ? 1ull << (row - w.P) : 0ull;
         const bool tail = (w.t0 + i + 1) * kTreeTile > w.P;
         const bool masked = tail || p.tau != nullptr;
-        if (E4M3) {
-          cp_async_wait_all();
-          if (i + 1 < nt) fetch_scales(i + 1);
-        }
+        if (E4M3 && i + 1 < nt) key_scale = fetch_scale(i + 1);
         ok = mbar_wait(&bar.s_full[buf], (gt >> 1) & 1, abort_flag) &&
              (gt < 2 || mbar_wait(&bar.pv_done[buf], ((gt >> 1) - 1) & 1, abort_flag));
-        // the 256 threads meet at the same barriers, so they give up together
-        if (named_bar_or(3, kEpiAll, !ok || *abort_flag != 0)) {
-          ok = false;
-          break;
-        }
         tc_fence_after();
-        auto pass = [&](auto mode) {
-          constexpr int kMode = decltype(mode)::value;
-          return masked ? tile_pass<D, E4M3, MAXG, true, kMode>(p, t, g0, ng, gpv, m, tau, cs, mask, l)
-                        : tile_pass<D, E4M3, MAXG, false, kMode>(p, t, g0, ng, gpv, m, tau, cs, mask, l);
+        auto weights = [&]() {
+          return masked ? weigh<E4M3, true>(s_tmem, p_buf + r * 16, mine, rw, m, tau, cs, mask)
+                        : weigh<E4M3, false>(s_tmem, p_buf + r * 16, mine, rw, m, tau, cs, mask);
         };
-        bool redo = i == 0;
-        if (!redo) {
-          redo = named_bar_or(1 + wg, 128, pass(Mode<kAccumulate>()));
-          if (redo) {
-            pass(Mode<kUndo>());
-            // the accumulators are moved below: the products so far must be in them (a wait that gives up sets
-            // the abort flag, seen at the next tile)
-            mbar_wait(&bar.pv_done[buf ^ 1], ((gt - 1) >> 1) & 1, abort_flag);
-            tc_fence_after();
-          }
-        }
-        if (redo) {
-          pass(Mode<kMax>());
-          named_bar_sync(1 + wg, 128);
-          const int c = et & 127;
-          if (c < ng * 8) {
-            const int ag = g0 + (c >> 3), vl = ag / gpv, col = vl * p.plan.nvp + (ag - vl * gpv) * 8 + (c & 7);
-            const float* words = column_words(t.p_buf, col) + (c & 7);
-            const float top = fmaxf(fmaxf(words[0], words[8]), fmaxf(words[16], words[24]));
-            const float old = m[col];
-            const float now = top > -INFINITY ? fmaxf(old, top - (E4M3 ? 8.f : 0.f)) : old;
-            m[col] = now;
-            fac[col] = old == kUnset ? 0.f : ex2(old - now);
-          }
-          named_bar_sync(1 + wg, 128);
+        // A segment's first tile: any score that every column sees is a good enough reference, so the tile's first
+        // row's; a tile with drafted rows takes the exact maxima.
+        float top = INFINITY;
+        if (i == 0 && !tail) {
+          if (quarter == 0) {
+            Groups g = mine;
+#pragma unroll 1
+            for (int n = g.count; n > 0; --n, g.step()) {
+              float s[8];
+              tmem_ld8(s_tmem + g.col, s);
+              exponents<E4M3, false, false>(s, rw, g.col, m, tau, cs, mask);
+              if (lane == 0) {
 #pragma unroll
-          for (int g = 0; g < MAXG; ++g) {
-            if (g < ng) {
-              const int vl = (g0 + g) / gpv, col = vl * p.plan.nvp + (g0 + g - vl * gpv) * 8;
-              float f[8];
-              *reinterpret_cast<float4*>(f) = *reinterpret_cast<const float4*>(fac + col);
-              *reinterpret_cast<float4*>(f + 4) = *reinterpret_cast<const float4*>(fac + col + 4);
-#pragma unroll
-              for (int k = 0; k < 8; ++k) l[g * 8 + k] *= f[k];
-              if (i > 0) {
-                float o[8];
-                tmem_ld8(o_tmem + lanes + col, o);
-#pragma unroll
-                for (int k = 0; k < 8; ++k) o[k] *= f[k];
-                tmem_st8(o_tmem + lanes + col, o);
+                for (int k = 0; k < 8; ++k)
+                  if (m[g.col + k] == kUnset) m[g.col + k] = s[k];
               }
             }
           }
-          pass(Mode<kAccumulate>());
+          named_bar_sync(1 + wg, 128);
+        }
+        if (i > 0 || !tail) top = weights();
+        if (named_bar_or(3, kEpiAll, top > kOver || !ok || *abort_flag != 0)) {
+          // new references, or the end of it all: the 256 threads meet at the same barriers, so they go together
+          if (named_bar_or(3, kEpiAll, !ok || *abort_flag != 0)) {
+            ok = false;
+            break;
+          }
+          if (masked) maxima<E4M3, true>(s_tmem, p_buf, mine, rw, m, tau, cs, mask);
+          else maxima<E4M3, false>(s_tmem, p_buf, mine, rw, m, tau, cs, mask);
+          named_bar_sync(1 + wg, 128);
+          for (int c = et & 127; c < mine.count * 8; c += 128) {
+            const int ag = g0 + (c >> 3), col = ag / mine.groups * mine.nvp + ag % mine.groups * 8 + (c & 7);
+            const float* words = column_words(p_buf, col) + (c & 7);
+            const float now = fmaxf(fmaxf(words[0], words[8]), fmaxf(words[16], words[24]));
+            const float old = m[col], next = now > -INFINITY ? fmaxf(old, now) : old;
+            m[col] = next;
+            fac[col] = old == kUnset ? 0.f : ex2(old - next);
+          }
+          if (i > 0) {
+            // the products so far must be in the accumulators (a wait that gives up sets the abort flag, which the
+            // next tile sees)
+            mbar_wait(&bar.pv_done[buf ^ 1], ((gt - 1) >> 1) & 1, abort_flag);
+            tc_fence_after();
+          }
+          named_bar_sync(1 + wg, 128);
+          if (i > 0) {
+            Groups g = mine;
+#pragma unroll 1
+            for (int n = g.count; n > 0; --n, g.step())
+#pragma unroll
+              for (int part = 0; part < (D == 64 ? 1 : 2); ++part) {
+                const uint32_t at = (part == 0 ? o_tmem : l_tmem) + lanes + g.col;
+                float o[8];
+                tmem_ld8(at, o);
+#pragma unroll
+                for (int k = 0; k < 8; ++k) o[k] *= fac[g.col + k];
+                tmem_st8(at, o);
+              }
+          }
+          weights();
         }
         fence_proxy_async_shared();
         tc_fence_before();
@@ -770,9 +859,9 @@ __global__ void __launch_bounds__(kTreeThreads<E4M3>, 1)
             if (!__all_sync(0xffffffffu, mbar_wait(&bar.full[vr.st], vr.round & 1, abort_flag))) break;
             if (bad) {
 #pragma unroll
-              for (int k = 0; k < D / 8; ++k)
+              for (int k = 0; k < D / 8; ++k)  // neighbouring rows at different banks
                 *reinterpret_cast<uint4*>(smem + vr.st * L.stage_bytes + (k >> 3) * (kTreeTile * 128) + r * 128 +
-                                          (k & 7) * 16) = make_uint4(0u, 0u, 0u, 0u);
+                                          ((k + r) & 7) * 16) = make_uint4(0u, 0u, 0u, 0u);
               fence_proxy_async_shared();
             }
             __syncwarp();
@@ -793,62 +882,55 @@ __global__ void __launch_bounds__(kTreeThreads<E4M3>, 1)
       tc_fence_after();
       const bool whole = w.t0 == 0 && w.t1 == w.tiles;
       const size_t slot = (size_t)blockIdx.x + w.item;
-      uint8_t* words0 = smem + L.p;
-      int* out_row = reinterpret_cast<int*>(tau);
+      // the sums of weights: lanes 64 .. 127 of the accumulators (d = 64), or lane 0 of their own columns
+      if (quarter == (D == 64 ? 2 : 0)) {
+        Groups g = mine;
+#pragma unroll 1
+        for (int n = g.count; n > 0; --n, g.step()) {
+          float l[8];
+          tmem_ld8((D == 64 ? o_tmem : l_tmem) + lanes + g.col, l);
+          float sum = l[0];
 #pragma unroll
-      for (int g = 0; g < MAXG; ++g) {
-        if (g < ng) {
-          const int vl = (g0 + g) / gpv, col = vl * p.plan.nvp + (g0 + g - vl * gpv) * 8;
-          const float x = octet_sum(l + g * 8, lane);
-          if ((lane & 3) == 0)
-            column_words(words0, col)[quarter * 8 + (lane >> 4 & 1) * 4 + (lane >> 3 & 1) * 2 + (lane >> 2 & 1)] = x;
-        }
-      }
-      named_bar_sync(1 + wg, 128);
-      {
-        const int c = et & 127;
-        if (c < ng * 8) {
-          const int ag = g0 + (c >> 3), vl = ag / gpv, col = vl * p.plan.nvp + (ag - vl * gpv) * 8 + (c & 7);
-          const float* words = column_words(words0, col) + (c & 7);
-          const float sum = (words[0] + words[8]) + (words[16] + words[24]);
-          int jj = 0, t = 0;
-          const bool there = tree_row(p.plan, p.tokens, h.chunk, col, &jj, &t) && t < w.n;
-          out_row[col] = there ? (w.b * p.tokens + t) * p.h_q + h.kh * G + jj : -1;
-          if (whole) {
-            fac[col] = sum > 0.f ? 1.f / sum : 0.f;
-          } else if (there) {
-            p.part_l[slot * cols + col] = sum;
-            p.part_m[slot * cols + col] = m[col];
+          for (int k = 1; k < 8; ++k) sum = lane == k ? l[k] : sum;
+          if (lane < 8) {
+            if (whole) {
+              fac[g.col + lane] = sum > 0.f ? 1.f / sum : 0.f;
+            } else {
+              p.part_l[slot * cols + g.col + lane] = sum;
+              p.part_m[slot * cols + g.col + lane] = m[g.col + lane];
+            }
           }
         }
       }
-      named_bar_sync(1 + wg, 128);
-      // lane of the accumulators: d (D = 128), or 16 of each warp's 32 (M = 64)
-      const bool has_d = D == 128 || lane < 16;
-      const int dd = D == 128 ? r : quarter * 16 + (lane & 15);
-      for (int g = 0; g < ng; ++g) {
-        const int vl = (g0 + g) / gpv, col = vl * p.plan.nvp + (g0 + g - vl * gpv) * 8;
-        float o[8];
-        tmem_ld8(o_tmem + lanes + col, o);
-        if (!has_d) continue;
+      if (whole) named_bar_sync(1 + wg, 128);
+      if (D == 128 || quarter < 2) {
+        Groups g = mine;
+#pragma unroll 1
+        for (int n = g.count; n > 0; --n, g.step()) {
+          float o[8];
+          tmem_ld8(o_tmem + lanes + g.col, o);
+          if (!whole) {  // padding too: nobody reads it
+            float* dst = p.part_o + (slot * cols + g.col) * D + r;
 #pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          const int row = out_row[col + k];
-          if (row < 0) continue;
-          if (!whole) {
-            p.part_o[(slot * cols + col + k) * D + dd] = o[k];
-          } else {
-            const float x = fac[col + k] > 0.f ? o[k] * fac[col + k] : 0.f;
-            if (p.out_bf16) static_cast<__nv_bfloat16*>(p.out)[(size_t)row * D + dd] = __float2bfloat16(x);
-            else static_cast<float*>(p.out)[(size_t)row * D + dd] = x;
+            for (int k = 0; k < 8; ++k) dst[k * D] = o[k];
+            continue;
+          }
+#pragma unroll
+          for (int k = 0; k < 8; ++k) {
+            const int row = out_row[g.col + k];
+            if (row < 0) continue;
+            const float f = fac[g.col + k], y = f > 0.f ? o[k] * f : 0.f;
+            if (p.out_bf16) static_cast<__nv_bfloat16*>(p.out)[(size_t)row * D + r] = __float2bfloat16(y);
+            else static_cast<float*>(p.out)[(size_t)row * D + r] = y;
           }
         }
       }
       tc_fence_before();
     } while (tree_walk_next(line_of(p), w));
-    if (E4M3) cp_async_wait_all();
   } else if (E4M3 && warp >= kConvWarp0) {
-    if (any) widen_tiles<D>(p, w, smem, bar, abort_flag);
+    if (any) widen_tiles<D>(p, w, smem, bar, progress, abort_flag);
+  } else if (E4M3 && warp == 2) {
+    if (any) prefetch_tiles<D>(p, w, progress, abort_flag);
   }
 
   tc_fence_before();
@@ -860,7 +942,7 @@ __global__ void __launch_bounds__(kTreeThreads<E4M3>, 1)
       for (int x = issued > stages ? issued - stages : 0; x < issued; ++x)
         mbar_wait_drain(&bar.full[x % stages], (x / stages) & 1);
     }
-    if (threadIdx.x == 32) {  // and so do the products
+    if (warp == 1) {  // and so do the products (every lane may have issued some)
       umma_commit(bar.drain);
       mbar_wait_drain(bar.drain, 0);
     }
@@ -873,93 +955,132 @@ __global__ void __launch_bounds__(kTreeThreads<E4M3>, 1)
 }
 
 // ------------------------------------------------------------------ the join
-// One CTA per query row: the partials of the CTAs that shared its item, each
-// relative to its own power of two.  A row whose item one CTA held is there
-// already.
-constexpr int kJoinThreads = 512;
+// The partials of the CTAs that shared a query row's item, each relative to
+// its own power of two.  A row whose item one CTA held is there already.
+// WARPS warps per row, each with every WARPS-th partial: 8 where an item is
+// spread over many CTAs (a CTA per row and 32 of its elements), 1 where items
+// are many and have few partials each (8 rows per CTA).  With 8 for all, the
+// rows of 64 tokens in a batch of 8 took 150 us to join and now 6.
+constexpr int kJoinThreads = 256;
 
-template <int D>
-__global__ void __launch_bounds__(kJoinThreads) saga_tree_join_kernel(const TreeParams p) {
-  constexpr int GROUPS = kJoinThreads / D;
-  __shared__ float weight[kJoinThreads], acc[GROUPS][D], red[2][kJoinThreads / 32];
-  __shared__ long long line[2];
+template <int WARPS, int COLS>
+__global__ void __launch_bounds__(kJoinThreads) saga_tree_join_kernel(const TreeParams p, const int d) {
+  constexpr int LANES = COLS / 4, AT_ONCE = 32 / LANES;  // lanes of a partial (16 bytes each), partials per load
+  constexpr int BATCH = 4;                               // loads in flight
+  __shared__ float4 acc[kJoinThreads];
+  __shared__ float sums[8], tops[8];
   pdl_trigger();
   pdl_wait();
-  const int j = blockIdx.x % p.h_q, bt = blockIdx.x / p.h_q, b = bt / p.tokens, t = bt - b * p.tokens;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const long long at_row = WARPS == 8 ? blockIdx.x : (long long)blockIdx.x * 8 + warp;
   const TreeLine rows = line_of(p);
+  if (at_row >= (long long)p.batch * p.tokens * p.h_q) return;  // WARPS == 1: the warp's own
+  const int row = (int)at_row;
+  const int j = row % p.h_q, bt = row / p.h_q, b = bt / p.tokens, t = bt - b * p.tokens;
   int P, n;
   tree_lens(rows, b, &P, &n);
   if (t >= n) return;
-  const int G = p.h_q / p.h_k, H = rows.items;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  if (warp == 0) {
-    long long before = 0, total = 0;
-    for (int i = lane; i < p.batch; i += 32) {
-      int P2, n2;
-      tree_lens(rows, i, &P2, &n2);
-      const long long x = (long long)H * tree_tiles(P2, n2);
-      total += x;
-      if (i < b) before += x;
-    }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-      total += __shfl_xor_sync(0xffffffffu, total, o);
-      before += __shfl_xor_sync(0xffffffffu, before, o);
-    }
-    if (lane == 0) {
-      line[0] = before;
-      line[1] = total;
-    }
+  long long before = 0, total = 0;
+  for (int i = lane; i < p.batch; i += 32) {
+    int P2, n2;
+    tree_lens(rows, i, &P2, &n2);
+    const long long y = (long long)rows.items * tree_tiles(P2, n2);
+    total += y;
+    if (i < b) before += y;
   }
-  __syncthreads();
-  const int tiles = tree_tiles(P, n);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    total += __shfl_xor_sync(0xffffffffu, total, o);
+    before += __shfl_xor_sync(0xffffffffu, before, o);
+  }
+  const int G = p.h_q / p.h_k, tiles = tree_tiles(P, n);
   const TreeSpot spot = tree_spot(p.plan, p.tokens, j % G, t);
   const int hc = (j / G) * p.plan.chunks + spot.chunk;
-  const long long first = line[0] + (long long)hc * tiles;
-  const int ctas = tree_ctas(line[1], p.ctas);
-  const int c0 = tree_cta_of(line[1], ctas, first), c1 = tree_cta_of(line[1], ctas, first + tiles - 1);
+  const long long first = before + (long long)hc * tiles;
+  const int ctas = tree_ctas(total, p.ctas);
+  const int c0 = tree_cta_of(total, ctas, first), c1 = tree_cta_of(total, ctas, first + tiles - 1);
   if (c0 == c1) return;
-  const size_t slot0 = (size_t)c0 + b * H + hc;
-  const int parts = c1 - c0 + 1;  // at most the CTAs of the attention kernel, under kJoinThreads
-  float mine = kUnset, ml = 0.f;
-  if (threadIdx.x < parts) {
-    mine = p.part_m[(slot0 + threadIdx.x) * p.plan.cols + spot.col];
-    ml = p.part_l[(slot0 + threadIdx.x) * p.plan.cols + spot.col];
+  const int w = WARPS == 8 ? warp : 0;
+  const int parts = c1 - c0 >= w ? (c1 - c0 - w) / WARPS + 1 : 0;  // this warp's: w, w + WARPS, ...
+  const size_t slot0 = (size_t)c0 + (size_t)b * rows.items + hc + w;
+  const int sub = lane / LANES, l4 = lane % LANES;
+  const size_t step = (size_t)WARPS * p.plan.cols;
+  const float4* src = reinterpret_cast<const float4*>(p.part_o + (slot0 * p.plan.cols + spot.col) * d + blockIdx.y * COLS) + l4;
+  const size_t step4 = step * d / 4;
+  float top = kUnset, sum = 0.f;
+  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int base = 0; base < parts; base += 32) {
+    float pm = kUnset, pl = 0.f;
+    if (base + lane < parts) {
+      pm = p.part_m[slot0 * p.plan.cols + spot.col + (base + lane) * step];
+      pl = p.part_l[slot0 * p.plan.cols + spot.col + (base + lane) * step];
+    }
+    const float now = fmaxf(top, warp_max(pl > 0.f ? pm : kUnset));
+    const float f = ex2(top - now), wt = pl > 0.f ? ex2(pm - now) : 0.f;
+    top = now;
+    float add = wt * pl;
+#pragma unroll
+    for (int x = 16; x > 0; x >>= 1) add += __shfl_xor_sync(0xffffffffu, add, x);
+    sum = sum * f + add;
+    o.x *= f, o.y *= f, o.z *= f, o.w *= f;
+    const int here = min(32, parts - base);
+    for (int i0 = 0; i0 < here; i0 += AT_ONCE * BATCH) {
+      float4 x[BATCH];
+      float fw[BATCH];
+#pragma unroll
+      for (int k = 0; k < BATCH; ++k) {
+        const int i = i0 + k * AT_ONCE + sub;
+        fw[k] = __shfl_sync(0xffffffffu, wt, i & 31);
+        if (i >= here) fw[k] = 0.f;
+        x[k] = fw[k] > 0.f ? src[(size_t)(base + i) * step4] : make_float4(0.f, 0.f, 0.f, 0.f);
+      }
+#pragma unroll
+      for (int k = 0; k < BATCH; ++k) {
+        o.x = fmaf(fw[k], x[k].x, o.x);
+        o.y = fmaf(fw[k], x[k].y, o.y);
+        o.z = fmaf(fw[k], x[k].z, o.z);
+        o.w = fmaf(fw[k], x[k].w, o.w);
+      }
+    }
   }
-  float top = ml > 0.f ? mine : kUnset;
-  top = warp_max(top);
-  if (lane == 0) red[0][warp] = top;
-  __syncthreads();
 #pragma unroll
-  for (int i = 0; i < kJoinThreads / 32; ++i) top = fmaxf(top, red[0][i]);
-  const float wt = ml > 0.f ? ex2(mine - top) : 0.f;
-  weight[threadIdx.x] = wt;
-  float sum = wt * ml;
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-  if (lane == 0) red[1][warp] = sum;
-  __syncthreads();
-  const int d = threadIdx.x % D, g = threadIdx.x / D;
-  float o = 0.f;
-  const float* src = p.part_o + (slot0 * p.plan.cols + spot.col) * D + d;
-  const size_t step = (size_t)p.plan.cols * D;
-#pragma unroll 8
-  for (int i = g; i < parts; i += GROUPS) {
-    const float x = src[i * step], f = weight[i];
-    o += f > 0.f ? x * f : 0.f;
+  for (int x = LANES; x < 32; x <<= 1) {
+    o.x += __shfl_xor_sync(0xffffffffu, o.x, x);
+    o.y += __shfl_xor_sync(0xffffffffu, o.y, x);
+    o.z += __shfl_xor_sync(0xffffffffu, o.z, x);
+    o.w += __shfl_xor_sync(0xffffffffu, o.w, x);
   }
-  acc[g][d] = o;
-  __syncthreads();
-  if (threadIdx.x < D) {
-    float total_o = 0.f, total_l = 0.f;
+  if (WARPS == 8) {
+    if (lane == 0) {
+      sums[warp] = sum;
+      tops[warp] = top;
+    }
+    acc[threadIdx.x] = o;
+    __syncthreads();
+    if (warp != 0) return;
 #pragma unroll
-    for (int i = 0; i < GROUPS; ++i) total_o += acc[i][d];
+    for (int i = 0; i < 8; ++i) top = fmaxf(top, tops[i]);
+    sum = 0.f;
+    o = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-    for (int i = 0; i < kJoinThreads / 32; ++i) total_l += red[1][i];
-    const float x = total_l > 0.f ? total_o / total_l : 0.f;
-    const size_t at = (size_t)blockIdx.x * D + d;
-    if (p.out_bf16) static_cast<__nv_bfloat16*>(p.out)[at] = __float2bfloat16(x);
-    else static_cast<float*>(p.out)[at] = x;
+    for (int i = 0; i < 8; ++i) {
+      const float f = ex2(tops[i] - top);
+      const float4 x = acc[i * 32 + lane];
+      sum = fmaf(f, sums[i], sum);
+      o.x = fmaf(f, x.x, o.x);
+      o.y = fmaf(f, x.y, o.y);
+      o.z = fmaf(f, x.z, o.z);
+      o.w = fmaf(f, x.w, o.w);
+    }
+  }
+  if (lane >= LANES) return;
+  const float inv = sum > 0.f ? 1.f / sum : 0.f;
+  const size_t at = (size_t)row * d + blockIdx.y * COLS + l4 * 4;
+  if (p.out_bf16) {
+    *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.out) + at) =
+        make_uint2(pack_bf16(o.x * inv, o.y * inv), pack_bf16(o.z * inv, o.w * inv));
+  } else {
+    *reinterpret_cast<float4*>(static_cast<float*>(p.out) + at) = make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv);
   }
 }
 
@@ -994,13 +1115,6 @@ TreeSizes tree_sizes(const saga_shape* s, const TreePlan& plan, int ctas) {
 
 typedef void (*TreeKernel)(CUtensorMap, CUtensorMap, TreeParams);
 
-template <int D, bool E4M3>
-TreeKernel pick_groups(int half, int* which) {
-  *which = half <= 1 ? 0 : half <= 2 ? 1 : half <= 4 ? 2 : 3;
-  return half <= 1 ? saga_tree_kernel<D, E4M3, 1> : half <= 2 ? saga_tree_kernel<D, E4M3, 2>
-         : half <= 4 ? saga_tree_kernel<D, E4M3, 4> : saga_tree_kernel<D, E4M3, 8>;
-}
-
 }  // namespace
 }  // namespace saga
 
@@ -1012,7 +1126,7 @@ size_t saga_tree_workspace_bytes(const saga_shape* s, int tokens) {
   if (validate_tree(s, tokens)) return 0;
   int sms = 0;
   if (api_device_sms(&sms)) return 0;
-  return tree_sizes(s, tree_plan(s->h_q, s->h_k, s->h_v, s->d, tokens), sms).total;
+  return tree_sizes(s, tree_plan(s->h_q, s->h_k, s->h_v, tokens), sms).total;
 }
 
 int saga_tree_attn(const saga_shape* s, int tokens, const void* q, const saga_cache* cache, const int* prefix_lens,
@@ -1031,11 +1145,11 @@ int saga_tree_attn(const saga_shape* s, int tokens, const void* q, const saga_ca
   rc = api_device_sms(&sms);
   if (rc) return rc;
   TreeParams p{};
-  p.plan = tree_plan(s->h_q, s->h_k, s->h_v, s->d, tokens);
+  p.plan = tree_plan(s->h_q, s->h_k, s->h_v, tokens);
   const TreeSizes z = tree_sizes(s, p.plan, sms);
   if (ws_bytes < z.total) return api_fail(SAGA_ERR_WORKSPACE, "workspace has %zu bytes, needs %zu", ws_bytes, z.total);
   const bool e4m3 = cache->format == SAGA_CACHE_E4M3;
-  p.smem = tree_smem(p.plan, s->d, e4m3);
+  p.smem = tree_smem(p.plan, s->d);
   p.q = static_cast<const uint16_t*>(q);
   p.k = cache->k;
   p.v = cache->v;
@@ -1055,7 +1169,7 @@ int saga_tree_attn(const saga_shape* s, int tokens, const void* q, const saga_ca
   p.h_k = s->h_k;
   p.h_v = s->h_v;
   p.l_cap = s->l_cap;
-  p.ctas = std::min(sms, kJoinThreads);  // the join holds one partial of each in a thread
+  p.ctas = sms;
   char* base = static_cast<char*>(workspace);
   p.part_o = reinterpret_cast<float*>(base + kTreeStatusBytes);
   p.part_m = reinterpret_cast<float*>(base + z.part_m);
@@ -1067,21 +1181,22 @@ int saga_tree_attn(const saga_shape* s, int tokens, const void* q, const saga_ca
     rc = api_rows_map(&vm, cache->v, (long long)s->batch * s->h_v * s->l_cap, s->d);
     if (rc) return rc;
   }
-  const int half = (p.plan.groups + 1) / 2;
-  int which = 0;
-  const TreeKernel kernel = s->d == 64 ? (e4m3 ? pick_groups<64, true>(half, &which) : pick_groups<64, false>(half, &which))
-                                       : (e4m3 ? pick_groups<128, true>(half, &which) : pick_groups<128, false>(half, &which));
-  static std::atomic<uint64_t> done[16], done_join[2];
+  const TreeKernel kernel = s->d == 64 ? (e4m3 ? saga_tree_kernel<64, true> : saga_tree_kernel<64, false>)
+                                       : (e4m3 ? saga_tree_kernel<128, true> : saga_tree_kernel<128, false>);
+  static std::atomic<uint64_t> done[4], done_join[3];
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   cudaError_t e = prepare_kernel(reinterpret_cast<const void*>(kernel), 227 * 1024,
-                                 done[which + (e4m3 ? 4 : 0) + (s->d == 64 ? 0 : 8)]);
+                                 done[(e4m3 ? 1 : 0) + (s->d == 64 ? 0 : 2)]);
   if (e == cudaSuccess)
     e = launch_pdl(kernel, dim3(p.ctas), dim3(e4m3 ? kTreeThreads<true> : kTreeThreads<false>), p.smem.total, st, km, vm, p);
   if (e != cudaSuccess) return api_cuda_fail(e, "drafted-token attention launch");
-  auto join = s->d == 64 ? saga_tree_join_kernel<64> : saga_tree_join_kernel<128>;
-  e = prepare_kernel(reinterpret_cast<const void*>(join), 0, done_join[s->d == 64 ? 0 : 1]);
+  // partials of an item: about ctas / items of them, and one more
+  const unsigned rows = (unsigned)s->batch * tokens * s->h_q;
+  const bool few = 4ll * s->batch * s->h_k * p.plan.chunks >= p.ctas;
+  auto join = !few ? saga_tree_join_kernel<8, 32> : s->d == 64 ? saga_tree_join_kernel<1, 64> : saga_tree_join_kernel<1, 128>;
+  e = prepare_kernel(reinterpret_cast<const void*>(join), 0, done_join[!few ? 0 : s->d == 64 ? 1 : 2]);
   if (e == cudaSuccess)
-    e = launch_pdl(join, dim3((unsigned)s->batch * tokens * s->h_q), dim3(kJoinThreads), 0, st, p);
+    e = launch_pdl(join, few ? dim3((rows + 7) / 8) : dim3(rows, s->d / 32), dim3(kJoinThreads), 0, st, p, s->d);
   if (e != cudaSuccess) return api_cuda_fail(e, "drafted-token join launch");
   return api_ok();
 }

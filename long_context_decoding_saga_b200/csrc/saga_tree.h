@@ -25,17 +25,17 @@ struct TreePlan {
   int rpc;     // columns of a value head per chunk, before padding
   int nvp;     // the same, padded
   int chunks;  // chunks per key head
-  int cols;    // columns of a chunk: nv * nvp, padded to 16
-  int groups;  // 8-column groups with a live column, per chunk
+  int cols;    // columns of a chunk: nv * nvp
+  int groups;  // 8-column groups with a live column, per value head of a chunk
 };
 
-__host__ __device__ inline TreePlan tree_plan(int h_q, int h_k, int h_v, int d, int T) {
+__host__ __device__ inline TreePlan tree_plan(int h_q, int h_k, int h_v, int T) {
   TreePlan p;
   const int G = h_q / h_k, per_v = h_q / h_v;
   p.hpv = per_v < G ? per_v : G;
   p.nvh = G / p.hpv;
   p.rows = p.hpv * T;
-  const int unit = d == 64 ? 8 : 16;  // columns of the value product: M = 64 takes 8, M = 128 takes 16
+  const int unit = 16;  // columns that a product with M = 128 is made of
   const int padded = (p.rows + unit - 1) / unit * unit;
   if (padded <= kTreeMaxCols) {
     const int per = kTreeMaxCols / padded;
@@ -53,8 +53,8 @@ __host__ __device__ inline TreePlan tree_plan(int h_q, int h_k, int h_v, int d, 
     p.nv = 1;
     p.chunks = p.nvh * p.rsplit;
   }
-  p.cols = (p.nv * p.nvp + 15) / 16 * 16;
-  p.groups = p.nv * ((p.rpc + 7) / 8);
+  p.cols = p.nv * p.nvp;
+  p.groups = (p.rpc + 7) / 8;
   return p;
 }
 
@@ -95,19 +95,19 @@ struct TreeWalk {
   int item;
 };
 
-// share: the batch row of the first tile, that tile's place among the batch
-// row's, the tiles of the share.
-__host__ __device__ inline bool tree_walk_begin(const TreeLine& l, const long long* share, TreeWalk& w) {
-  w.left = share[2];
-  if (w.left == 0) return false;
-  w.b = (int)share[0];
-  tree_lens(l, w.b, &w.P, &w.n);
+// The first segment of a share of `count` >= 1 tiles whose first is the
+// `place`-th of batch row b's.
+__host__ __device__ inline TreeWalk tree_walk_begin(const TreeLine& l, int b, long long place, long long count) {
+  TreeWalk w;
+  w.left = count;
+  w.b = b;
+  tree_lens(l, b, &w.P, &w.n);
   w.tiles = tree_tiles(w.P, w.n);
-  w.hc = (int)(share[1] / w.tiles);
-  w.t0 = (int)(share[1] - (long long)w.hc * w.tiles);
-  w.t1 = w.tiles - w.t0 < w.left ? w.tiles : w.t0 + (int)w.left;
-  w.item = w.b * l.items + w.hc;
-  return true;
+  w.hc = (int)(place / w.tiles);
+  w.t0 = (int)(place - (long long)w.hc * w.tiles);
+  w.t1 = w.tiles - w.t0 < count ? w.tiles : w.t0 + (int)count;
+  w.item = b * l.items + w.hc;
+  return w;
 }
 
 __host__ __device__ inline bool tree_walk_next(const TreeLine& l, TreeWalk& w) {
@@ -193,33 +193,33 @@ __host__ __device__ inline bool tree_row(const TreePlan& p, int T, int chunk, in
   return true;
 }
 
-// Shared memory of the kernel: the tile ring, Q, two P buffers, per-column
-// words, the scales of two tiles (8-bit caches), barriers.
+// Shared memory of the kernel: the tile ring, ones (the operand that adds the
+// weights up), Q, two P buffers, per-column words, barriers.
 struct TreeSmem {
   int stages, stage_bytes;
-  int q, p, p_bytes, m, tau, cs, f, mask, scales, bars, total;
+  int ones, q, p, p_bytes, mask, m, tau, cs, f, row, bars, total;
 };
-__host__ __device__ inline TreeSmem tree_smem(const TreePlan& p, int d, bool e4m3) {
+__host__ __device__ inline TreeSmem tree_smem(const TreePlan& p, int d) {
   TreeSmem s;
   s.stage_bytes = kTreeTile * d * 2;
   const int budget = 227 * 1024 - 1024;  // less the slack that aligns the base to 1024 bytes
   const int q_bytes = p.cols * d * 2;
   s.p_bytes = p.cols * kTreeTile * 2;
-  const int words = p.cols * (4 + 4 + 4 + 4 + 8);
-  const int scale_bytes = e4m3 ? 2 * 2 * (1 + p.nv) * kTreeTile * 4 : 0;
-  const int bar_bytes = 8 * (3 * kTreeMaxStages + 16) + 64;
-  const int fixed = q_bytes + 2 * s.p_bytes + words + scale_bytes + bar_bytes;
+  const int words = p.cols * (8 + 5 * 4);
+  const int bar_bytes = 8 * (3 * kTreeMaxStages + 16) + 16 + (int)sizeof(TreeWalk);
+  const int fixed = 2048 + q_bytes + 2 * s.p_bytes + words + bar_bytes;
   s.stages = (budget - fixed) / s.stage_bytes;
   if (s.stages > kTreeMaxStages) s.stages = kTreeMaxStages;
-  s.q = s.stages * s.stage_bytes;
+  s.ones = s.stages * s.stage_bytes;
+  s.q = s.ones + 2048;
   s.p = s.q + q_bytes;
   s.mask = s.p + 2 * s.p_bytes;
   s.m = s.mask + p.cols * 8;
   s.tau = s.m + p.cols * 4;
   s.cs = s.tau + p.cols * 4;
   s.f = s.cs + p.cols * 4;
-  s.scales = s.f + p.cols * 4;
-  s.bars = s.scales + scale_bytes;
+  s.row = s.f + p.cols * 4;
+  s.bars = s.row + p.cols * 4;
   s.total = s.bars + bar_bytes + 1024;
   return s;
 }

@@ -3,10 +3,11 @@
 Bound, element by element, with w the exact softmax weights: a score is off by at most
   es = ((D + 64) 2^-23 + 2^-21) sum |q_c k_c| / sqrt(d)
 (fp32 sums in any order with truncating tensor-core steps, the products with the scales), which changes weights by
-a factor of at most e^(2 es); the weights are rounded to 16 bits (2^-8 for bf16; half precision is finer), the
-exponential and the fp32 sums over L rows add 2^-20 + L 2^-23, weights that half precision loses in its last place add
-2^-24 of the largest weight per row, and a bf16 output adds 2^-8 of the value:
-  |out - exact| <= sum w |v| (2^-8 + e^(2 es) - 1 + 2^-20 + L 2^-23 + ...) (+ 2^-8 |exact| for bf16).
+a factor of at most e^(2 es).  The weights are rounded to bf16, w' = w (1 + d) with |d| <= 2^-8, and divided by the sum
+of the rounded ones, so sum w' v / sum w' is off by at most sum w |v| (2^-8 + 2^-8) to first order (2^-15 covers the
+second).  Values of an 8-bit cache are rounded to bf16 too: 2^-8 more.  The exponential and the fp32 sums over L rows add
+2^-20 + L 2^-23, and a bf16 output 2^-8 of the value:
+  |out - exact| <= sum w |v| (2 or 3 * 2^-8 + 2^-15 + e^(2 es) - 1 + 2^-20 + L 2^-23)  (+ 2^-8 |exact| for bf16).
 Thresholds are placed so that every score is more than es from them: a score that is off by at most es is then on
 the same side of its threshold.
 """
@@ -68,7 +69,7 @@ def _words(masks):
     return torch.tensor([[m - (1 << 64) if m >> 63 else m for m in row] for row in masks], dtype=torch.int64)
 
 
-def _bounds(q, K, V, prefix, n, masks, tau, D):
+def _bounds(q, K, V, prefix, n, masks, tau, D, fmt):
     """exact outputs, and their bounds for an fp32 output, of one batch row."""
     exact, border = so.attend(q, K, V, prefix, n, masks, tau)
     spread, _ = so.attend(q, K, np.abs(V), prefix, n, masks, tau)
@@ -78,9 +79,8 @@ def _bounds(q, K, V, prefix, n, masks, tau, D):
         return exact, np.zeros_like(exact), border, 0.0
     dots = max(float((np.abs(q[:n, j]) @ np.abs(K[j * K.shape[0] // h_q, :L]).T).max()) for j in range(h_q))
     es = ((D + 64) * 2.0 ** -23 + 2.0 ** -21) * dots / np.sqrt(d)
-    rel = 2.0 ** -8 + np.expm1(2 * es) + 2.0 ** -20 + L * 2.0 ** -23
-    vmax = float(np.abs(V[:, :L]).max())
-    return exact, spread * rel + L * 2.0 ** -24 * vmax * 2.0 ** -4, border, es
+    rel = (2 if fmt == BF16 else 3) * 2.0 ** -8 + 2.0 ** -15 + np.expm1(2 * es) + 2.0 ** -20 + L * 2.0 ** -23
+    return exact, spread * rel, border, es
 
 
 def _check(heads, fmt, prefixes, T, masks=None, counts=None, tau_n=0, out_dtype=torch.float32, seed=0, l_cap=None,
@@ -134,7 +134,7 @@ def _check(heads, fmt, prefixes, T, masks=None, counts=None, tau_n=0, out_dtype=
     assert torch.equal(out, again), "a second call on the workspace differs"
     for b in range(B):
         exact, bound, border, es = _bounds(qe[b], K[b], V[b], prefixes[b], n[b], None if masks is None else masks[b],
-                                           None if tau is None else tau[b].astype(np.float64), d)
+                                           None if tau is None else tau[b].astype(np.float64), d, fmt)
         if tau_n:
             assert border > es, "the thresholds of this test are too near a score"
         got = out[b, :n[b]].double().cpu().numpy()
@@ -234,7 +234,7 @@ def test_rising_scores():
         out = torch.empty((1, 1, 12, 128), device="cuda")
         ws = saga.alloc_tree_workspace(shape, 1)
         saga.saga_tree_attn(shape, q.cuda(), cache, torch.tensor([P], dtype=torch.int32).cuda(), out, ws)
-        exact, bound, _, _ = _bounds(q[0].double().numpy(), K[0], V[0], P, 1, None, None, 128)
+        exact, bound, _, _ = _bounds(q[0].double().numpy(), K[0], V[0], P, 1, None, None, 128, fmt)
         assert (np.abs(out[0].double().cpu().numpy() - exact) <= bound).all()
 
 
@@ -249,7 +249,7 @@ def test_a_bad_prefix_is_clamped_and_flagged():
     saga.saga_tree_attn(shape, q.cuda(), cache, torch.tensor([-5, 98], dtype=torch.int32).cuda(), out, ws)
     assert saga.saga_get_status(ws) == saga.SAGA_STATUS_LEN_CLAMPED
     for b, P in enumerate((0, 97)):
-        exact, bound, _, _ = _bounds(q[b].double().numpy(), K[b], V[b], P, 3, None, None, 64)
+        exact, bound, _, _ = _bounds(q[b].double().numpy(), K[b], V[b], P, 3, None, None, 64, BF16)
         assert (np.abs(out[b].double().cpu().numpy() - exact) <= bound).all()
 
 
@@ -265,7 +265,7 @@ def test_one_token_matches_the_dense_decode_call():
     tau = torch.empty((1, 32), device="cuda")
     saga.saga_decode_attn(shape, q[:, 0].contiguous(), cache.k, cache.v, 1001, 1200, 1, 0, tau, ref,
                           saga.alloc_workspace(shape))
-    exact, bound, _, _ = _bounds(q[0].double().cpu().numpy(), K[0], V[0], 1000, 1, None, None, 64)
+    exact, bound, _, _ = _bounds(q[0].double().cpu().numpy(), K[0], V[0], 1000, 1, None, None, 64, BF16)
     assert (np.abs(out[0, 0].double().cpu().numpy() - ref[0].double().cpu().numpy()) <= 2 * bound[0]).all()
 
 
@@ -360,10 +360,10 @@ def test_a_served_step(fmt):
     qn = so.rotate(so.norm(xe[:, :h_q], w.double().numpy(), 1e-6), (P + depth[0]).numpy(), inv.double().numpy(), False)
     qg = q_out[0].double().cpu().numpy()
     assert np.abs(qg - qn).max() <= 2.0 ** -8 * np.abs(qn).max() * 1.01
-    exact, bound, _, _ = _bounds(qg, K[0], V[0], P, T, masks[0], None, d)
+    exact, bound, _, _ = _bounds(qg, K[0], V[0], P, T, masks[0], None, d, fmt)
     assert (np.abs(outs["dense"][0].double().cpu().numpy() - exact) <= bound).all()
     te = tau[0].double().cpu().numpy()
-    exact, bound, border, es = _bounds(qg, K[0], V[0], P, T, masks[0], te, d)
+    exact, bound, border, es = _bounds(qg, K[0], V[0], P, T, masks[0], te, d, fmt)
     if border > es:
         assert (np.abs(outs["kept"][0].double().cpu().numpy() - exact) <= bound).all()
     counts = (K[0, 0, :P + 1] @ qg[0].T / np.sqrt(d) >= te).sum(axis=0)

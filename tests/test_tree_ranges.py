@@ -32,10 +32,10 @@ static void plans() {
       if (h_q % h_k || h_q % h_v || (h_v % h_k && h_k % h_v) || h_q / h_k > (d == 64 ? 64 : 32)) continue;
       if (h_v > h_k && h_v / h_k > 32) continue;
       for (int T : Ts) {
-        const TreePlan p = tree_plan(h_q, h_k, h_v, d, T);
-        const int G = h_q / h_k, unit = d == 64 ? 8 : 16;
-        CHECK(p.cols <= kTreeMaxCols && p.cols % 16 == 0 && p.nvp % unit == 0 && p.nv * p.nvp <= p.cols, "cols");
-        CHECK(p.groups <= 16 && p.groups >= 1, "groups");
+        const TreePlan p = tree_plan(h_q, h_k, h_v, T);
+        const int G = h_q / h_k;
+        CHECK(p.cols <= kTreeMaxCols && p.cols % 16 == 0 && p.nvp % 16 == 0 && p.nv * p.nvp <= p.cols, "cols");
+        CHECK(p.groups * 8 <= p.nvp && p.groups >= 1, "groups");
         CHECK(p.hpv * p.nvh == G, "heads");
         std::map<std::pair<int, int>, int> seen;
         for (int jj = 0; jj < G; ++jj) for (int t = 0; t < T; ++t) {
@@ -56,10 +56,10 @@ static void plans() {
           live += tree_row(p, T, c, col, &a, &b);
         }
         CHECK(live == G * T, "live columns %d of %d", live, G * T);
-        for (int e = 0; e < 2; ++e) {
-          const TreeSmem s = tree_smem(p, d, e);
+        {
+          const TreeSmem s = tree_smem(p, d);
           CHECK(s.stages >= 3 && s.stages <= kTreeMaxStages && s.total <= 227 * 1024, "smem %d stages %d", s.total, s.stages);
-          CHECK(s.q % 1024 == 0 && s.p % 1024 == 0 && s.m % 16 == 0 && s.f % 16 == 0 && s.bars % 8 == 0, "smem alignment");
+          CHECK(s.ones % 1024 == 0 && s.q % 1024 == 0 && s.p % 1024 == 0 && s.m % 16 == 0 && s.f % 16 == 0 && s.bars % 8 == 0, "smem alignment");
         }
       }
     }
@@ -95,9 +95,8 @@ static void lines() {
       int b = 0;
       while (b + 1 < B && before[b + 1] <= first) ++b;
       { int P, n; tree_lens(line, b, &P, &n); while (tree_tiles(P, n) == 0) { --b; tree_lens(line, b, &P, &n); } }
-      const long long share[3] = {b, first - before[b], count};
-      TreeWalk w;
-      bool more = tree_walk_begin(line, share, w);
+      TreeWalk w = tree_walk_begin(line, b, first - before[b], count);
+      bool more = true;
       while (more) {
         CHECK(w.t0 < w.t1 && w.t1 <= w.tiles && w.hc < items, "segment");
         CHECK(w.item == w.b * items + w.hc, "item");
