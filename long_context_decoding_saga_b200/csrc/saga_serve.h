@@ -91,6 +91,7 @@ struct TreeParams {
   float* part_o;   // [slots, cols, d]: sums of weights times values
   float* part_m;   // [slots, cols]: the power of two that the weights are relative to
   float* part_l;   // [slots, cols]: sums of weights
+  int2* holders;   // [items]: first and last CTA of an item
 };
 
 int api_check_cache(const saga_shape* s, const saga_cache* c);

@@ -54,6 +54,42 @@ __device__ __forceinline__ TreeLine line_of(const TreeParams& p) {
   return TreeLine{p.prefix_lens, p.counts, p.tokens, p.l_cap, p.h_k * p.plan.chunks};
 }
 
+__device__ __forceinline__ int warp_sum(int x) { return __reduce_add_sync(0xffffffffu, x); }
+__device__ __forceinline__ int warp_scan(int x) {  // inclusive
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int y = __shfl_up_sync(0xffffffffu, x, o);
+    if (lane_id() >= o) x += y;
+  }
+  return x;
+}
+
+// The cut of the line (a whole warp calls; the same in every warp of both kernels).
+__device__ __forceinline__ TreeCut cut_of(const TreeLine& line, int batch, int most, bool* clamped) {
+  TreeCut c{0, most, false};
+  int P = 0, n = 0;
+  for (int b = lane_id(); b < batch; b += 32) {
+    if (!tree_lens(line, b, &P, &n)) *clamped = true;
+    c.total += line.items * tree_tiles(P, n);
+  }
+  c.total = warp_sum(c.total);
+  *clamped = __any_sync(0xffffffffu, *clamped);
+  if (c.total == 0) return c;
+  int fewest = 1 << 30, longest = 0;
+  for (int b = lane_id(); b < batch; b += 32) {
+    if (batch > 32) tree_lens(line, b, &P, &n);  // else it is the one just read
+    const int tiles = tree_tiles(P, n);
+    if (tiles == 0) continue;
+    const int k = tree_item_ctas(c, tiles);
+    fewest = min(fewest, k);
+    if (k > 0) longest = max(longest, tree_longest(tiles, k));
+  }
+  fewest = __reduce_min_sync(0xffffffffu, fewest);
+  longest = __reduce_max_sync(0xffffffffu, longest);
+  c.by_items = fewest > 0 && longest <= tree_longest_even(c) + kTreeChange;
+  return c;
+}
+
 // Heads of a segment.
 struct Heads {
   int kh, chunk, nv;  // key head, chunk, value heads here
@@ -207,35 +243,47 @@ struct Row {
   unsigned long long bit;  // else the drafted token in it (0: none)
 };
 
+
+__device__ __forceinline__ void load8(const float* from, float* to) {
+  *reinterpret_cast<float4*>(to) = *reinterpret_cast<const float4*>(from);
+  *reinterpret_cast<float4*>(to + 4) = *reinterpret_cast<const float4*>(from + 4);
+}
+
 // Scores of 8 columns in powers of two, less the columns' references with
-// RELATIVE; -inf where hidden or below the threshold.
-template <bool E4M3, bool MASKED, bool RELATIVE>
+// RELATIVE; with TEST -inf where the row is hidden or the score below the
+// threshold (a row of the prefix is hidden from nobody: no masks are read).
+template <bool E4M3, bool TEST, bool RELATIVE>
 __device__ __forceinline__ void exponents(float* s, const Row& r, int col, const float* m, const float* tau,
                                           const float* cs, const unsigned long long* mask) {
-  float mm[8], cc[8];
-  if (RELATIVE) {
-    *reinterpret_cast<float4*>(mm) = *reinterpret_cast<const float4*>(m + col);
-    *reinterpret_cast<float4*>(mm + 4) = *reinterpret_cast<const float4*>(m + col + 4);
-  }
-  if (E4M3) {
-    *reinterpret_cast<float4*>(cc) = *reinterpret_cast<const float4*>(cs + col);
-    *reinterpret_cast<float4*>(cc + 4) = *reinterpret_cast<const float4*>(cs + col + 4);
+  float mm[8], cc[8], tt[8];
+  if (RELATIVE) load8(m + col, mm);
+  if (E4M3) load8(cs + col, cc);
+  if (TEST) load8(tau + col, tt);
+  unsigned seen = 0xffu;
+  if (TEST && !r.all) {
+    seen = 0u;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const ulonglong2 x = *reinterpret_cast<const ulonglong2*>(mask + col + 2 * i);
+      if ((x.x & r.bit) != 0ull) seen |= 1u << (2 * i);
+      if ((x.y & r.bit) != 0ull) seen |= 2u << (2 * i);
+    }
   }
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
     const float f = E4M3 ? r.f * cc[i] : r.f;
-    if (!MASKED) {
+    if (!TEST) {
       s[i] = RELATIVE ? fmaf(s[i], f * kLog2e, -mm[i]) : s[i] * (f * kLog2e);
     } else {
       const float a = s[i] * f;
-      const bool keep = (r.all || (mask[col + i] & r.bit) != 0ull) && a >= tau[col + i];
+      const bool keep = a >= tt[i] && (seen >> i & 1u) != 0u;
       s[i] = keep ? (RELATIVE ? fmaf(a, kLog2e, -mm[i]) : a * kLog2e) : -INFINITY;
     }
   }
 }
 
 // Weights of a tile into P; returns the largest exponent of the thread's.
-template <bool E4M3, bool MASKED>
+template <bool E4M3, bool TEST>
 __device__ __forceinline__ float weigh(uint32_t s_tmem, uint8_t* p_row, Groups g, const Row& r, const float* m,
                                        const float* tau, const float* cs, const unsigned long long* mask) {
   float top = -INFINITY;
@@ -248,7 +296,7 @@ __device__ __forceinline__ float weigh(uint32_t s_tmem, uint8_t* p_row, Groups g
     const int col = g.col;
     g.step();
     if (n > 1) tmem_ld8_start(s_tmem + g.col, raw);  // the next group's scores, while this one's are weighed
-    exponents<E4M3, MASKED, true>(s, r, col, m, tau, cs, mask);
+    exponents<E4M3, TEST, true>(s, r, col, m, tau, cs, mask);
     uint32_t w[4];
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
@@ -263,14 +311,14 @@ __device__ __forceinline__ float weigh(uint32_t s_tmem, uint8_t* p_row, Groups g
 }
 
 // The columns' largest scores over the warp's rows, into the column words.
-template <bool E4M3, bool MASKED>
+template <bool E4M3, bool TEST>
 __device__ __forceinline__ void maxima(uint32_t s_tmem, uint8_t* p_buf, Groups g, const Row& r, const float* m,
                                        const float* tau, const float* cs, const unsigned long long* mask) {
 #pragma unroll 1
   for (int n = g.count; n > 0; --n, g.step()) {
     float s[8];
     tmem_ld8(s_tmem + g.col, s);
-    exponents<E4M3, MASKED, false>(s, r, g.col, m, tau, cs, mask);
+    exponents<E4M3, TEST, false>(s, r, g.col, m, tau, cs, mask);
     float* words = column_words(p_buf, g.col) + (threadIdx.x >> 5 & 3) * 8;
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
@@ -410,7 +458,7 @@ __device__ void widen_tiles(const TreeParams& p, const TreeWalk& w0, uint8_t* sm
   };
   Ring r;
   if (group == 1) {
-    f.next(p);  // a share has a key tile and a value tile at least
+    f.next(p);  // a run has a key tile and a value tile at least
     r.step(L.stages);
   }
   fetch();
@@ -469,7 +517,8 @@ __global__ void __launch_bounds__(kTreeThreads<E4M3>, 1)
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bar.drain + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   TreeWalk* share = reinterpret_cast<TreeWalk*>(tmem_slot + 2);  // left == 0: this CTA has no tiles
-  volatile int* progress = reinterpret_cast<volatile int*>(share + 1);
+  TreeCut* share_cut = reinterpret_cast<TreeCut*>(share + 1);
+  volatile int* progress = reinterpret_cast<volatile int*>(share_cut + 1);
   const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   const int stages = L.stages;
   const int cols = p.plan.cols;
@@ -508,45 +557,40 @@ __global__ void __launch_bounds__(kTreeThreads<E4M3>, 1)
       *reinterpret_cast<uint4*>(smem + L.ones + i * 16) = make_uint4(0x3f803f80u, 0x3f803f80u, 0x3f803f80u, 0x3f803f80u);
     fence_proxy_async_shared();
   }
+  if (warp == 3) {
+    // lines that the start needs, into L2 before the dependency wait: a prefetch moves no values
+    if (lane == 0) prefetch_l2_line(p.prefix_lens);
+    if (lane == 1 && p.counts != nullptr) prefetch_l2_line(p.counts);
+    const long long q_lines = (long long)p.batch * p.tokens * p.h_q * D / 64;
+    for (long long i = (long long)blockIdx.x * 32 + lane; i < q_lines; i += (long long)gridDim.x * 32) prefetch_l2_line(p.q + i * 64);
+    if (p.mask != nullptr)
+      for (int i = blockIdx.x * 32 + lane; i < p.batch * p.tokens / 16; i += gridDim.x * 32) prefetch_l2_line(p.mask + i * 16);
+    if (p.tau != nullptr)
+      for (int i = blockIdx.x * 32 + lane; i < p.batch * p.h_q / 32; i += gridDim.x * 32) prefetch_l2_line(p.tau + i * 32);
+  }
   pdl_trigger();
   pdl_wait();
   if (warp == 0) {
-    // this CTA's share of the line of tiles
+    // this CTA's run of the line of tiles
     const TreeLine line = line_of(p);
-    const long long H = line.items;
-    long long total = 0;
     bool clamped = false;
-    for (int b = lane; b < p.batch; b += 32) {
-      int P, n;
-      clamped |= !tree_lens(line, b, &P, &n);
-      total += H * tree_tiles(P, n);
-    }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
+    const TreeCut cut = cut_of(line, p.batch, p.ctas, &clamped);
     if (blockIdx.x == 0 && clamped) flag_status(p.status, SAGA_STATUS_LEN_CLAMPED);
-    const int ctas = tree_ctas(total, p.ctas);
-    const bool working = (int)blockIdx.x < ctas;
-    const long long first = working ? tree_first_tile(total, ctas, blockIdx.x) : 0;
-    const long long count = working ? tree_first_tile(total, ctas, blockIdx.x + 1) - first : 0;
-    long long base = 0;
+    const int at = tree_start(cut, blockIdx.x);
     if (lane == 0) share->left = 0;
     __syncwarp();
-    for (int b0 = 0; b0 < p.batch && count > 0; b0 += 32) {
-      long long mine = 0;
-      if (b0 + lane < p.batch) {
-        int P, n;
-        tree_lens(line, b0 + lane, &P, &n);
-        mine = H * tree_tiles(P, n);
-      }
-      long long incl = mine;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const long long x = __shfl_up_sync(0xffffffffu, incl, o);
-        if (lane >= o) incl += x;
-      }
-      const unsigned hit = __ballot_sync(0xffffffffu, base + incl > first);
+    int base = 0;
+    for (int b0 = 0; b0 < p.batch && at >= 0; b0 += 32) {
+      int P = 0, n = 0;
+      if (b0 + lane < p.batch) tree_lens(line, b0 + lane, &P, &n);
+      const int mine = tree_extent(line, cut, tree_tiles(P, n));
+      const int incl = warp_scan(mine);
+      const unsigned hit = __ballot_sync(0xffffffffu, base + incl > at);
       if (hit != 0u) {
-        if (lane == __ffs(hit) - 1) *share = tree_walk_begin(line, b0 + lane, first - (base + incl - mine), count);
+        if (lane == __ffs(hit) - 1) {
+          *share = tree_walk_begin(line, cut, blockIdx.x, b0 + lane, at - (base + incl - mine), P, n);
+          *share_cut = cut;
+        }
         break;
       }
       base += __shfl_sync(0xffffffffu, incl, 31);
@@ -716,52 +760,61 @@ __global__ void __launch_bounds__(kTreeThreads<E4M3>, 1)
         out_row[et] = my_row;
       }
       named_bar_sync(3, kEpiAll);
-      constexpr int LPR = D / 8, STEP = kEpiAll / LPR, PER = kTreeMaxCols / STEP;
-      uint4 x[PER];
+      constexpr int LPR = D / 8, STEP = kEpiAll / LPR, FLIGHT = 4;
       const int c = et % LPR;
+#pragma unroll 1
+      for (int col0 = et / LPR; col0 - et / LPR < cols; col0 += FLIGHT * STEP) {
+        uint4 x[FLIGHT];
 #pragma unroll
-      for (int i = 0; i < PER; ++i) {
-        const int col = et / LPR + i * STEP;
-        const int row = col < cols ? out_row[col] : -1;
-        x[i] = make_uint4(0u, 0u, 0u, 0u);
-        if (row >= 0) x[i] = __ldg(reinterpret_cast<const uint4*>(p.q + (size_t)row * D + c * 8));
+        for (int i = 0; i < FLIGHT; ++i) {
+          const int row = col0 + i * STEP < cols ? out_row[col0 + i * STEP] : -1;
+          x[i] = make_uint4(0u, 0u, 0u, 0u);
+          if (row >= 0) x[i] = __ldg(reinterpret_cast<const uint4*>(p.q + (size_t)row * D + c * 8));
+        }
+#pragma unroll
+        for (int i = 0; i < FLIGHT; ++i) {
+          const int col = col0 + i * STEP;
+          if (E4M3) {
+            float f[8];
+            const uint32_t u[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+            float amax = 0.f;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              f[2 * k] = __uint_as_float(u[k] << 16);
+              f[2 * k + 1] = __uint_as_float(u[k] & 0xffff0000u);
+              amax = fmaxf(amax, fmaxf(fabsf(f[2 * k]), fabsf(f[2 * k + 1])));
+            }
+#pragma unroll
+            for (int o = LPR / 2; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+            // a power of two that brings the row's largest element into [1, 2); both it and its inverse are normal
+            const int ex = min(max((int)(__float_as_uint(amax) >> 23) - 127, -126), 126);
+            const float down = __uint_as_float((uint32_t)(127 - ex) << 23);
+            uint32_t y[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) y[k] = pack_half(f[2 * k] * down, f[2 * k + 1] * down);
+            x[i] = make_uint4(y[0], y[1], y[2], y[3]);
+            if (c == 0 && col < cols) cs[col] = __uint_as_float((uint32_t)(127 + ex) << 23) * p.scale;
+          }
+          if (col < cols)
+            *reinterpret_cast<uint4*>(smem + L.q + (c >> 3) * (cols * 128) + col * 128 + (((c & 7) ^ (col & 7)) << 4)) = x[i];
+        }
       }
       if (et < cols) {
         tau[et] = my_tau;
         mask[et] = my_mask;
       }
-      unsigned long long seen = 0;
-      if (!E4M3 && w.t1 * kTreeTile > w.P) seen = seen_by_any(p, w);
-#pragma unroll
-      for (int i = 0; i < PER; ++i) {
-        const int col = et / LPR + i * STEP;
-        if (E4M3) {
-          float f[8];
-          const uint32_t u[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
-          float amax = 0.f;
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            f[2 * k] = __uint_as_float(u[k] << 16);
-            f[2 * k + 1] = __uint_as_float(u[k] & 0xffff0000u);
-            amax = fmaxf(amax, fmaxf(fabsf(f[2 * k]), fabsf(f[2 * k + 1])));
-          }
-#pragma unroll
-          for (int o = LPR / 2; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-          // a power of two that brings the row's largest element into [1, 2); both it and its inverse are normal
-          const int ex = min(max((int)(__float_as_uint(amax) >> 23) - 127, -126), 126);
-          const float down = __uint_as_float((uint32_t)(127 - ex) << 23);
-          uint32_t y[4];
-#pragma unroll
-          for (int k = 0; k < 4; ++k) y[k] = pack_half(f[2 * k] * down, f[2 * k + 1] * down);
-          x[i] = make_uint4(y[0], y[1], y[2], y[3]);
-          if (c == 0 && col < cols) cs[col] = __uint_as_float((uint32_t)(127 + ex) << 23) * p.scale;
-        }
-        if (col < cols)
-          *reinterpret_cast<uint4*>(smem + L.q + (c >> 3) * (cols * 128) + col * 128 + (((c & 7) ^ (col & 7)) << 4)) = x[i];
-      }
       fence_proxy_async_shared();
       named_bar_sync(3, kEpiAll);
       if (lane == 0) mbar_arrive(bar.q_full);
+      // for the join: the CTAs that hold the item (even runs: the line's tile at which it begins is the run's first
+      // and what the run has done so far)
+      if (et == 0 && w.t0 == 0) {
+        const TreeCut cut = *share_cut;
+        const int place = cut.by_items ? 0 : tree_even_first(cut, blockIdx.x) + gt;
+        p.holders[w.item] = make_int2(blockIdx.x, tree_last_holder(cut, blockIdx.x, w.tiles, place));
+      }
+      unsigned long long seen = 0;
+      if (!E4M3 && w.t1 * kTreeTile > w.P) seen = seen_by_any(p, w);
 
       for (int i = 0; i < nt; ++i, ++gt) {
         const int buf = gt & 1;
@@ -773,44 +826,59 @@ __global__ void __launch_bounds__(kTreeThreads<E4M3>, 1)
         rw.all = row < w.P;
         rw.bit = !rw.all && row < w.P + w.n ? 1ull << (row - w.P) : 0ull;
         const bool tail = (w.t0 + i + 1) * kTreeTile > w.P;
-        const bool masked = tail || p.tau != nullptr;
+        const bool test = tail || p.tau != nullptr;
         if (E4M3 && i + 1 < nt) key_scale = fetch_scale(i + 1);
         ok = mbar_wait(&bar.s_full[buf], (gt >> 1) & 1, abort_flag) &&
              (gt < 2 || mbar_wait(&bar.pv_done[buf], ((gt >> 1) - 1) & 1, abort_flag));
         tc_fence_after();
         auto weights = [&]() {
-          return masked ? weigh<E4M3, true>(s_tmem, p_buf + r * 16, mine, rw, m, tau, cs, mask)
-                        : weigh<E4M3, false>(s_tmem, p_buf + r * 16, mine, rw, m, tau, cs, mask);
+          uint8_t* at = p_buf + r * 16;
+          return test ? weigh<E4M3, true>(s_tmem, at, mine, rw, m, tau, cs, mask)
+                      : weigh<E4M3, false>(s_tmem, at, mine, rw, m, tau, cs, mask);
         };
         // A segment's first tile: any score that every column sees is a good enough reference, so the tile's first
-        // row's; a tile with drafted rows takes the exact maxima.
+        // row's; where that is a drafted row, the exact maxima.
+        const bool common = (w.t0 + i) * kTreeTile < w.P;
         float top = INFINITY;
-        if (i == 0 && !tail) {
+        if (i == 0 && common) {
           if (quarter == 0) {
             Groups g = mine;
 #pragma unroll 1
-            for (int n = g.count; n > 0; --n, g.step()) {
-              float s[8];
-              tmem_ld8(s_tmem + g.col, s);
-              exponents<E4M3, false, false>(s, rw, g.col, m, tau, cs, mask);
-              if (lane == 0) {
+            for (int n = g.count; n > 0; n -= 2) {
+              uint32_t raw[2][8];
+              const int col = g.col;
+              tmem_ld8_start(s_tmem + g.col, raw[0]);
+              g.step();
+              const int next = g.col;
+              if (n > 1) tmem_ld8_start(s_tmem + g.col, raw[1]);
+              g.step();
 #pragma unroll
-                for (int k = 0; k < 8; ++k)
-                  if (m[g.col + k] == kUnset) m[g.col + k] = s[k];
+              for (int k = 0; k < 2; ++k) {
+                if (k >= n) break;
+                float s[8];
+                tmem_ld8_end(raw[k], s);
+                const int at = k == 0 ? col : next;
+                exponents<E4M3, false, false>(s, rw, at, m, tau, cs, mask);
+                if (lane == 0) {
+                  float old[8];
+                  load8(m + at, old);  // padding keeps its own
+#pragma unroll
+                  for (int i2 = 0; i2 < 8; ++i2) m[at + i2] = old[i2] == kUnset ? s[i2] : old[i2];
+                }
               }
             }
           }
           named_bar_sync(1 + wg, 128);
         }
-        if (i > 0 || !tail) top = weights();
+        if (i > 0 || common) top = weights();
         if (named_bar_or(3, kEpiAll, top > kOver || !ok || *abort_flag != 0)) {
           // new references, or the end of it all: the 256 threads meet at the same barriers, so they go together
           if (named_bar_or(3, kEpiAll, !ok || *abort_flag != 0)) {
             ok = false;
             break;
           }
-          if (masked) maxima<E4M3, true>(s_tmem, p_buf, mine, rw, m, tau, cs, mask);
-          else maxima<E4M3, false>(s_tmem, p_buf, mine, rw, m, tau, cs, mask);
+          // the general test serves every tile here: rows of a tile without drafted ones are seen by all
+          maxima<E4M3, true>(s_tmem, p_buf, mine, rw, m, tau, cs, mask);
           named_bar_sync(1 + wg, 128);
           for (int c = et & 127; c < mine.count * 8; c += 128) {
             const int ag = g0 + (c >> 3), col = ag / mine.groups * mine.nvp + ag % mine.groups * 8 + (c & 7);
@@ -966,43 +1034,25 @@ constexpr int kJoinThreads = 256;
 template <int WARPS, int COLS>
 __global__ void __launch_bounds__(kJoinThreads) saga_tree_join_kernel(const TreeParams p, const int d) {
   constexpr int LANES = COLS / 4, AT_ONCE = 32 / LANES;  // lanes of a partial (16 bytes each), partials per load
-  constexpr int BATCH = 4;                               // loads in flight
+  constexpr int BATCH = WARPS == 8 ? 5 : 4;              // loads in flight
   __shared__ float4 acc[kJoinThreads];
   __shared__ float sums[8], tops[8];
   pdl_trigger();
   pdl_wait();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const long long at_row = WARPS == 8 ? blockIdx.x : (long long)blockIdx.x * 8 + warp;
-  const TreeLine rows = line_of(p);
   if (at_row >= (long long)p.batch * p.tokens * p.h_q) return;  // WARPS == 1: the warp's own
   const int row = (int)at_row;
   const int j = row % p.h_q, bt = row / p.h_q, b = bt / p.tokens, t = bt - b * p.tokens;
-  int P, n;
-  tree_lens(rows, b, &P, &n);
-  if (t >= n) return;
-  long long before = 0, total = 0;
-  for (int i = lane; i < p.batch; i += 32) {
-    int P2, n2;
-    tree_lens(rows, i, &P2, &n2);
-    const long long y = (long long)rows.items * tree_tiles(P2, n2);
-    total += y;
-    if (i < b) before += y;
-  }
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
-    total += __shfl_xor_sync(0xffffffffu, total, o);
-    before += __shfl_xor_sync(0xffffffffu, before, o);
-  }
-  const int G = p.h_q / p.h_k, tiles = tree_tiles(P, n);
-  const TreeSpot spot = tree_spot(p.plan, p.tokens, j % G, t);
-  const int hc = (j / G) * p.plan.chunks + spot.chunk;
-  const long long first = before + (long long)hc * tiles;
-  const int ctas = tree_ctas(total, p.ctas);
-  const int c0 = tree_cta_of(total, ctas, first), c1 = tree_cta_of(total, ctas, first + tiles - 1);
+  const TreeSpot spot = tree_spot(p.plan, p.tokens, j % (p.h_q / p.h_k), t);
+  const int item = (b * p.h_k + j / (p.h_q / p.h_k)) * p.plan.chunks + spot.chunk;
+  const int2 held = p.holders[item];  // not written where the batch row has no tokens
+  if (p.counts != nullptr && t >= p.counts[b]) return;
+  const int c0 = held.x, c1 = held.y;
   if (c0 == c1) return;
   const int w = WARPS == 8 ? warp : 0;
   const int parts = c1 - c0 >= w ? (c1 - c0 - w) / WARPS + 1 : 0;  // this warp's: w, w + WARPS, ...
-  const size_t slot0 = (size_t)c0 + (size_t)b * rows.items + hc + w;
+  const size_t slot0 = (size_t)c0 + item + w;
   const int sub = lane / LANES, l4 = lane % LANES;
   const size_t step = (size_t)WARPS * p.plan.cols;
   const float4* src = reinterpret_cast<const float4*>(p.part_o + (slot0 * p.plan.cols + spot.col) * d + blockIdx.y * COLS) + l4;
@@ -1010,8 +1060,15 @@ __global__ void __launch_bounds__(kJoinThreads) saga_tree_join_kernel(const Tree
   float top = kUnset, sum = 0.f;
   float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
   for (int base = 0; base < parts; base += 32) {
+    const int here = min(32, parts - base);
+    float4 x[BATCH];  // the first loads do not wait for the weights
+#pragma unroll
+    for (int k = 0; k < BATCH; ++k) {
+      const int i = k * AT_ONCE + sub;
+      x[k] = i < here ? src[(size_t)(base + i) * step4] : make_float4(0.f, 0.f, 0.f, 0.f);
+    }
     float pm = kUnset, pl = 0.f;
-    if (base + lane < parts) {
+    if (lane < here) {
       pm = p.part_m[slot0 * p.plan.cols + spot.col + (base + lane) * step];
       pl = p.part_l[slot0 * p.plan.cols + spot.col + (base + lane) * step];
     }
@@ -1020,26 +1077,27 @@ __global__ void __launch_bounds__(kJoinThreads) saga_tree_join_kernel(const Tree
     top = now;
     float add = wt * pl;
 #pragma unroll
-    for (int x = 16; x > 0; x >>= 1) add += __shfl_xor_sync(0xffffffffu, add, x);
+    for (int y = 16; y > 0; y >>= 1) add += __shfl_xor_sync(0xffffffffu, add, y);
     sum = sum * f + add;
     o.x *= f, o.y *= f, o.z *= f, o.w *= f;
-    const int here = min(32, parts - base);
     for (int i0 = 0; i0 < here; i0 += AT_ONCE * BATCH) {
-      float4 x[BATCH];
-      float fw[BATCH];
+      if (i0 > 0) {
 #pragma unroll
-      for (int k = 0; k < BATCH; ++k) {
-        const int i = i0 + k * AT_ONCE + sub;
-        fw[k] = __shfl_sync(0xffffffffu, wt, i & 31);
-        if (i >= here) fw[k] = 0.f;
-        x[k] = fw[k] > 0.f ? src[(size_t)(base + i) * step4] : make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int k = 0; k < BATCH; ++k) {
+          const int i = i0 + k * AT_ONCE + sub;
+          x[k] = i < here ? src[(size_t)(base + i) * step4] : make_float4(0.f, 0.f, 0.f, 0.f);
+        }
       }
 #pragma unroll
       for (int k = 0; k < BATCH; ++k) {
-        o.x = fmaf(fw[k], x[k].x, o.x);
-        o.y = fmaf(fw[k], x[k].y, o.y);
-        o.z = fmaf(fw[k], x[k].z, o.z);
-        o.w = fmaf(fw[k], x[k].w, o.w);
+        const int i = i0 + k * AT_ONCE + sub;
+        const float fw = __shfl_sync(0xffffffffu, wt, i & 31);
+        if (i < here && fw > 0.f) {  // a partial without weights may hold anything
+          o.x = fmaf(fw, x[k].x, o.x);
+          o.y = fmaf(fw, x[k].y, o.y);
+          o.z = fmaf(fw, x[k].z, o.z);
+          o.w = fmaf(fw, x[k].w, o.w);
+        }
       }
     }
   }
@@ -1101,7 +1159,7 @@ int validate_tree(const saga_shape* s, int tokens) {
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
 struct TreeSizes {
-  size_t slots, part_m, part_l, total;  // byte offsets; the sums follow the status word
+  size_t slots, part_m, part_l, holders, total;  // byte offsets; the sums follow the status word
 };
 
 TreeSizes tree_sizes(const saga_shape* s, const TreePlan& plan, int ctas) {
@@ -1109,7 +1167,8 @@ TreeSizes tree_sizes(const saga_shape* s, const TreePlan& plan, int ctas) {
   z.slots = (size_t)ctas + (size_t)s->batch * s->h_k * plan.chunks;
   z.part_m = kTreeStatusBytes + z.slots * plan.cols * s->d * 4;
   z.part_l = z.part_m + z.slots * plan.cols * 4;
-  z.total = z.part_l + z.slots * plan.cols * 4;
+  z.holders = z.part_l + z.slots * plan.cols * 4;
+  z.total = z.holders + (size_t)s->batch * s->h_k * plan.chunks * 8;
   return z;
 }
 
@@ -1126,7 +1185,7 @@ size_t saga_tree_workspace_bytes(const saga_shape* s, int tokens) {
   if (validate_tree(s, tokens)) return 0;
   int sms = 0;
   if (api_device_sms(&sms)) return 0;
-  return tree_sizes(s, tree_plan(s->h_q, s->h_k, s->h_v, tokens), sms).total;
+  return tree_sizes(s, tree_plan(s->h_q, s->h_k, s->h_v, tokens), std::min(sms, kTreeMaxCtas)).total;
 }
 
 int saga_tree_attn(const saga_shape* s, int tokens, const void* q, const saga_cache* cache, const int* prefix_lens,
@@ -1146,7 +1205,7 @@ int saga_tree_attn(const saga_shape* s, int tokens, const void* q, const saga_ca
   if (rc) return rc;
   TreeParams p{};
   p.plan = tree_plan(s->h_q, s->h_k, s->h_v, tokens);
-  const TreeSizes z = tree_sizes(s, p.plan, sms);
+  const TreeSizes z = tree_sizes(s, p.plan, std::min(sms, kTreeMaxCtas));
   if (ws_bytes < z.total) return api_fail(SAGA_ERR_WORKSPACE, "workspace has %zu bytes, needs %zu", ws_bytes, z.total);
   const bool e4m3 = cache->format == SAGA_CACHE_E4M3;
   p.smem = tree_smem(p.plan, s->d);
@@ -1169,11 +1228,12 @@ int saga_tree_attn(const saga_shape* s, int tokens, const void* q, const saga_ca
   p.h_k = s->h_k;
   p.h_v = s->h_v;
   p.l_cap = s->l_cap;
-  p.ctas = sms;
+  p.ctas = std::min(sms, kTreeMaxCtas);
   char* base = static_cast<char*>(workspace);
   p.part_o = reinterpret_cast<float*>(base + kTreeStatusBytes);
   p.part_m = reinterpret_cast<float*>(base + z.part_m);
   p.part_l = reinterpret_cast<float*>(base + z.part_l);
+  p.holders = reinterpret_cast<int2*>(base + z.holders);
   CUtensorMap km{}, vm{};
   if (!e4m3) {
     rc = api_rows_map(&km, cache->k, (long long)s->batch * s->h_k * s->l_cap, s->d);

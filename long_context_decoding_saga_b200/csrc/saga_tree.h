@@ -59,12 +59,19 @@ __host__ __device__ inline TreePlan tree_plan(int h_q, int h_k, int h_v, int T) 
 }
 
 // The work is a line of tiles: batch rows in order, in each its `items`
-// (key head, chunk) items in order, in each its tiles.  CTA i of `ctas` takes
-// tiles [i W / ctas, (i + 1) W / ctas) of the W; an item that several CTAs
-// share is joined from their partials.  No more CTAs work than there are
-// tiles, so each of them has one at least.  CTA i's partial of item k lies in
-// slot i + k: along the line one of the two grows from one partial to the
-// next, so no two share a slot.
+// (key head, chunk) items in order, in each its tiles.  It is cut in one of
+// two ways.  Evenly: CTA i takes the i-th of `ctas` runs of tiles whose lengths
+// differ by one at most, wherever items begin and end.  By items: each item of
+// batch row b gets a whole number of CTAs, in proportion to its tiles, so that
+// no CTA has to change items; a change costs about as much as five tiles (Q and
+// the references anew, the sums written out), so this is taken where its
+// longest run is not longer than the even one by more.  No CTA has a run
+// without tiles between two that have some.  CTA i's partial of item k lies in
+// slot i + k: along the line one of the two grows from one partial to the next,
+// so no two share a slot.
+constexpr int kTreeChange = 5;
+constexpr int kTreeMaxCtas = 240;
+
 struct TreeLine {
   const int* prefix;
   const int* counts;  // nullable
@@ -82,30 +89,72 @@ __host__ __device__ inline bool tree_lens(const TreeLine& l, int b, int* P, int*
   return *P == given;
 }
 __host__ __device__ inline int tree_tiles(int prefix, int n) { return n > 0 ? (prefix + n + kTreeTile - 1) / kTreeTile : 0; }
-__host__ __device__ inline int tree_ctas(long long total, int most) { return total < most ? (int)total : most; }
-__host__ __device__ inline long long tree_first_tile(long long total, int ctas, int i) { return (long long)i * total / ctas; }
-// The CTA that tile x of the line belongs to.
-__host__ __device__ inline int tree_cta_of(long long total, int ctas, long long x) { return (int)(((x + 1) * ctas - 1) / total); }
 
-// One segment of a CTA's share of the line: tiles [t0, t1) of item `hc` of
-// batch row b.
+// How the line of `total` tiles is cut into runs for `most` <= kTreeMaxCtas
+// CTAs.  32 bits hold the tiles (cache rows are below 2^31, chunks of a key
+// head at most 64) and the products of an item's tiles with a number of CTAs.
+struct TreeCut {
+  int total, most;
+  bool by_items;
+};
+// CTAs of each item of a batch row of `tiles` tiles; 0: too few CTAs to cut by items.
+__host__ __device__ inline int tree_item_ctas(const TreeCut& c, int tiles) {
+  const int x = (int)((unsigned)c.most * (unsigned)tiles / (unsigned)c.total);
+  return x < tiles ? x : tiles;
+}
+// The longest run of such an item.
+__host__ __device__ inline int tree_longest(int tiles, int ctas) { return (tiles + ctas - 1) / ctas; }
+__host__ __device__ inline int tree_longest_even(const TreeCut& c) { return (c.total + c.most - 1) / c.most; }
+
+// Even runs: the first tile of CTA i, and the CTA of tile x.
+__host__ __device__ inline int tree_even_ctas(const TreeCut& c) { return c.total < c.most ? c.total : c.most; }
+__host__ __device__ inline int tree_even_first(const TreeCut& c, int i) {
+  const int n = tree_even_ctas(c), base = c.total / n, more = c.total - base * n;
+  return i * base + (i < more ? i : more);
+}
+__host__ __device__ inline int tree_even_cta(const TreeCut& c, int x) {
+  const int n = tree_even_ctas(c), base = c.total / n, more = c.total - base * n, longer = more * (base + 1);
+  return x < longer ? x / (base + 1) : more + (x - longer) / base;
+}
+
+// One segment of a CTA's run: tiles [t0, t1) of item `hc` of batch row b.
 struct TreeWalk {
   int b, hc, t0, t1, tiles, P, n;
-  long long left;  // tiles of the share from t0 on
+  int left;  // tiles of the run from t0 on
   int item;
 };
 
-// The first segment of a share of `count` >= 1 tiles whose first is the
-// `place`-th of batch row b's.
-__host__ __device__ inline TreeWalk tree_walk_begin(const TreeLine& l, int b, long long place, long long count) {
+// What a batch row takes of the axis along which runs are found: CTAs (by
+// items) or tiles (even).
+__host__ __device__ inline int tree_extent(const TreeLine& l, const TreeCut& c, int tiles) {
+  return tiles == 0 ? 0 : l.items * (c.by_items ? tree_item_ctas(c, tiles) : tiles);
+}
+// Where CTA i starts on that axis; -1: it has nothing (by items, that shows when no batch row holds it).
+__host__ __device__ inline int tree_start(const TreeCut& c, int i) {
+  if (c.total == 0) return -1;
+  return c.by_items ? i : i < tree_even_ctas(c) ? tree_even_first(c, i) : -1;
+}
+// CTA i's first segment, `place` units into what batch row b takes.
+__host__ __device__ inline TreeWalk tree_walk_begin(const TreeLine& l, const TreeCut& c, int i, int b, int place, int P,
+                                                    int n) {
   TreeWalk w;
-  w.left = count;
   w.b = b;
-  tree_lens(l, b, &w.P, &w.n);
-  w.tiles = tree_tiles(w.P, w.n);
-  w.hc = (int)(place / w.tiles);
-  w.t0 = (int)(place - (long long)w.hc * w.tiles);
-  w.t1 = w.tiles - w.t0 < count ? w.tiles : w.t0 + (int)count;
+  w.P = P;
+  w.n = n;
+  w.tiles = tree_tiles(P, n);
+  if (c.by_items) {
+    const int k = tree_item_ctas(c, w.tiles);
+    w.hc = place / k;
+    const int part = place - w.hc * k;
+    w.t0 = (int)((unsigned)part * (unsigned)w.tiles / (unsigned)k);
+    w.t1 = (int)((unsigned)(part + 1) * (unsigned)w.tiles / (unsigned)k);
+    w.left = w.t1 - w.t0;
+  } else {
+    w.left = tree_even_first(c, i + 1) - tree_even_first(c, i);
+    w.hc = place / w.tiles;
+    w.t0 = place - w.hc * w.tiles;
+    w.t1 = w.tiles - w.t0 < w.left ? w.tiles : w.t0 + w.left;
+  }
   w.item = b * l.items + w.hc;
   return w;
 }
@@ -116,15 +165,22 @@ __host__ __device__ inline bool tree_walk_next(const TreeLine& l, TreeWalk& w) {
   w.t0 = 0;
   if (++w.hc == l.items) {
     w.hc = 0;
-    do {  // ends: tiles of the share are left, so a later batch row has some
+    do {  // ends: tiles of the run are left, so a later batch row has some
       ++w.b;
       tree_lens(l, w.b, &w.P, &w.n);
       w.tiles = tree_tiles(w.P, w.n);
     } while (w.tiles == 0);
   }
-  w.t1 = w.tiles < w.left ? w.tiles : (int)w.left;
+  w.t1 = w.tiles < w.left ? w.tiles : w.left;
   w.item = w.b * l.items + w.hc;
   return true;
+}
+
+// The last CTA of the item whose first tile is CTA i's first segment's (its
+// first CTA: t0 == 0) or begins within CTA i's run.  `place`: the item's first
+// tile on the line, for even runs.
+__host__ __device__ inline int tree_last_holder(const TreeCut& c, int i, int tiles, int place) {
+  return c.by_items ? i + tree_item_ctas(c, tiles) - 1 : tree_even_cta(c, place + tiles - 1);
 }
 
 // The order of a segment's loads: K(t0), then for every t: K(t + 1) if there
@@ -206,7 +262,7 @@ __host__ __device__ inline TreeSmem tree_smem(const TreePlan& p, int d) {
   const int q_bytes = p.cols * d * 2;
   s.p_bytes = p.cols * kTreeTile * 2;
   const int words = p.cols * (8 + 5 * 4);
-  const int bar_bytes = 8 * (3 * kTreeMaxStages + 16) + 16 + (int)sizeof(TreeWalk);
+  const int bar_bytes = 8 * (3 * kTreeMaxStages + 16) + 16 + (int)(sizeof(TreeWalk) + sizeof(TreeCut));
   const int fixed = 2048 + q_bytes + 2 * s.p_bytes + words + bar_bytes;
   s.stages = (budget - fixed) / s.stage_bytes;
   if (s.stages > kTreeMaxStages) s.stages = kTreeMaxStages;

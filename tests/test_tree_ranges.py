@@ -66,49 +66,73 @@ static void plans() {
 }
 
 static void lines() {
+  int by_items = 0;
   std::srand(1);
   for (int round = 0; round < 3000; ++round) {
     const int B = 1 + std::rand() % 40, items = 1 + std::rand() % 9, T = 1 + std::rand() % 64, cap = 64 + std::rand() % 3000;
-    const int most = (round % 3 == 0) ? 148 : 1 + std::rand() % 20, nv = 1 + std::rand() % 5;
+    const int most = (round % 3 == 0) ? 148 : (round % 3 == 1) ? 600 : 1 + std::rand() % 20, nv = 1 + std::rand() % 5;
     std::vector<int> prefix(B), counts(B);
     for (int b = 0; b < B; ++b) {
       prefix[b] = std::rand() % 5 == 0 ? 0 : std::rand() % (cap + 50) - 20;
       counts[b] = std::rand() % 4 == 0 ? 0 : std::rand() % (T + 3) - 1;
     }
     const TreeLine line{prefix.data(), round % 2 ? counts.data() : nullptr, T, cap, items};
-    long long total = 0;
-    std::vector<long long> before(B);
+    TreeCut cut{0, most, false};
     for (int b = 0; b < B; ++b) {
       int P, n;
       tree_lens(line, b, &P, &n);
       CHECK(P >= 0 && n >= 0 && P + n <= cap, "lens");
-      before[b] = total;
-      total += (long long)items * tree_tiles(P, n);
+      cut.total += items * tree_tiles(P, n);
     }
-    const int ctas = tree_ctas(total, most);
-    long long x = 0;
+    bool can = cut.total > 0;
+    int longest = 0;
+    for (int b = 0; b < B; ++b) {
+      int P, n;
+      tree_lens(line, b, &P, &n);
+      const int tiles = tree_tiles(P, n);
+      if (tiles == 0) continue;
+      const int k = tree_item_ctas(cut, tiles);
+      can = can && k > 0;
+      if (k > 0 && tree_longest(tiles, k) > longest) longest = tree_longest(tiles, k);
+    }
+    cut.by_items = can && (round % 4 < 2);
+    by_items += cut.by_items;
+    std::vector<int> before(B + 1, 0), tiles_before(B + 1, 0);
+    for (int b = 0; b < B; ++b) {
+      int P, n;
+      tree_lens(line, b, &P, &n);
+      before[b + 1] = before[b] + tree_extent(line, cut, tree_tiles(P, n));
+      tiles_before[b + 1] = tiles_before[b] + items * tree_tiles(P, n);
+    }
+    CHECK(!cut.by_items || before[B] <= most, "by items: %d CTAs of %d", before[B], most);
+    int x = 0, longest_seen = 0;
     std::set<long long> slots;
     std::map<int, std::pair<int, int>> held;  // item -> first and last CTA
-    for (int i = 0; i < ctas; ++i) {
-      const long long first = tree_first_tile(total, ctas, i), count = tree_first_tile(total, ctas, i + 1) - first;
-      CHECK(first == x && count >= 1, "share of CTA %d", i);
+    std::map<int, int> told;                   // item -> what its first CTA says is its last
+    for (int i = 0; i < most; ++i) {
+      const int at = tree_start(cut, i);
+      if (at < 0 || at >= before[B]) continue;
       int b = 0;
-      while (b + 1 < B && before[b + 1] <= first) ++b;
-      { int P, n; tree_lens(line, b, &P, &n); while (tree_tiles(P, n) == 0) { --b; tree_lens(line, b, &P, &n); } }
-      TreeWalk w = tree_walk_begin(line, b, first - before[b], count);
+      while (before[b + 1] <= at) ++b;
+      int P, n;
+      tree_lens(line, b, &P, &n);
+      TreeWalk w = tree_walk_begin(line, cut, i, b, at - before[b], P, n);
+      CHECK(w.left >= 1, "empty run");
+      if (w.left > longest_seen) longest_seen = w.left;
       bool more = true;
       while (more) {
-        CHECK(w.t0 < w.t1 && w.t1 <= w.tiles && w.hc < items, "segment");
+        CHECK(w.t0 < w.t1 && w.t1 <= w.tiles && w.hc < items && w.t1 - w.t0 <= w.left, "segment");
         CHECK(w.item == w.b * items + w.hc, "item");
         CHECK(slots.insert((long long)i + w.item).second, "slot used twice");
-        CHECK(i + w.item < ctas + (long long)B * items, "slot out of range");
-        if (!held.count(w.item)) held[w.item] = {i, i};
+        CHECK(i + w.item < most + (long long)B * items, "slot out of range");
+        if (!held.count(w.item)) held[w.item] = std::make_pair(i, i);
         CHECK(held[w.item].second >= i - 1, "a CTA between has no partial");
         held[w.item].second = i;
-        for (int t = w.t0; t < w.t1; ++t, ++x) {
-          CHECK(x == before[w.b] + (long long)w.hc * w.tiles + t, "tile order");
-          CHECK(tree_cta_of(total, ctas, x) == i, "CTA of tile");
-        }
+        if (w.t0 == 0) told[w.item] = tree_last_holder(cut, i, w.tiles, tiles_before[w.b] + w.hc * w.tiles);
+        CHECK(told.count(w.item) == 1, "an item's first tile comes first");
+        CHECK(w.t1 == w.tiles ? told[w.item] == i : told[w.item] > i, "last holder %d, CTA %d", told[w.item], i);
+        for (int t = w.t0; t < w.t1; ++t, ++x)
+          CHECK(x == tiles_before[w.b] + w.hc * w.tiles + t, "tile order");
         // the feed: K(t0), then K(t + 1), V(t, ...)
         std::vector<std::pair<int, int>> want, got;
         want.push_back({w.t0, -1});
@@ -123,8 +147,11 @@ static void lines() {
         more = tree_walk_next(line, w);
       }
     }
-    CHECK(x == total, "tiles covered %lld of %lld", x, total);
+    CHECK(x == cut.total, "tiles covered %d of %d", x, cut.total);
+    if (cut.by_items) CHECK(longest_seen == longest, "longest run");
+    else CHECK(cut.total == 0 || longest_seen == tree_longest_even(cut), "longest even run");
   }
+  CHECK(by_items > 100, "few lines cut by items: %d", by_items);
 }
 
 int main() {
