@@ -397,16 +397,17 @@ int api_ok() { return ok(); }
 int api_cuda_fail(cudaError_t e, const char* what) { return cuda_fail(e, what); }
 int api_validate_shape(const saga_shape* s) { return validate_shape(s); }
 int api_device_sms(int* sms) { return device_sms(sms); }
-int api_rows_map(CUtensorMap* m, const void* base, long long rows, int d) {
+int api_rows_map(CUtensorMap* m, const void* base, long long rows, int d, bool e4m3) {
   EncodeTiledFn enc = get_encode();
   if (enc == nullptr) return fail(SAGA_ERR_CUDA, "cuTensorMapEncodeTiled unavailable from the driver");
   cuuint64_t dims[2] = {(cuuint64_t)d, (cuuint64_t)rows};
-  cuuint64_t strides[1] = {(cuuint64_t)d * 2};
-  cuuint32_t box[2] = {64u, (cuuint32_t)kTreeTile};
+  cuuint64_t strides[1] = {(cuuint64_t)d * (e4m3 ? 1 : 2)};
+  cuuint32_t box[2] = {(cuuint32_t)(e4m3 ? d : 64), (cuuint32_t)kTreeTile};
   cuuint32_t estr[2] = {1u, 1u};
-  CUresult r = enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(base), dims, strides, box, estr,
-                   CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  CUresult r = enc(m, e4m3 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2,
+                   const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                   e4m3 && d == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B,
+                   CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   if (r != CUDA_SUCCESS) return fail(SAGA_ERR_CUDA, "cuTensorMapEncodeTiled (rows) failed (%d)", (int)r);
   return SAGA_OK;
 }

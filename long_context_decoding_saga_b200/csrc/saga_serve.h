@@ -19,9 +19,10 @@ int api_ok();
 int api_cuda_fail(cudaError_t e, const char* what);
 int api_validate_shape(const saga_shape* s);
 int api_device_sms(int* sms);
-// Tensor map over `rows` rows of d bf16 elements: boxes of 64 columns (one
-// 128-byte swizzle row) by kTreeTile rows.
-int api_rows_map(CUtensorMap* m, const void* base, long long rows, int d);
+// Tensor map over `rows` cache rows of d elements, kTreeTile rows a box: 64
+// columns of bf16 (one 128-byte swizzle row), or the whole row of e4m3 codes
+// (swizzled in its own 64 or 128 bytes).
+int api_rows_map(CUtensorMap* m, const void* base, long long rows, int d, bool e4m3);
 
 // A quantised row: value = code * scale with scale = amax / kE4m3Max over the
 // row's d elements.  Rows whose largest magnitude is below kAmaxFloor use it

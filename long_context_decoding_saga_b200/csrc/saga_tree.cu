@@ -13,19 +13,25 @@
 // transposed operand, so nothing is transposed.
 //
 // P = 2^(x - m) with x the score in powers of two and m a reference per column.
-// The softmax needs no exact maximum: any m within the range of bf16's exponent
-// gives the same quotient.  So m is taken from the first tile's maximum and
-// moved only when a score rises 2^32 above it, which one comparison per score
-// and one vote per tile watch for; then the accumulators are rescaled and the
-// tile is done again.  The weights are rounded to bf16, and what they are
-// divided by is the sum of the rounded weights: a row of ones beside V in the
-// second product adds them up in fp32.
+// The softmax needs no exact maximum: any m within the range of the weights'
+// exponents gives the same quotient.  So m comes from the first tile and is
+// moved only when a score rises too far above it, which one comparison per
+// score and one vote per tile watch for; then the accumulators are rescaled and
+// the tile is done again.
 //
-// 8-bit caches: codes are widened on their way into the same tile ring.  Keys
-// become half precision, exactly, and a key row's scale multiplies its scores
-// in fp32 (q goes to half precision scaled by a power of two, exact for all
-// that matters of bf16).  Values are multiplied by their row's scale in fp32
-// and rounded to bf16, which is finer than their own 4 bits.
+// bf16 caches: weights are rounded to bf16, and what they are divided by is the
+// sum of the rounded weights: a row of ones beside V in the second product adds
+// them up in fp32.
+//
+// 8-bit caches: the codes go to the tensor cores as they are (kind::f8f6f4), so
+// a tile is read once, by TMA, and nothing is widened.  The other operands are
+// given in pieces whose products add up in the same accumulators: q, scaled by
+// a power of two, as the sum of two e4m3 numbers (4 + 4 of bf16's 8 bits,
+// exact for all elements but those 2^-14 below the row's largest); the weights
+// as an e5m2 number and what it leaves as e4m3 (off by 2^-7 at most, finer than
+// the values' own 2^-4).  A key row's scale multiplies its scores and a value
+// row's scale its weights, both in fp32 and before any rounding; the sums of
+// weights are fp32 sums of the unrounded ones.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>
@@ -42,12 +48,14 @@ namespace {
 
 constexpr float kUnset = -1e37f;      // a column's reference before any kept score
 constexpr float kLog2e = 1.4426950408889634f;
-constexpr float kOver = 32.f;         // a score this far (in powers of two) above its reference moves the reference
-constexpr int kEpiWarp0 = 4, kConvWarp0 = 12, kConvWarps = 8;
-constexpr int kEpiAll = 256;
-
-template <bool E4M3>
-constexpr int kTreeThreads = E4M3 ? (kConvWarp0 + kConvWarps) * 32 : kConvWarp0 * 32;
+constexpr int kEpiWarp0 = 4, kEpiAll = 256, kTreeThreads = kEpiWarp0 * 32 + kEpiAll;
+// How far (in powers of two) a weight may rise above its column's reference:
+// bf16 has fp32's exponents; e5m2 ends below 2^16.
+constexpr float kOverBf16 = 32.f, kOverE5m2 = 15.f;
+// Where the first tile's largest weight is put: e5m2's smallest numbers are
+// 2^-16, so rows down to 2^-26 of the largest still count.
+constexpr float kTopE5m2 = 10.f;
+constexpr float kMinScale = 8.271806125530277e-25f;  // 2^-80: smaller value scales do not lower the reference
 
 // ------------------------------------------------------------------ the line of tiles
 __device__ __forceinline__ TreeLine line_of(const TreeParams& p) {
@@ -123,23 +131,43 @@ __device__ __forceinline__ bool row_seen(const TreeWalk& w, unsigned long long s
 }
 
 // ------------------------------------------------------------------ tcgen05 pieces beyond saga_device.cuh
-// Matrix descriptors.  V tile: 128-byte swizzle, the product's M (d) dense:
-// 64-element blocks `block` bytes apart, 8-row groups 1024 bytes apart.  For
-// d = 64 the second block of the M = 128 product is the ones.
+// Shared-memory matrix descriptors (addresses, distances in bytes).
+__device__ __forceinline__ uint64_t smem_desc(uint32_t addr, uint32_t lead, uint32_t stride, uint32_t layout) {
+  return (uint64_t)((addr >> 4) & 0x3FFFu) | ((uint64_t)(lead >> 4) << 16) | ((uint64_t)(stride >> 4) << 32) |
+         ((uint64_t)1u << 46) | ((uint64_t)layout << 61);
+}
+constexpr uint32_t kLayoutPlain = 0, kLayout128 = 2, kLayout64 = 4;
+// K tile and Q: rows of the inner dimension, 8-row groups 8 rows apart.
+template <int D, bool E4M3>
+__device__ __forceinline__ uint64_t desc_rows(uint32_t addr) {
+  return E4M3 && D == 64 ? smem_desc(addr, 16, 512, kLayout64) : smem_desc(addr, 16, 1024, kLayout128);
+}
+// V tile: the product's M (d) dense, 8-row groups of the inner dimension one
+// after the other.  bf16: 64-element blocks `block` bytes apart; for d = 64 the
+// second block of the M = 128 product is the ones.
+template <int D, bool E4M3>
 __device__ __forceinline__ uint64_t desc_v(uint32_t addr, uint32_t block) {
-  return (uint64_t)((addr >> 4) & 0x3FFFu) | ((uint64_t)(block >> 4) << 16) | ((uint64_t)(1024u >> 4) << 32) |
-         ((uint64_t)1u << 46) | ((uint64_t)2u << 61);
+  return E4M3 && D == 64 ? smem_desc(addr, block, 512, kLayout64) : smem_desc(addr, block, 1024, kLayout128);
 }
-// P: no swizzle, N (columns) dense in 16-byte groups of 8; the 8 x 8 blocks of
-// a column group lie 128 bytes apart along the rows, column groups 2048 bytes.
-__device__ __forceinline__ uint64_t desc_p(uint32_t addr) {
-  return (uint64_t)((addr >> 4) & 0x3FFFu) | ((uint64_t)(128u >> 4) << 16) | ((uint64_t)(2048u >> 4) << 32) |
-         ((uint64_t)1u << 46);
+// P: N (columns) dense in 16-byte groups; the 8-row blocks of a column group
+// lie 128 bytes apart, column groups 2048 bytes.
+__device__ __forceinline__ uint64_t desc_p(uint32_t addr) { return smem_desc(addr, 128, 2048, kLayoutPlain); }
+
+// Instruction descriptor: fp32 sums; a, b: operand formats of the kind.
+__host__ __device__ constexpr uint32_t idesc(uint32_t a, uint32_t b, int M, int N, bool transposed) {
+  return (1u << 4) | (a << 7) | (b << 10) | (transposed ? 3u << 15 : 0u) | ((uint32_t)(N >> 3) << 17) |
+         ((uint32_t)(M >> 4) << 24);
 }
-// Instruction descriptor: fp32 sums of bf16 (1) or half (0) operands.
-__host__ __device__ constexpr uint32_t idesc16(bool half, int M, int N, bool transposed) {
-  return (1u << 4) | ((half ? 0u : 1u) << 7) | ((half ? 0u : 1u) << 10) | (transposed ? 3u << 15 : 0u) |
-         ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
+constexpr uint32_t kBf16 = 1;            // kind::f16
+constexpr uint32_t kE4m3 = 0, kE5m2 = 1; // kind::f8f6f4
+
+__device__ __forceinline__ void umma_8bit(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t id, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "l"(adesc), "l"(bdesc), "r"(id), "r"(accumulate)
+      : "memory");
 }
 
 // 8 columns of this thread's lane: the load, and the wait after which they may be read.
@@ -183,13 +211,23 @@ __device__ __forceinline__ float ex2(float x) {
   return y;
 }
 
-__device__ __forceinline__ uint32_t pack_half(float a, float b) {
-  const __half2 h = __floats2half2_rn(a, b);
-  return reinterpret_cast<const uint32_t&>(h);
+// Two numbers as an 8-bit format each, in the low 16 bits, and back.
+__device__ __forceinline__ uint32_t pack_8bit(float a, float b, __nv_fp8_interpretation_t f) {
+  return __nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, f);
+}
+__device__ __forceinline__ float2 unpack_8bit(uint32_t x, __nv_fp8_interpretation_t f) {
+  const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)x, f);
+  return __half22float2(__half2(h));
 }
 __device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
   const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
   return reinterpret_cast<const uint32_t&>(h);
+}
+
+__device__ __forceinline__ void cp_async4_zfill(void* smem_dst, const void* gsrc, bool valid) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(smem_u32(smem_dst)),
+               "l"(reinterpret_cast<uint64_t>(gsrc)), "r"(valid ? 4 : 0)
+               : "memory");
 }
 
 // A position in the tile ring.
@@ -216,21 +254,17 @@ struct Bars {
   uint64_t *q_full, *drain;
 };
 
-// Words for exchanging a column group's values between the four warps of its
-// warpgroup: the group's part of a P buffer while that holds no weights.
-__device__ __forceinline__ float* column_words(uint8_t* p_buf, int col) {
-  return reinterpret_cast<float*>(p_buf + (col >> 3) * 2048);
-}
-
 // The column groups (8 live columns or fewer, the rest padding) of a
 // warpgroup: `count` of them from `col` on, `groups` to a value head of `nvp`
-// columns, the first of them the `at`-th of its value head.
+// columns, the first of them the `at`-th of its value head; v counts the value
+// heads from the warpgroup's first on.
 struct Groups {
-  int col, at, count, groups, nvp;
+  int col, at, v, count, groups, nvp;
   __device__ __forceinline__ void step() {
     col += 8;
     if (++at == groups) {
       at = 0;
+      ++v;
       col += nvp - groups * 8;
     }
   }
@@ -240,9 +274,16 @@ struct Groups {
 struct Row {
   float f;                 // score factor, without the columns'
   bool all;                // every column sees the row
+  bool live;               // some column does
   unsigned long long bit;  // else the drafted token in it (0: none)
+  const float* scale;      // 8-bit: value scales of the row, the v-th kTreeTile words on
 };
 
+// The columns' words.
+struct Columns {
+  float *m, *tau, *cs;
+  unsigned long long* mask;
+};
 
 __device__ __forceinline__ void load8(const float* from, float* to) {
   *reinterpret_cast<float4*>(to) = *reinterpret_cast<const float4*>(from);
@@ -253,18 +294,17 @@ __device__ __forceinline__ void load8(const float* from, float* to) {
 // RELATIVE; with TEST -inf where the row is hidden or the score below the
 // threshold (a row of the prefix is hidden from nobody: no masks are read).
 template <bool E4M3, bool TEST, bool RELATIVE>
-__device__ __forceinline__ void exponents(float* s, const Row& r, int col, const float* m, const float* tau,
-                                          const float* cs, const unsigned long long* mask) {
+__device__ __forceinline__ void exponents(float* s, const Row& r, int col, const Columns& c) {
   float mm[8], cc[8], tt[8];
-  if (RELATIVE) load8(m + col, mm);
-  if (E4M3) load8(cs + col, cc);
-  if (TEST) load8(tau + col, tt);
+  if (RELATIVE) load8(c.m + col, mm);
+  if (E4M3) load8(c.cs + col, cc);
+  if (TEST) load8(c.tau + col, tt);
   unsigned seen = 0xffu;
   if (TEST && !r.all) {
     seen = 0u;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const ulonglong2 x = *reinterpret_cast<const ulonglong2*>(mask + col + 2 * i);
+      const ulonglong2 x = *reinterpret_cast<const ulonglong2*>(c.mask + col + 2 * i);
       if ((x.x & r.bit) != 0ull) seen |= 1u << (2 * i);
       if ((x.y & r.bit) != 0ull) seen |= 2u << (2 * i);
     }
@@ -282,10 +322,35 @@ __device__ __forceinline__ void exponents(float* s, const Row& r, int col, const
   }
 }
 
+// 8 columns' sums over the 32 lanes; lane 4 c holds column octet_column(lane).
+__device__ __forceinline__ int octet_column(int lane) { return (lane >> 4 & 1) * 4 + (lane >> 3 & 1) * 2 + (lane >> 2 & 1); }
+__device__ __forceinline__ float octet_sum(const float* v, int lane) {
+  float a[4], b[2], c;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float mine = lane & 16 ? v[4 + i] : v[i], other = lane & 16 ? v[i] : v[4 + i];
+    a[i] = mine + __shfl_xor_sync(0xffffffffu, other, 16);
+  }
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const float mine = lane & 8 ? a[2 + i] : a[i], other = lane & 8 ? a[i] : a[2 + i];
+    b[i] = mine + __shfl_xor_sync(0xffffffffu, other, 8);
+  }
+  {
+    const float mine = lane & 4 ? b[1] : b[0], other = lane & 4 ? b[0] : b[1];
+    c = mine + __shfl_xor_sync(0xffffffffu, other, 4);
+  }
+  c += __shfl_xor_sync(0xffffffffu, c, 2);
+  c += __shfl_xor_sync(0xffffffffu, c, 1);
+  return c;
+}
+
 // Weights of a tile into P; returns the largest exponent of the thread's.
+// bf16: a row of P is 16 bytes per 8 columns.  8-bit: 8 bytes per 8 columns of
+// each piece, the second piece `piece` bytes on.
 template <bool E4M3, bool TEST>
-__device__ __forceinline__ float weigh(uint32_t s_tmem, uint8_t* p_row, Groups g, const Row& r, const float* m,
-                                       const float* tau, const float* cs, const unsigned long long* mask) {
+__device__ __forceinline__ float weigh(uint32_t s_tmem, uint8_t* p_row, int piece, Groups g, const Row& r,
+                                       const Columns& c) {
   float top = -INFINITY;
   uint32_t raw[8];
   if (g.count > 0) tmem_ld8_start(s_tmem + g.col, raw);
@@ -294,211 +359,83 @@ __device__ __forceinline__ float weigh(uint32_t s_tmem, uint8_t* p_row, Groups g
     float s[8];
     tmem_ld8_end(raw, s);
     const int col = g.col;
+    const float vs = E4M3 && r.live ? r.scale[g.v * kTreeTile] : 0.f;
     g.step();
     if (n > 1) tmem_ld8_start(s_tmem + g.col, raw);  // the next group's scores, while this one's are weighed
-    exponents<E4M3, TEST, true>(s, r, col, m, tau, cs, mask);
-    uint32_t w[4];
+    exponents<E4M3, TEST, true>(s, r, col, c);
+    if (!E4M3) {
+      uint32_t w[4];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      top = fmaxf(top, s[i]);
-      s[i] = ex2(s[i]);
+      for (int i = 0; i < 8; ++i) {
+        top = fmaxf(top, s[i]);
+        s[i] = ex2(s[i]);
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) w[i] = pack_bf16(s[2 * i], s[2 * i + 1]);
+      *reinterpret_cast<uint4*>(p_row + (col >> 3) * 2048) = make_uint4(w[0], w[1], w[2], w[3]);
+    } else {
+      float most = s[0];
+#pragma unroll
+      for (int i = 1; i < 8; ++i) most = fmaxf(most, s[i]);
+      top = fmaxf(top, most + __log2f(fmaxf(vs, kMinScale)));
+      uint32_t w[4], z[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float a = ex2(s[2 * i]) * vs, b = ex2(s[2 * i + 1]) * vs;
+        w[i] = pack_8bit(a, b, __NV_E5M2);
+        const float2 had = unpack_8bit(w[i], __NV_E5M2);
+        z[i] = pack_8bit(a - had.x, b - had.y, __NV_E4M3);
+      }
+      uint8_t* at = p_row + (col >> 4) * 2048 + (col & 8);
+      *reinterpret_cast<uint2*>(at) = make_uint2(w[0] | w[1] << 16, w[2] | w[3] << 16);
+      *reinterpret_cast<uint2*>(at + piece) = make_uint2(z[0] | z[1] << 16, z[2] | z[3] << 16);
     }
-#pragma unroll
-    for (int i = 0; i < 4; ++i) w[i] = pack_bf16(s[2 * i], s[2 * i + 1]);
-    *reinterpret_cast<uint4*>(p_row + (col >> 3) * 2048) = make_uint4(w[0], w[1], w[2], w[3]);
   }
   return top;
 }
 
-// The columns' largest scores over the warp's rows, into the column words.
-template <bool E4M3, bool TEST>
-__device__ __forceinline__ void maxima(uint32_t s_tmem, uint8_t* p_buf, Groups g, const Row& r, const float* m,
-                                       const float* tau, const float* cs, const unsigned long long* mask) {
+// 8-bit: the weights' sums over the warp's rows, added to the warp's sums.
+template <bool TEST>
+__device__ __forceinline__ void add_weights(uint32_t s_tmem, float* sums, Groups g, const Row& r, const Columns& c) {
+  const int lane = lane_id();
 #pragma unroll 1
   for (int n = g.count; n > 0; --n, g.step()) {
     float s[8];
     tmem_ld8(s_tmem + g.col, s);
-    exponents<E4M3, TEST, false>(s, r, g.col, m, tau, cs, mask);
-    float* words = column_words(p_buf, g.col) + (threadIdx.x >> 5 & 3) * 8;
+    exponents<true, TEST, true>(s, r, g.col, c);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) s[i] = ex2(s[i]);
+    const float x = octet_sum(s, lane);
+    if ((lane & 3) == 0) sums[g.col + octet_column(lane)] += x;
+  }
+}
+
+// The columns' largest weights over the warp's rows, in powers of two, into
+// the column's word of this warp.
+template <bool E4M3>
+__device__ __forceinline__ void maxima(uint32_t s_tmem, float* words, Groups g, const Row& r, const Columns& c) {
+#pragma unroll 1
+  for (int n = g.count; n > 0; --n, g.step()) {
+    float s[8];
+    tmem_ld8(s_tmem + g.col, s);
+    exponents<E4M3, true, false>(s, r, g.col, c);
+    const float lv = E4M3 ? __log2f(fmaxf(r.scale[g.v * kTreeTile], kMinScale)) : 0.f;
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      const uint32_t k = __reduce_max_sync(0xffffffffu, float_key(s[i]));
-      if (lane_id() == 0) words[i] = key_float(k);
+      const uint32_t k = __reduce_max_sync(0xffffffffu, float_key(s[i] + lv));
+      if (lane_id() == 0) words[(g.col + i) * 4 + (threadIdx.x >> 5 & 3)] = key_float(k);
     }
-  }
-}
-
-// ------------------------------------------------------------------ 8-bit tiles into the ring
-// The loads of a CTA's share in ring order, with where each comes from.
-template <int D>
-struct Feed {
-  TreeWalk w;
-  TreeFeed at;
-  Heads h;
-  unsigned long long seen;
-  bool live;
-  __device__ __forceinline__ void segment(const TreeParams& p) {
-    h = heads_of(p, w);
-    at = tree_feed(w);
-    seen = w.t1 * kTreeTile > w.P ? seen_by_any(p, w) : 0ull;
-  }
-  __device__ __forceinline__ void next(const TreeParams& p) {
-    if (tree_feed_next(w, h.nv, at)) return;
-    live = tree_walk_next(line_of(p), w);
-    if (live) segment(p);
-  }
-  __device__ __forceinline__ size_t row(const TreeParams& p) const {  // the tile's first, of the cache array
-    return (at.v < 0 ? h.key : h.value + (size_t)at.v * p.l_cap) + (size_t)at.t * kTreeTile;
-  }
-  __device__ __forceinline__ const uint8_t* base(const TreeParams& p) const {
-    return static_cast<const uint8_t*>(at.v < 0 ? p.k : p.v) + row(p) * D;
-  }
-  __device__ __forceinline__ const float* scales(const TreeParams& p) const {
-    return (at.v < 0 ? p.k_scale : p.v_scale) + row(p);
-  }
-  __device__ __forceinline__ int rows() const {  // rows of the tile that hold anything
-    return min(kTreeTile, w.P + w.n - at.t * kTreeTile);
-  }
-};
-
-__device__ __forceinline__ float2 mul2(float2 a, float b) {
-  unsigned long long x, y, z;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(x) : "f"(a.x), "f"(a.y));
-  asm("mov.b64 %0, {%1, %1};" : "=l"(y) : "f"(b));
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(z) : "l"(x), "l"(y));
-  asm("mov.b64 {%0, %1}, %2;" : "=f"(a.x), "=f"(a.y) : "l"(z));
-  return a;
-}
-
-// 16 codes as half precision (keys: exact), or times the row's scale as bf16.
-__device__ __forceinline__ void widen16(const uint4& u, bool value, float scale, uint4* a, uint4* b) {
-  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-  uint32_t y[8];
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(w[i >> 1] >> (16 * (i & 1))), __NV_E4M3);
-    y[i] = reinterpret_cast<const uint32_t&>(h);
-  }
-  if (value) {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      float2 f = __half22float2(reinterpret_cast<const __half2&>(y[i]));
-      f = mul2(f, scale);
-      y[i] = pack_bf16(f.x, f.y);
-    }
-  }
-  *a = make_uint4(y[0], y[1], y[2], y[3]);
-  *b = make_uint4(y[4], y[5], y[6], y[7]);
-}
-
-// Two groups of 128 threads take the tiles in turn: 16-byte pieces of the
-// codes are loaded into registers as soon as the group's last tile is out of
-// them, widened, and stored in the 128-byte swizzle that the products read.
-// Rows that no token sees become zeros.  Another warp asks L2 for the tiles
-// further on: `progress` tells it how many tiles the first group has done.
-constexpr int kFeedAhead = 8;
-
-template <int D>
-__device__ void prefetch_tiles(const TreeParams& p, const TreeWalk& w0, volatile int* progress, volatile int* abort_flag) {
-  Feed<D> f;
-  f.w = w0;
-  f.live = true;
-  f.segment(p);
-  const int lane = lane_id();
-  int asked = 0;
-  while (f.live) {
-    const unsigned long long t0 = global_ns();
-    while (asked >= 2 * *progress + kFeedAhead) {  // ends: the first group goes on, or gives up and sets the flag
-      if (*abort_flag != 0 || global_ns() - t0 > kWaitLimitNs) return;
-      __nanosleep(100);
-    }
-    const int rows = f.rows();
-    if (lane == 0) prefetch_l2_bulk(f.base(p), (uint32_t)rows * D);
-    if (lane * 32 < rows) prefetch_l2_line(f.scales(p) + lane * 32);
-    f.next(p);
-    ++asked;
-  }
-}
-
-template <int D>
-__device__ void widen_tiles(const TreeParams& p, const TreeWalk& w0, uint8_t* smem, const Bars& bar,
-                            volatile int* progress, volatile int* abort_flag) {
-  constexpr int CPR = D / 16;                  // pieces per row
-  constexpr int PER = kTreeTile * CPR / 128;   // pieces per thread
-  constexpr int RSTEP = 128 / CPR;             // rows between a thread's pieces
-  const int group = (threadIdx.x - kConvWarp0 * 32) >> 7;
-  const int tid = threadIdx.x & 127, lane = threadIdx.x & 31;
-  const int c = tid % CPR, r0 = tid / CPR;
-  const TreeSmem& L = p.smem;
-  Feed<D> f;
-  f.w = w0;
-  f.live = true;
-  f.segment(p);
-  uint4 x[PER];
-  float sc[PER];
-  auto fetch = [&]() {
-    const uint8_t* src = f.base(p) + (size_t)r0 * D + c * 16;
-    const float* scale = f.scales(p) + r0;
-    const int row0 = f.at.t * kTreeTile + r0;
-    const bool value = f.at.v >= 0;
-    if ((f.at.t + 1) * kTreeTile <= f.w.P) {
-#pragma unroll
-      for (int i = 0; i < PER; ++i) {
-        x[i] = __ldg(reinterpret_cast<const uint4*>(src + (size_t)i * RSTEP * D));
-        if (value) sc[i] = __ldg(scale + i * RSTEP);
-      }
-    } else {
-#pragma unroll
-      for (int i = 0; i < PER; ++i) {
-        const bool there = row_seen(f.w, f.seen, row0 + i * RSTEP);
-        x[i] = there ? __ldg(reinterpret_cast<const uint4*>(src + (size_t)i * RSTEP * D)) : make_uint4(0u, 0u, 0u, 0u);
-        sc[i] = there && value ? __ldg(scale + i * RSTEP) : 0.f;
-      }
-    }
-  };
-  Ring r;
-  if (group == 1) {
-    f.next(p);  // a run has a key tile and a value tile at least
-    r.step(L.stages);
-  }
-  fetch();
-  while (true) {
-    const bool ok = r.round == 0 || mbar_wait(&bar.empty[r.st], (r.round - 1) & 1, abort_flag);
-    if (!__all_sync(0xffffffffu, ok)) break;
-    uint8_t* dst = smem + r.st * L.stage_bytes + ((c * 16) >> 6) * (kTreeTile * 128);
-    const int j = (c & 3) * 2, flip = c >> 2;  // the two halves of a row start with different chunks: other banks
-    const bool value = f.at.v >= 0;
-#pragma unroll
-    for (int i = 0; i < PER; ++i) {
-      uint4 a, b;
-      widen16(x[i], value, sc[i], &a, &b);
-      const int row = r0 + i * RSTEP;
-      uint8_t* at = dst + row * 128;
-      *reinterpret_cast<uint4*>(at + (((j + flip) ^ (row & 7)) << 4)) = flip ? b : a;
-      *reinterpret_cast<uint4*>(at + (((j + 1 - flip) ^ (row & 7)) << 4)) = flip ? a : b;
-    }
-    f.next(p);
-    if (f.live) f.next(p);
-    if (f.live) fetch();
-    fence_proxy_async_shared();
-    __syncwarp();
-    if (lane == 0) mbar_arrive(&bar.full[r.st]);
-    if (group == 0 && tid == 0) *progress = *progress + 1;
-    r.step(L.stages);
-    r.step(L.stages);
-    if (!f.live) break;
   }
 }
 
 // ------------------------------------------------------------------ the kernel
-// Warp 0: TMA loads of the tiles (bf16 caches).  Warp 1: the products, issued
-// by one lane.  Warps 4 .. 11: two warpgroups, each half of the column groups
-// of every tile.  Warps 12 .. 19: widening of 8-bit tiles into the ring.
+// Warp 0: TMA loads of the tiles.  Warp 1: the products, issued by one lane.
+// Warps 4 .. 11: two warpgroups, each half of the column groups of every tile.
 // Ring order: K of tile 0, then for each tile K of the next one and its own
 // value heads, so that the next tile's scores are there while a tile's weights
 // are computed.
 template <int D, bool E4M3>
-__global__ void __launch_bounds__(kTreeThreads<E4M3>, 1)
+__global__ void __launch_bounds__(kTreeThreads, 1)
     saga_tree_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
                      const TreeParams p) {
   extern __shared__ uint8_t smem_raw[];
@@ -518,19 +455,17 @@ __global__ void __launch_bounds__(kTreeThreads<E4M3>, 1)
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   TreeWalk* share = reinterpret_cast<TreeWalk*>(tmem_slot + 2);  // left == 0: this CTA has no tiles
   TreeCut* share_cut = reinterpret_cast<TreeCut*>(share + 1);
-  volatile int* progress = reinterpret_cast<volatile int*>(share_cut + 1);
   const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   const int stages = L.stages;
   const int cols = p.plan.cols;
-  // two score buffers, the accumulators, and the sums of weights (d = 64: lanes 64 .. 127 of the accumulators)
-  const int used = (D == 64 ? 3 : 4) * cols;
+  // two score buffers, the accumulators, and bf16 weights' sums (d = 64: lanes 64 .. 127 of the accumulators)
+  const int used = (D == 64 || E4M3 ? 3 : 4) * cols;
   const uint32_t tmem_cols = used <= 64 ? 64u : used <= 128 ? 128u : used <= 256 ? 256u : 512u;
 
   if (threadIdx.x == 0) {
     *abort_flag = 0;
-    *progress = 0;
     for (int i = 0; i < stages; ++i) {
-      mbar_init(&bar.full[i], E4M3 ? kConvWarps / 2 : 1);
+      mbar_init(&bar.full[i], 1);
       mbar_init(&bar.empty[i], 1);
       mbar_init(&bar.vfix[i], 4);
     }
@@ -543,10 +478,8 @@ __global__ void __launch_bounds__(kTreeThreads<E4M3>, 1)
     mbar_init(bar.q_full, 8);
     mbar_init(bar.drain, 32);
     mbar_init_fence();
-    if (!E4M3) {
-      tma_prefetch_desc(&kmap);
-      tma_prefetch_desc(&vmap);
-    }
+    tma_prefetch_desc(&kmap);
+    tma_prefetch_desc(&vmap);
   }
   if (warp == 1) {
     tmem_alloc(tmem_slot, tmem_cols);
@@ -605,7 +538,7 @@ __global__ void __launch_bounds__(kTreeThreads<E4M3>, 1)
   TreeWalk w = *share;
   const bool any = w.left > 0;
 
-  if (warp == 0 && !E4M3) {
+  if (warp == 0) {
     if (any) {
       Ring r;
       bool ok = true;
@@ -616,7 +549,7 @@ __global__ void __launch_bounds__(kTreeThreads<E4M3>, 1)
         if (elect_one()) {
           mbar_arrive_expect_tx(&bar.full[r.st], (uint32_t)L.stage_bytes);
 #pragma unroll
-          for (int h = 0; h < D / 64; ++h)
+          for (int h = 0; h < (E4M3 ? 1 : D / 64); ++h)
             tma_load_2d(smem + r.st * L.stage_bytes + h * (kTreeTile * 128), map, &bar.full[r.st], h * 64, (int)row);
         }
         __syncwarp();
@@ -634,11 +567,13 @@ __global__ void __launch_bounds__(kTreeThreads<E4M3>, 1)
     }
   } else if (warp == 1) {
     if (any) {
-      const uint32_t idesc_s = idesc16(E4M3, kTreeTile, cols, false);
-      const uint32_t idesc_o = idesc16(false, 128, p.plan.nvp, true), idesc_l = idesc16(false, 64, cols, true);
+      const uint32_t id_s = E4M3 ? idesc(kE4m3, kE4m3, kTreeTile, cols, false) : idesc(kBf16, kBf16, kTreeTile, cols, false);
+      const uint32_t id_o = E4M3 ? idesc(kE4m3, kE5m2, D, p.plan.nvp, true) : idesc(kBf16, kBf16, 128, p.plan.nvp, true);
+      const uint32_t id_o2 = idesc(kE4m3, kE4m3, D, p.plan.nvp, true);  // the weights' second piece
+      const uint32_t id_l = idesc(kBf16, kBf16, 64, cols, true);
       const uint32_t ones = smem_u32(smem + L.ones), ring0 = smem_u32(smem);
-      const uint64_t q_desc = umma_sdesc_sw128(smem_u32(smem + L.q));
-      const uint64_t l_desc = desc_v(ones, 0);
+      const uint64_t q_desc = desc_rows<D, E4M3>(smem_u32(smem + L.q));
+      const uint64_t l_desc = desc_v<128, false>(ones, 0);
       Ring r;
       uint32_t fixed = 0;  // parity of each stage's vfix barrier
       int gs = 0, gp = 0, seg = 0;  // score products, value products, segments so far
@@ -648,13 +583,20 @@ __global__ void __launch_bounds__(kTreeThreads<E4M3>, 1)
         if (!wait(&bar.full[r.st], r.round & 1)) return false;
         if (gs >= 2 && !wait(&bar.s_empty[gs & 1], ((gs >> 1) - 1) & 1)) return false;
         tc_fence_after();
-        const uint64_t k_desc = umma_sdesc_sw128(ring0 + r.st * L.stage_bytes);
+        const uint64_t k_desc = desc_rows<D, E4M3>(ring0 + r.st * L.stage_bytes);
         const uint32_t d = tmem + (gs & 1) * cols;
         if (elect_one()) {
+          if (E4M3) {
 #pragma unroll
-          for (int k = 0; k < D / 16; ++k)  // 64-column halves: K of the tile 16 KB apart, Q cols * 128 bytes
-            umma_bf16(d, k_desc + (k >> 2) * (kTreeTile * 128 / 16) + (k & 3) * 2,
-                      q_desc + (k >> 2) * (cols * 8) + (k & 3) * 2, idesc_s, k > 0);
+            for (int k = 0; k < D / 32; ++k) umma_8bit(d, k_desc + k * 2, q_desc + k * 2, id_s, k > 0);
+#pragma unroll
+            for (int k = 0; k < D / 32; ++k) umma_8bit(d, k_desc + k * 2, q_desc + cols * (D / 16) + k * 2, id_s, 1u);
+          } else {
+#pragma unroll
+            for (int k = 0; k < D / 16; ++k)  // 64-column halves: K of the tile 16 KB apart, Q cols * 128 bytes
+              umma_bf16(d, k_desc + (k >> 2) * (kTreeTile * 128 / 16) + (k & 3) * 2,
+                        q_desc + (k >> 2) * (cols * 8) + (k & 3) * 2, id_s, k > 0);
+          }
           umma_commit(&bar.empty[r.st]);
           umma_commit(&bar.s_full[gs & 1]);
         }
@@ -673,7 +615,7 @@ __global__ void __launch_bounds__(kTreeThreads<E4M3>, 1)
           if (t + 1 < w.t1) ok = scores();
           ok = ok && wait(&bar.p_full[gp & 1], (gp >> 1) & 1);
           const uint64_t p_desc = desc_p(smem_u32(smem + L.p + (gp & 1) * L.p_bytes));
-          const bool fix = !E4M3 && (t + 1) * kTreeTile > w.P;
+          const bool fix = (t + 1) * kTreeTile > w.P;
           const uint32_t first = t > w.t0 ? 1u : 0u;
           for (int v = 0; ok && v < h.nv; ++v) {
             ok = wait(&bar.full[r.st], r.round & 1);
@@ -684,14 +626,23 @@ __global__ void __launch_bounds__(kTreeThreads<E4M3>, 1)
             if (!ok) break;
             tc_fence_after();
             const uint32_t a0 = ring0 + r.st * L.stage_bytes, d = o_tmem + v * p.plan.nvp;
-            // d = 64: the block of ones stays where it is while the tile's rows go by
-            const uint64_t a = desc_v(a0, D == 64 ? ones - a0 : kTreeTile * 128);
-            const uint64_t b = p_desc + v * (p.plan.nvp * 16);
+            // bf16, d = 64: the block of ones stays where it is while the tile's rows go by
+            const uint64_t a = desc_v<D, E4M3>(a0, E4M3 ? 0 : D == 64 ? ones - a0 : kTreeTile * 128);
+            const uint64_t b = p_desc + v * (p.plan.nvp >> (E4M3 ? 4 : 3)) * 128;
             constexpr uint64_t kStep = D == 64 ? 128ull - (128ull << 16) : 128ull;
             if (elect_one()) {
+              if (E4M3) {  // 32 rows a step: 4 groups of 8
 #pragma unroll
-              for (int k = 0; k < kTreeTile / 16; ++k)
-                umma_bf16(d, a + k * kStep, b + k * 16, idesc_o, k > 0 ? 1u : first);
+                for (int k = 0; k < kTreeTile / 32; ++k)
+                  umma_8bit(d, a + k * (D * 2), b + k * 32, id_o, k > 0 ? 1u : first);
+#pragma unroll
+                for (int k = 0; k < kTreeTile / 32; ++k)
+                  umma_8bit(d, a + k * (D * 2), b + cols * 8 + k * 32, id_o2, 1u);
+              } else {
+#pragma unroll
+                for (int k = 0; k < kTreeTile / 16; ++k)
+                  umma_bf16(d, a + k * kStep, b + k * 16, id_o, k > 0 ? 1u : first);
+              }
               umma_commit(&bar.empty[r.st]);
             }
             __syncwarp();
@@ -699,9 +650,9 @@ __global__ void __launch_bounds__(kTreeThreads<E4M3>, 1)
           }
           if (!ok) break;
           if (elect_one()) {
-            if (D == 128) {  // the sums of weights, which d = 64 has beside the values
+            if (D == 128 && !E4M3) {  // the sums of weights, which d = 64 has beside the values
 #pragma unroll
-              for (int k = 0; k < kTreeTile / 16; ++k) umma_bf16(l_tmem, l_desc, p_desc + k * 16, idesc_l, k > 0 ? 1u : first);
+              for (int k = 0; k < kTreeTile / 16; ++k) umma_bf16(l_tmem, l_desc, p_desc + k * 16, id_l, k > 0 ? 1u : first);
             }
             umma_commit(&bar.pv_done[gp & 1]);
           }
@@ -714,12 +665,16 @@ __global__ void __launch_bounds__(kTreeThreads<E4M3>, 1)
     const int wg = (warp - kEpiWarp0) >> 2, quarter = warp & 3;
     const int r = quarter * 32 + lane;        // cache row of the tile
     const int et = threadIdx.x - kEpiWarp0 * 32;  // 0 .. 255
-    float* m = reinterpret_cast<float*>(smem + L.m);
-    float* tau = reinterpret_cast<float*>(smem + L.tau);
-    float* cs = reinterpret_cast<float*>(smem + L.cs);
+    Columns cw;
+    cw.m = reinterpret_cast<float*>(smem + L.m);
+    cw.tau = reinterpret_cast<float*>(smem + L.tau);
+    cw.cs = reinterpret_cast<float*>(smem + L.cs);
+    cw.mask = reinterpret_cast<unsigned long long*>(smem + L.mask);
     float* fac = reinterpret_cast<float*>(smem + L.f);
     int* out_row = reinterpret_cast<int*>(smem + L.row);
-    unsigned long long* mask = reinterpret_cast<unsigned long long*>(smem + L.mask);
+    float* words = reinterpret_cast<float*>(smem + L.words);
+    float* sums = reinterpret_cast<float*>(smem + L.sums) + quarter * cols;  // 8-bit: this quarter's
+    constexpr float kOver = E4M3 ? kOverE5m2 : kOverBf16;
     const uint32_t lanes = (uint32_t)(quarter * 32) << 16;
     const int G = p.h_q / p.h_k;
     int gt = 0;  // tiles so far
@@ -734,14 +689,26 @@ __global__ void __launch_bounds__(kTreeThreads<E4M3>, 1)
       const int live = h.nv * mine.groups, g0 = wg == 0 ? 0 : (live + 1) >> 1;
       mine.count = wg == 0 ? (live + 1) >> 1 : live >> 1;
       mine.at = g0 % mine.groups;
-      mine.col = g0 / mine.groups * mine.nvp + mine.at * 8;
+      mine.v = 0;
+      const int v_first = g0 / mine.groups;
+      mine.col = v_first * mine.nvp + mine.at * 8;
       const int nt = w.t1 - w.t0;
-      auto fetch_scale = [&](int i) {  // of the row in the segment's tile i
+      // 8-bit: the scales of this thread's row, of the key head and of the warpgroup's value heads, a tile ahead
+      const int v_count = mine.count > 0 ? (g0 + mine.count - 1) / mine.groups - v_first + 1 : 0;
+      const int scale_slot = 2 * (1 + p.plan.nv) * kTreeTile;
+      float* scales = reinterpret_cast<float*>(smem + L.scales) + wg * (1 + p.plan.nv) * kTreeTile + r;
+      auto fetch_scales = [&](int i) {  // of the segment's tile i
+        if (!E4M3) return;
+        float* dst = scales + (i & 1) * scale_slot;
         const int row = (w.t0 + i) * kTreeTile + r;
-        return row < w.P + w.n ? __ldg(p.k_scale + h.key + row) : 0.f;
+        const bool there = row < w.P + w.n;
+        const size_t safe = there ? row : 0;
+        cp_async4_zfill(dst, p.k_scale + h.key + safe, there);
+        for (int v = 0; v < v_count; ++v)
+          cp_async4_zfill(dst + (1 + v) * kTreeTile, p.v_scale + h.value + (size_t)(v_first + v) * p.l_cap + safe, there);
+        cp_async_commit();
       };
-      float key_scale = 0.f;
-      if (E4M3) key_scale = fetch_scale(0);
+      fetch_scales(0);
       // the columns' words, then Q with every load in flight before the first is used
       int my_row = -1;  // of the output: thread et's column
       float my_tau = INFINITY;
@@ -756,7 +723,7 @@ __global__ void __launch_bounds__(kTreeThreads<E4M3>, 1)
       }
       named_bar_sync(3, kEpiAll);  // the last segment's words and Q are no longer read
       if (et < cols) {
-        m[et] = my_row >= 0 ? kUnset : -kUnset;  // padding: weights of zero whatever its scores
+        cw.m[et] = my_row >= 0 ? kUnset : -kUnset;  // padding: weights of zero whatever its scores
         out_row[et] = my_row;
       }
       named_bar_sync(3, kEpiAll);
@@ -786,22 +753,34 @@ __global__ void __launch_bounds__(kTreeThreads<E4M3>, 1)
             }
 #pragma unroll
             for (int o = LPR / 2; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-            // a power of two that brings the row's largest element into [1, 2); both it and its inverse are normal
-            const int ex = min(max((int)(__float_as_uint(amax) >> 23) - 127, -126), 126);
+            // a power of two that brings the row's largest element into [128, 256); both it and its inverse are normal
+            const int ex = min(max((int)(__float_as_uint(amax) >> 23) - 127 - 7, -126), 126);
             const float down = __uint_as_float((uint32_t)(127 - ex) << 23);
-            uint32_t y[4];
+            uint32_t y[4], z[4];
 #pragma unroll
-            for (int k = 0; k < 4; ++k) y[k] = pack_half(f[2 * k] * down, f[2 * k + 1] * down);
-            x[i] = make_uint4(y[0], y[1], y[2], y[3]);
-            if (c == 0 && col < cols) cs[col] = __uint_as_float((uint32_t)(127 + ex) << 23) * p.scale;
-          }
-          if (col < cols)
+            for (int k = 0; k < 4; ++k) {
+              const float a = f[2 * k] * down, b = f[2 * k + 1] * down;
+              y[k] = pack_8bit(a, b, __NV_E4M3);
+              const float2 had = unpack_8bit(y[k], __NV_E4M3);
+              z[k] = pack_8bit(a - had.x, b - had.y, __NV_E4M3);
+            }
+            if (col < cols) {  // 8 of the row's codes: half a 16-byte piece of its swizzled D bytes
+              uint8_t* at = smem + L.q + col * D + (c & 1) * 8 +
+                            (((c >> 1) ^ (D == 64 ? col >> 1 & 3 : col & 7)) << 4);
+              *reinterpret_cast<uint2*>(at) = make_uint2(y[0] | y[1] << 16, y[2] | y[3] << 16);
+              *reinterpret_cast<uint2*>(at + cols * D) = make_uint2(z[0] | z[1] << 16, z[2] | z[3] << 16);
+              if (c == 0) cw.cs[col] = __uint_as_float((uint32_t)(127 + ex) << 23) * p.scale;
+            }
+          } else if (col < cols) {
             *reinterpret_cast<uint4*>(smem + L.q + (c >> 3) * (cols * 128) + col * 128 + (((c & 7) ^ (col & 7)) << 4)) = x[i];
+          }
         }
       }
+      if (E4M3)
+        for (int i = et; i < 4 * cols; i += kEpiAll) reinterpret_cast<float*>(smem + L.sums)[i] = 0.f;
       if (et < cols) {
-        tau[et] = my_tau;
-        mask[et] = my_mask;
+        cw.tau[et] = my_tau;
+        cw.mask[et] = my_mask;
       }
       fence_proxy_async_shared();
       named_bar_sync(3, kEpiAll);
@@ -814,7 +793,7 @@ __global__ void __launch_bounds__(kTreeThreads<E4M3>, 1)
         p.holders[w.item] = make_int2(blockIdx.x, tree_last_holder(cut, blockIdx.x, w.tiles, place));
       }
       unsigned long long seen = 0;
-      if (!E4M3 && w.t1 * kTreeTile > w.P) seen = seen_by_any(p, w);
+      if (w.t1 * kTreeTile > w.P) seen = seen_by_any(p, w);
 
       for (int i = 0; i < nt; ++i, ++gt) {
         const int buf = gt & 1;
@@ -822,23 +801,31 @@ __global__ void __launch_bounds__(kTreeThreads<E4M3>, 1)
         uint8_t* p_buf = smem + L.p + buf * L.p_bytes;
         const int row = (w.t0 + i) * kTreeTile + r;
         Row rw;
-        rw.f = E4M3 ? key_scale : p.scale;
         rw.all = row < w.P;
+        rw.live = row_seen(w, seen, row);
         rw.bit = !rw.all && row < w.P + w.n ? 1ull << (row - w.P) : 0ull;
         const bool tail = (w.t0 + i + 1) * kTreeTile > w.P;
         const bool test = tail || p.tau != nullptr;
-        if (E4M3 && i + 1 < nt) key_scale = fetch_scale(i + 1);
+        if (E4M3) {
+          cp_async_wait_all();  // this thread's own copies
+          rw.scale = scales + (i & 1) * scale_slot + kTreeTile;
+          rw.f = rw.scale[-kTreeTile];
+          if (i + 1 < nt) fetch_scales(i + 1);
+        } else {
+          rw.f = p.scale;
+          rw.scale = nullptr;
+        }
         ok = mbar_wait(&bar.s_full[buf], (gt >> 1) & 1, abort_flag) &&
              (gt < 2 || mbar_wait(&bar.pv_done[buf], ((gt >> 1) - 1) & 1, abort_flag));
         tc_fence_after();
         auto weights = [&]() {
           uint8_t* at = p_buf + r * 16;
-          return test ? weigh<E4M3, true>(s_tmem, at, mine, rw, m, tau, cs, mask)
-                      : weigh<E4M3, false>(s_tmem, at, mine, rw, m, tau, cs, mask);
+          return test ? weigh<E4M3, true>(s_tmem, at, cols * kTreeTile, mine, rw, cw)
+                      : weigh<E4M3, false>(s_tmem, at, cols * kTreeTile, mine, rw, cw);
         };
-        // A segment's first tile: any score that every column sees is a good enough reference, so the tile's first
-        // row's; where that is a drafted row, the exact maxima.
-        const bool common = (w.t0 + i) * kTreeTile < w.P;
+        // A segment's first tile.  bf16: any score that every column sees is a good enough reference, so the tile's
+        // first row's; where that is a drafted row, the exact maxima.  8-bit weights want the maxima.
+        const bool common = !E4M3 && (w.t0 + i) * kTreeTile < w.P;
         float top = INFINITY;
         if (i == 0 && common) {
           if (quarter == 0) {
@@ -858,12 +845,12 @@ __global__ void __launch_bounds__(kTreeThreads<E4M3>, 1)
                 float s[8];
                 tmem_ld8_end(raw[k], s);
                 const int at = k == 0 ? col : next;
-                exponents<E4M3, false, false>(s, rw, at, m, tau, cs, mask);
+                exponents<E4M3, false, false>(s, rw, at, cw);
                 if (lane == 0) {
                   float old[8];
-                  load8(m + at, old);  // padding keeps its own
+                  load8(cw.m + at, old);  // padding keeps its own
 #pragma unroll
-                  for (int i2 = 0; i2 < 8; ++i2) m[at + i2] = old[i2] == kUnset ? s[i2] : old[i2];
+                  for (int x = 0; x < 8; ++x) cw.m[at + x] = old[x] == kUnset ? s[x] : old[x];
                 }
               }
             }
@@ -878,14 +865,14 @@ __global__ void __launch_bounds__(kTreeThreads<E4M3>, 1)
             break;
           }
           // the general test serves every tile here: rows of a tile without drafted ones are seen by all
-          maxima<E4M3, true>(s_tmem, p_buf, mine, rw, m, tau, cs, mask);
+          maxima<E4M3>(s_tmem, words, mine, rw, cw);
           named_bar_sync(1 + wg, 128);
           for (int c = et & 127; c < mine.count * 8; c += 128) {
             const int ag = g0 + (c >> 3), col = ag / mine.groups * mine.nvp + ag % mine.groups * 8 + (c & 7);
-            const float* words = column_words(p_buf, col) + (c & 7);
-            const float now = fmaxf(fmaxf(words[0], words[8]), fmaxf(words[16], words[24]));
-            const float old = m[col], next = now > -INFINITY ? fmaxf(old, now) : old;
-            m[col] = next;
+            const float4 x = *reinterpret_cast<const float4*>(words + col * 4);
+            const float now = fmaxf(fmaxf(x.x, x.y), fmaxf(x.z, x.w)) - (E4M3 ? kTopE5m2 : 0.f);
+            const float old = cw.m[col], next = now > -INFINITY ? fmaxf(old, now) : old;
+            cw.m[col] = next;
             fac[col] = old == kUnset ? 0.f : ex2(old - next);
           }
           if (i > 0) {
@@ -898,9 +885,9 @@ __global__ void __launch_bounds__(kTreeThreads<E4M3>, 1)
           if (i > 0) {
             Groups g = mine;
 #pragma unroll 1
-            for (int n = g.count; n > 0; --n, g.step())
+            for (int n = g.count; n > 0; --n, g.step()) {
 #pragma unroll
-              for (int part = 0; part < (D == 64 ? 1 : 2); ++part) {
+              for (int part = 0; part < (D == 64 || E4M3 ? 1 : 2); ++part) {
                 const uint32_t at = (part == 0 ? o_tmem : l_tmem) + lanes + g.col;
                 float o[8];
                 tmem_ld8(at, o);
@@ -908,6 +895,8 @@ __global__ void __launch_bounds__(kTreeThreads<E4M3>, 1)
                 for (int k = 0; k < 8; ++k) o[k] *= fac[g.col + k];
                 tmem_st8(at, o);
               }
+              if (E4M3 && (lane & 3) == 0) sums[g.col + octet_column(lane)] *= fac[g.col + octet_column(lane)];
+            }
           }
           weights();
         }
@@ -915,10 +904,17 @@ __global__ void __launch_bounds__(kTreeThreads<E4M3>, 1)
         tc_fence_before();
         __syncwarp();
         if (lane == 0) {
-          mbar_arrive(&bar.s_empty[buf]);
           mbar_arrive(&bar.p_full[buf]);
+          if (!E4M3) mbar_arrive(&bar.s_empty[buf]);
         }
-        if (!E4M3 && tail && wg == 0) {
+        if (E4M3) {  // while the products run
+          if (test) add_weights<true>(s_tmem, sums, mine, rw, cw);
+          else add_weights<false>(s_tmem, sums, mine, rw, cw);
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&bar.s_empty[buf]);
+        }
+        if (tail && wg == 0) {
           // value rows that no token sees may hold anything: zero them before the product reads them
           const bool bad = !row_seen(w, seen, row);
           Ring vr = seg_ring;
@@ -927,9 +923,12 @@ __global__ void __launch_bounds__(kTreeThreads<E4M3>, 1)
             if (!__all_sync(0xffffffffu, mbar_wait(&bar.full[vr.st], vr.round & 1, abort_flag))) break;
             if (bad) {
 #pragma unroll
-              for (int k = 0; k < D / 8; ++k)  // neighbouring rows at different banks
-                *reinterpret_cast<uint4*>(smem + vr.st * L.stage_bytes + (k >> 3) * (kTreeTile * 128) + r * 128 +
-                                          ((k + r) & 7) * 16) = make_uint4(0u, 0u, 0u, 0u);
+              for (int k = 0; k < (E4M3 ? D / 16 : D / 8); ++k) {  // neighbouring rows at different banks
+                uint8_t* line = smem + vr.st * L.stage_bytes +
+                                (E4M3 ? r * D + ((k + r) & (D / 16 - 1)) * 16
+                                      : (k >> 3) * (kTreeTile * 128) + r * 128 + ((k + r) & 7) * 16);
+                *reinterpret_cast<uint4*>(line) = make_uint4(0u, 0u, 0u, 0u);
+              }
               fence_proxy_async_shared();
             }
             __syncwarp();
@@ -950,8 +949,22 @@ __global__ void __launch_bounds__(kTreeThreads<E4M3>, 1)
       tc_fence_after();
       const bool whole = w.t0 == 0 && w.t1 == w.tiles;
       const size_t slot = (size_t)blockIdx.x + w.item;
-      // the sums of weights: lanes 64 .. 127 of the accumulators (d = 64), or lane 0 of their own columns
-      if (quarter == (D == 64 ? 2 : 0)) {
+      // the sums of weights: lanes 64 .. 127 of the accumulators (bf16, d = 64), lane 0 of their own columns (d = 128),
+      // or the four warps' (8-bit)
+      if (E4M3) {
+        named_bar_sync(1 + wg, 128);
+        for (int c = et & 127; c < mine.count * 8; c += 128) {
+          const int ag = g0 + (c >> 3), col = ag / mine.groups * mine.nvp + ag % mine.groups * 8 + (c & 7);
+          const float* x = reinterpret_cast<const float*>(smem + L.sums) + col;
+          const float sum = (x[0] + x[cols]) + (x[2 * cols] + x[3 * cols]);
+          if (whole) {
+            fac[col] = sum > 0.f ? 1.f / sum : 0.f;
+          } else {
+            p.part_l[slot * cols + col] = sum;
+            p.part_m[slot * cols + col] = cw.m[col];
+          }
+        }
+      } else if (quarter == (D == 64 ? 2 : 0)) {
         Groups g = mine;
 #pragma unroll 1
         for (int n = g.count; n > 0; --n, g.step()) {
@@ -965,20 +978,24 @@ __global__ void __launch_bounds__(kTreeThreads<E4M3>, 1)
               fac[g.col + lane] = sum > 0.f ? 1.f / sum : 0.f;
             } else {
               p.part_l[slot * cols + g.col + lane] = sum;
-              p.part_m[slot * cols + g.col + lane] = m[g.col + lane];
+              p.part_m[slot * cols + g.col + lane] = cw.m[g.col + lane];
             }
           }
         }
       }
       if (whole) named_bar_sync(1 + wg, 128);
-      if (D == 128 || quarter < 2) {
+      // lane of the accumulators: d where M = 128; 16 of each warp's 32 where M = 64 (8-bit, d = 64)
+      const int dd = E4M3 && D == 64 ? quarter * 16 + lane : r;
+      const bool has_d = E4M3 && D == 64 ? lane < 16 : D == 128 || quarter < 2;
+      if (__any_sync(0xffffffffu, has_d)) {
         Groups g = mine;
 #pragma unroll 1
         for (int n = g.count; n > 0; --n, g.step()) {
           float o[8];
           tmem_ld8(o_tmem + lanes + g.col, o);
+          if (!has_d) continue;
           if (!whole) {  // padding too: nobody reads it
-            float* dst = p.part_o + (slot * cols + g.col) * D + r;
+            float* dst = p.part_o + (slot * cols + g.col) * D + dd;
 #pragma unroll
             for (int k = 0; k < 8; ++k) dst[k * D] = o[k];
             continue;
@@ -988,17 +1005,13 @@ __global__ void __launch_bounds__(kTreeThreads<E4M3>, 1)
             const int row = out_row[g.col + k];
             if (row < 0) continue;
             const float f = fac[g.col + k], y = f > 0.f ? o[k] * f : 0.f;
-            if (p.out_bf16) static_cast<__nv_bfloat16*>(p.out)[(size_t)row * D + r] = __float2bfloat16(y);
-            else static_cast<float*>(p.out)[(size_t)row * D + r] = y;
+            if (p.out_bf16) static_cast<__nv_bfloat16*>(p.out)[(size_t)row * D + dd] = __float2bfloat16(y);
+            else static_cast<float*>(p.out)[(size_t)row * D + dd] = y;
           }
         }
       }
       tc_fence_before();
     } while (tree_walk_next(line_of(p), w));
-  } else if (E4M3 && warp >= kConvWarp0) {
-    if (any) widen_tiles<D>(p, w, smem, bar, progress, abort_flag);
-  } else if (E4M3 && warp == 2) {
-    if (any) prefetch_tiles<D>(p, w, progress, abort_flag);
   }
 
   tc_fence_before();
@@ -1208,7 +1221,7 @@ int saga_tree_attn(const saga_shape* s, int tokens, const void* q, const saga_ca
   const TreeSizes z = tree_sizes(s, p.plan, std::min(sms, kTreeMaxCtas));
   if (ws_bytes < z.total) return api_fail(SAGA_ERR_WORKSPACE, "workspace has %zu bytes, needs %zu", ws_bytes, z.total);
   const bool e4m3 = cache->format == SAGA_CACHE_E4M3;
-  p.smem = tree_smem(p.plan, s->d);
+  p.smem = tree_smem(p.plan, s->d, e4m3);
   p.q = static_cast<const uint16_t*>(q);
   p.k = cache->k;
   p.v = cache->v;
@@ -1235,12 +1248,10 @@ int saga_tree_attn(const saga_shape* s, int tokens, const void* q, const saga_ca
   p.part_l = reinterpret_cast<float*>(base + z.part_l);
   p.holders = reinterpret_cast<int2*>(base + z.holders);
   CUtensorMap km{}, vm{};
-  if (!e4m3) {
-    rc = api_rows_map(&km, cache->k, (long long)s->batch * s->h_k * s->l_cap, s->d);
-    if (rc) return rc;
-    rc = api_rows_map(&vm, cache->v, (long long)s->batch * s->h_v * s->l_cap, s->d);
-    if (rc) return rc;
-  }
+  rc = api_rows_map(&km, cache->k, (long long)s->batch * s->h_k * s->l_cap, s->d, e4m3);
+  if (rc) return rc;
+  rc = api_rows_map(&vm, cache->v, (long long)s->batch * s->h_v * s->l_cap, s->d, e4m3);
+  if (rc) return rc;
   const TreeKernel kernel = s->d == 64 ? (e4m3 ? saga_tree_kernel<64, true> : saga_tree_kernel<64, false>)
                                        : (e4m3 ? saga_tree_kernel<128, true> : saga_tree_kernel<128, false>);
   static std::atomic<uint64_t> done[4], done_join[3];
@@ -1248,7 +1259,7 @@ int saga_tree_attn(const saga_shape* s, int tokens, const void* q, const saga_ca
   cudaError_t e = prepare_kernel(reinterpret_cast<const void*>(kernel), 227 * 1024,
                                  done[(e4m3 ? 1 : 0) + (s->d == 64 ? 0 : 2)]);
   if (e == cudaSuccess)
-    e = launch_pdl(kernel, dim3(p.ctas), dim3(e4m3 ? kTreeThreads<true> : kTreeThreads<false>), p.smem.total, st, km, vm, p);
+    e = launch_pdl(kernel, dim3(p.ctas), dim3(kTreeThreads), p.smem.total, st, km, vm, p);
   if (e != cudaSuccess) return api_cuda_fail(e, "drafted-token attention launch");
   // partials of an item: about ctas / items of them, and one more
   const unsigned rows = (unsigned)s->batch * tokens * s->h_q;

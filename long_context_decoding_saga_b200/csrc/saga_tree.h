@@ -249,21 +249,24 @@ __host__ __device__ inline bool tree_row(const TreePlan& p, int T, int chunk, in
   return true;
 }
 
-// Shared memory of the kernel: the tile ring, ones (the operand that adds the
-// weights up), Q, two P buffers, per-column words, barriers.
+// Shared memory of the kernel: the tile ring, ones (the operand that adds bf16
+// weights up), Q and two P buffers (16 bits an element: bf16, or two 8-bit
+// pieces one after the other), per-column words, and for 8-bit caches the rows'
+// scales of two tiles and the sums of weights.
 struct TreeSmem {
   int stages, stage_bytes;
-  int ones, q, p, p_bytes, mask, m, tau, cs, f, row, bars, total;
+  int ones, q, p, p_bytes, mask, m, tau, cs, f, row, words, sums, scales, bars, total;
 };
-__host__ __device__ inline TreeSmem tree_smem(const TreePlan& p, int d) {
+__host__ __device__ inline TreeSmem tree_smem(const TreePlan& p, int d, bool e4m3) {
   TreeSmem s;
-  s.stage_bytes = kTreeTile * d * 2;
+  s.stage_bytes = kTreeTile * d * (e4m3 ? 1 : 2);
   const int budget = 227 * 1024 - 1024;  // less the slack that aligns the base to 1024 bytes
   const int q_bytes = p.cols * d * 2;
   s.p_bytes = p.cols * kTreeTile * 2;
-  const int words = p.cols * (8 + 5 * 4);
+  const int words = p.cols * (8 + 5 * 4 + 4 * 4);
+  const int eight = e4m3 ? p.cols * 4 * 4 + 2 * 2 * (1 + p.nv) * kTreeTile * 4 : 0;
   const int bar_bytes = 8 * (3 * kTreeMaxStages + 16) + 16 + (int)(sizeof(TreeWalk) + sizeof(TreeCut));
-  const int fixed = 2048 + q_bytes + 2 * s.p_bytes + words + bar_bytes;
+  const int fixed = 2048 + q_bytes + 2 * s.p_bytes + words + eight + bar_bytes;
   s.stages = (budget - fixed) / s.stage_bytes;
   if (s.stages > kTreeMaxStages) s.stages = kTreeMaxStages;
   s.ones = s.stages * s.stage_bytes;
@@ -275,7 +278,10 @@ __host__ __device__ inline TreeSmem tree_smem(const TreePlan& p, int d) {
   s.cs = s.tau + p.cols * 4;
   s.f = s.cs + p.cols * 4;
   s.row = s.f + p.cols * 4;
-  s.bars = s.row + p.cols * 4;
+  s.words = s.row + p.cols * 4;
+  s.sums = s.words + p.cols * 16;
+  s.scales = s.sums + (e4m3 ? p.cols * 16 : 0);
+  s.bars = s.words + p.cols * 16 + eight;
   s.total = s.bars + bar_bytes + 1024;
   return s;
 }
