@@ -211,6 +211,14 @@ __device__ __forceinline__ float ex2(float x) {
   return y;
 }
 
+__device__ __forceinline__ __half2 as_half2(uint32_t x) { return reinterpret_cast<const __half2&>(x); }
+__device__ __forceinline__ uint32_t pack_half(float a, float b) {
+  const __half2 h = __floats2half2_rn(a, b);
+  return reinterpret_cast<const uint32_t&>(h);
+}
+__device__ __forceinline__ uint32_t pack_e4m3(__half2 x) {
+  return __nv_cvt_halfraw2_to_fp8x2(static_cast<__half2_raw>(x), __NV_SATFINITE, __NV_E4M3);
+}
 // Two numbers as an 8-bit format each, in the low 16 bits, and back.
 __device__ __forceinline__ uint32_t pack_8bit(float a, float b, __nv_fp8_interpretation_t f) {
   return __nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, f);
@@ -279,7 +287,8 @@ struct Row {
   const float* scale;      // 8-bit: value scales of the row, the v-th kTreeTile words on
 };
 
-// The columns' words.
+// The columns' words: the reference, negated; the threshold and the score
+// factor (8-bit: both in powers of two); which drafted rows the column sees.
 struct Columns {
   float *m, *tau, *cs;
   unsigned long long* mask;
@@ -290,9 +299,31 @@ __device__ __forceinline__ void load8(const float* from, float* to) {
   *reinterpret_cast<float4*>(to + 4) = *reinterpret_cast<const float4*>(from + 4);
 }
 
+// Two fp32 products (and sums) at once: the weights of a tile are bound by the
+// instructions issued for them.
+__device__ __forceinline__ unsigned long long two(float a, float b) {
+  unsigned long long x;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(x) : "f"(a), "f"(b));
+  return x;
+}
+__device__ __forceinline__ void untwo(unsigned long long x, float& a, float& b) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(x));
+}
+__device__ __forceinline__ unsigned long long mul2(unsigned long long a, unsigned long long b) {
+  unsigned long long x;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(x) : "l"(a), "l"(b));
+  return x;
+}
+__device__ __forceinline__ unsigned long long fma2(unsigned long long a, unsigned long long b, unsigned long long c) {
+  unsigned long long x;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(x) : "l"(a), "l"(b), "l"(c));
+  return x;
+}
+
 // Scores of 8 columns in powers of two, less the columns' references with
 // RELATIVE; with TEST -inf where the row is hidden or the score below the
 // threshold (a row of the prefix is hidden from nobody: no masks are read).
+// bf16 compares fl(product * scale) with the threshold, as the decode calls do.
 template <bool E4M3, bool TEST, bool RELATIVE>
 __device__ __forceinline__ void exponents(float* s, const Row& r, int col, const Columns& c) {
   float mm[8], cc[8], tt[8];
@@ -309,15 +340,31 @@ __device__ __forceinline__ void exponents(float* s, const Row& r, int col, const
       if ((x.y & r.bit) != 0ull) seen |= 2u << (2 * i);
     }
   }
+  const float f = E4M3 || TEST ? r.f : r.f * kLog2e;
+  const unsigned long long ff = two(f, f), ll = two(kLog2e, kLog2e);
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const float f = E4M3 ? r.f * cc[i] : r.f;
-    if (!TEST) {
-      s[i] = RELATIVE ? fmaf(s[i], f * kLog2e, -mm[i]) : s[i] * (f * kLog2e);
+  for (int i = 0; i < 8; i += 2) {
+    unsigned long long x = two(s[i], s[i + 1]);
+    bool keep0 = true, keep1 = true;
+    if (TEST) {
+      x = mul2(x, ff);
+      if (E4M3) x = mul2(x, two(cc[i], cc[i + 1]));
+      float a, b;
+      untwo(x, a, b);
+      keep0 = a >= tt[i] && (seen >> i & 1u) != 0u;
+      keep1 = b >= tt[i + 1] && (seen >> i & 2u) != 0u;
+      if (RELATIVE) x = fma2(x, E4M3 ? two(1.f, 1.f) : ll, two(mm[i], mm[i + 1]));
+      else if (!E4M3) x = mul2(x, ll);
+    } else if (E4M3) {
+      x = mul2(x, ff);
+      x = RELATIVE ? fma2(x, two(cc[i], cc[i + 1]), two(mm[i], mm[i + 1])) : mul2(x, two(cc[i], cc[i + 1]));
     } else {
-      const float a = s[i] * f;
-      const bool keep = a >= tt[i] && (seen >> i & 1u) != 0u;
-      s[i] = keep ? (RELATIVE ? fmaf(a, kLog2e, -mm[i]) : a * kLog2e) : -INFINITY;
+      x = RELATIVE ? fma2(x, ff, two(mm[i], mm[i + 1])) : mul2(x, ff);
+    }
+    untwo(x, s[i], s[i + 1]);
+    if (TEST) {
+      s[i] = keep0 ? s[i] : -INFINITY;
+      s[i + 1] = keep1 ? s[i + 1] : -INFINITY;
     }
   }
 }
@@ -347,11 +394,16 @@ __device__ __forceinline__ float octet_sum(const float* v, int lane) {
 
 // Weights of a tile into P; returns the largest exponent of the thread's.
 // bf16: a row of P is 16 bytes per 8 columns.  8-bit: 8 bytes per 8 columns of
-// each piece, the second piece `piece` bytes on.
+// each piece, the second piece `piece` bytes on; and the weights' sums over the
+// warp's rows into here[column] (a tile that is done again overwrites them).
+// The pieces are taken in half precision, whose upper byte is an e5m2 number:
+// the first is that byte rounded, the rest an exact subtraction away.  (From
+// fp32, with a conversion each way, a tile of 96 columns took 3.9 us.)
 template <bool E4M3, bool TEST>
-__device__ __forceinline__ float weigh(uint32_t s_tmem, uint8_t* p_row, int piece, Groups g, const Row& r,
+__device__ __forceinline__ float weigh(uint32_t s_tmem, uint8_t* p_row, int piece, float* here, Groups g, const Row& r,
                                        const Columns& c) {
   float top = -INFINITY;
+  const int lane = lane_id();
   uint32_t raw[8];
   if (g.count > 0) tmem_ld8_start(s_tmem + g.col, raw);
 #pragma unroll 1
@@ -380,34 +432,24 @@ __device__ __forceinline__ float weigh(uint32_t s_tmem, uint8_t* p_row, int piec
       top = fmaxf(top, most + __log2f(fmaxf(vs, kMinScale)));
       uint32_t w[4], z[4];
 #pragma unroll
+      for (int i = 0; i < 8; ++i) s[i] = ex2(s[i]);
+#pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const float a = ex2(s[2 * i]) * vs, b = ex2(s[2 * i + 1]) * vs;
-        w[i] = pack_8bit(a, b, __NV_E5M2);
-        const float2 had = unpack_8bit(w[i], __NV_E5M2);
-        z[i] = pack_8bit(a - had.x, b - had.y, __NV_E4M3);
+        float a, b;
+        untwo(mul2(two(s[2 * i], s[2 * i + 1]), two(vs, vs)), a, b);
+        const uint32_t all = pack_half(a, b);
+        w[i] = (all + 0x00800080u) & 0xff00ff00u;
+        const __half2 rest = __hsub2(as_half2(all), as_half2(w[i]));
+        z[i] = pack_e4m3(rest);
       }
       uint8_t* at = p_row + (col >> 4) * 2048 + (col & 8);
-      *reinterpret_cast<uint2*>(at) = make_uint2(w[0] | w[1] << 16, w[2] | w[3] << 16);
+      *reinterpret_cast<uint2*>(at) = make_uint2(__byte_perm(w[0], w[1], 0x7531), __byte_perm(w[2], w[3], 0x7531));
       *reinterpret_cast<uint2*>(at + piece) = make_uint2(z[0] | z[1] << 16, z[2] | z[3] << 16);
+      const float sum = octet_sum(s, lane);
+      if ((lane & 3) == 0) here[col + octet_column(lane)] = sum;
     }
   }
   return top;
-}
-
-// 8-bit: the weights' sums over the warp's rows, added to the warp's sums.
-template <bool TEST>
-__device__ __forceinline__ void add_weights(uint32_t s_tmem, float* sums, Groups g, const Row& r, const Columns& c) {
-  const int lane = lane_id();
-#pragma unroll 1
-  for (int n = g.count; n > 0; --n, g.step()) {
-    float s[8];
-    tmem_ld8(s_tmem + g.col, s);
-    exponents<true, TEST, true>(s, r, g.col, c);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) s[i] = ex2(s[i]);
-    const float x = octet_sum(s, lane);
-    if ((lane & 3) == 0) sums[g.col + octet_column(lane)] += x;
-  }
 }
 
 // The columns' largest weights over the warp's rows, in powers of two, into
@@ -673,7 +715,8 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
     float* fac = reinterpret_cast<float*>(smem + L.f);
     int* out_row = reinterpret_cast<int*>(smem + L.row);
     float* words = reinterpret_cast<float*>(smem + L.words);
-    float* sums = reinterpret_cast<float*>(smem + L.sums) + quarter * cols;  // 8-bit: this quarter's
+    float* sums = reinterpret_cast<float*>(smem + L.sums) + quarter * cols;  // 8-bit: this quarter's rows,
+    float* sums_here = sums + 4 * cols;                                      // and those of the tile in hand
     constexpr float kOver = E4M3 ? kOverE5m2 : kOverBf16;
     const uint32_t lanes = (uint32_t)(quarter * 32) << 16;
     const int G = p.h_q / p.h_k;
@@ -723,7 +766,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
       }
       named_bar_sync(3, kEpiAll);  // the last segment's words and Q are no longer read
       if (et < cols) {
-        cw.m[et] = my_row >= 0 ? kUnset : -kUnset;  // padding: weights of zero whatever its scores
+        cw.m[et] = my_row >= 0 ? -kUnset : kUnset;  // padding: weights of zero whatever its scores
         out_row[et] = my_row;
       }
       named_bar_sync(3, kEpiAll);
@@ -769,7 +812,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
                             (((c >> 1) ^ (D == 64 ? col >> 1 & 3 : col & 7)) << 4);
               *reinterpret_cast<uint2*>(at) = make_uint2(y[0] | y[1] << 16, y[2] | y[3] << 16);
               *reinterpret_cast<uint2*>(at + cols * D) = make_uint2(z[0] | z[1] << 16, z[2] | z[3] << 16);
-              if (c == 0) cw.cs[col] = __uint_as_float((uint32_t)(127 + ex) << 23) * p.scale;
+              if (c == 0) cw.cs[col] = __uint_as_float((uint32_t)(127 + ex) << 23) * (p.scale * kLog2e);
             }
           } else if (col < cols) {
             *reinterpret_cast<uint4*>(smem + L.q + (c >> 3) * (cols * 128) + col * 128 + (((c & 7) ^ (col & 7)) << 4)) = x[i];
@@ -779,7 +822,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
       if (E4M3)
         for (int i = et; i < 4 * cols; i += kEpiAll) reinterpret_cast<float*>(smem + L.sums)[i] = 0.f;
       if (et < cols) {
-        cw.tau[et] = my_tau;
+        cw.tau[et] = E4M3 ? my_tau * kLog2e : my_tau;
         cw.mask[et] = my_mask;
       }
       fence_proxy_async_shared();
@@ -820,8 +863,8 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
         tc_fence_after();
         auto weights = [&]() {
           uint8_t* at = p_buf + r * 16;
-          return test ? weigh<E4M3, true>(s_tmem, at, cols * kTreeTile, mine, rw, cw)
-                      : weigh<E4M3, false>(s_tmem, at, cols * kTreeTile, mine, rw, cw);
+          return test ? weigh<E4M3, true>(s_tmem, at, cols * kTreeTile, sums_here, mine, rw, cw)
+                      : weigh<E4M3, false>(s_tmem, at, cols * kTreeTile, sums_here, mine, rw, cw);
         };
         // A segment's first tile.  bf16: any score that every column sees is a good enough reference, so the tile's
         // first row's; where that is a drafted row, the exact maxima.  8-bit weights want the maxima.
@@ -850,7 +893,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
                   float old[8];
                   load8(cw.m + at, old);  // padding keeps its own
 #pragma unroll
-                  for (int x = 0; x < 8; ++x) cw.m[at + x] = old[x] == kUnset ? s[x] : old[x];
+                  for (int x = 0; x < 8; ++x) cw.m[at + x] = old[x] == -kUnset ? -s[x] : old[x];
                 }
               }
             }
@@ -871,8 +914,8 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
             const int ag = g0 + (c >> 3), col = ag / mine.groups * mine.nvp + ag % mine.groups * 8 + (c & 7);
             const float4 x = *reinterpret_cast<const float4*>(words + col * 4);
             const float now = fmaxf(fmaxf(x.x, x.y), fmaxf(x.z, x.w)) - (E4M3 ? kTopE5m2 : 0.f);
-            const float old = cw.m[col], next = now > -INFINITY ? fmaxf(old, now) : old;
-            cw.m[col] = next;
+            const float old = -cw.m[col], next = now > -INFINITY ? fmaxf(old, now) : old;
+            cw.m[col] = -next;
             fac[col] = old == kUnset ? 0.f : ex2(old - next);
           }
           if (i > 0) {
@@ -895,7 +938,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
                 for (int k = 0; k < 8; ++k) o[k] *= fac[g.col + k];
                 tmem_st8(at, o);
               }
-              if (E4M3 && (lane & 3) == 0) sums[g.col + octet_column(lane)] *= fac[g.col + octet_column(lane)];
+              if (E4M3 && lane < 8) sums[g.col + lane] *= fac[g.col + lane];
             }
           }
           weights();
@@ -905,14 +948,12 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
         __syncwarp();
         if (lane == 0) {
           mbar_arrive(&bar.p_full[buf]);
-          if (!E4M3) mbar_arrive(&bar.s_empty[buf]);
+          mbar_arrive(&bar.s_empty[buf]);
         }
         if (E4M3) {  // while the products run
-          if (test) add_weights<true>(s_tmem, sums, mine, rw, cw);
-          else add_weights<false>(s_tmem, sums, mine, rw, cw);
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&bar.s_empty[buf]);
+          Groups g = mine;
+          for (int n = g.count; n > 0; --n, g.step())
+            if (lane < 8) sums[g.col + lane] += sums_here[g.col + lane];
         }
         if (tail && wg == 0) {
           // value rows that no token sees may hold anything: zero them before the product reads them
@@ -961,7 +1002,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
             fac[col] = sum > 0.f ? 1.f / sum : 0.f;
           } else {
             p.part_l[slot * cols + col] = sum;
-            p.part_m[slot * cols + col] = cw.m[col];
+            p.part_m[slot * cols + col] = -cw.m[col];
           }
         }
       } else if (quarter == (D == 64 ? 2 : 0)) {
@@ -978,7 +1019,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
               fac[g.col + lane] = sum > 0.f ? 1.f / sum : 0.f;
             } else {
               p.part_l[slot * cols + g.col + lane] = sum;
-              p.part_m[slot * cols + g.col + lane] = cw.m[g.col + lane];
+              p.part_m[slot * cols + g.col + lane] = -cw.m[g.col + lane];
             }
           }
         }
