@@ -423,30 +423,44 @@ def key_head_merge(x, q, w_k, h_k: int, workspace=None, stream=None):
 
 class KVCache:
     """One layer's caches in either format: bf16 k [B, h_k, l_cap, d] and v [B, h_v, l_cap, d], or e4m3 codes of the
-    same shapes (float8_e4m3fn or uint8) with one fp32 scale per row, k_scale [B, h_k, l_cap] and v_scale."""
+    same shapes (float8_e4m3fn or uint8) with one fp32 scale per row, k_scale [B, h_k, l_cap] and v_scale.  Checked
+    once, here; the tensors cannot be exchanged afterwards."""
+
+    __slots__ = ("_k", "_v", "_k_scale", "_v_scale", "_format", "_device", "_dims", "_struct")
 
     def __init__(self, k, v, k_scale=None, v_scale=None):
         if (k_scale is None) != (v_scale is None):
             raise ValueError("pass both scales (an 8-bit cache) or neither (bf16)")
-        self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
-        self.format = SAGA_CACHE_BF16 if k_scale is None else SAGA_CACHE_E4M3
+        for name, t in (("cache.k", k), ("cache.v", v)):
+            if not isinstance(t, torch.Tensor) or t.dim() != 4:
+                raise ValueError(f"{name} must be a 4-D tensor [batch, heads, l_cap, d]")
+        B, hk, lc, d = k.shape
+        hv = int(v.shape[1])
+        if k_scale is None:
+            _expect(k, "cache.k", torch.bfloat16)
+            _expect(v, "cache.v", torch.bfloat16, (B, hv, lc, d))
+        else:
+            for name, t, shape in (("cache.k", k, (B, hk, lc, d)), ("cache.v", v, (B, hv, lc, d))):
+                _expect(t, name, torch.uint8 if t.dtype == torch.uint8 else torch.float8_e4m3fn, shape)
+            _expect(k_scale, "cache.k_scale", torch.float32, (B, hk, lc))
+            _expect(v_scale, "cache.v_scale", torch.float32, (B, hv, lc))
+        if len({t.device for t in (k, v, k_scale, v_scale) if t is not None}) != 1:
+            raise ValueError("cache tensors on different devices")
+        self._k, self._v, self._k_scale, self._v_scale = k, v, k_scale, v_scale
+        self._format = SAGA_CACHE_BF16 if k_scale is None else SAGA_CACHE_E4M3
+        self._device = k.get_device()
+        self._dims = (int(B), int(hk), hv, int(d), int(lc))
+        self._struct = _Cache(k.data_ptr(), v.data_ptr(), None if k_scale is None else k_scale.data_ptr(),
+                              None if v_scale is None else v_scale.data_ptr(), self._format)
 
-    def _struct(self, shape: SagaShape) -> "_Cache":
-        B, hq, hk, hv, d, lc = shape.astuple()
-        for name, t, h in (("cache.k", self.k, hk), ("cache.v", self.v, hv)):
-            if self.format == SAGA_CACHE_BF16:
-                _expect(t, name, torch.bfloat16, (B, h, lc, d))
-            else:
-                _expect(t, name, torch.uint8 if t.dtype == torch.uint8 else torch.float8_e4m3fn, (B, h, lc, d))
-        if self.format == SAGA_CACHE_E4M3:
-            _expect(self.k_scale, "cache.k_scale", torch.float32, (B, hk, lc))
-            _expect(self.v_scale, "cache.v_scale", torch.float32, (B, hv, lc))
-        return _Cache(self.k.data_ptr(), self.v.data_ptr(),
-                      None if self.k_scale is None else self.k_scale.data_ptr(),
-                      None if self.v_scale is None else self.v_scale.data_ptr(), self.format)
+    k = property(lambda self: self._k)
+    v = property(lambda self: self._v)
+    k_scale = property(lambda self: self._k_scale)
+    v_scale = property(lambda self: self._v_scale)
+    format = property(lambda self: self._format)
 
     def _tensors(self):
-        return (self.k, self.v, self.k_scale, self.v_scale)
+        return (self._k, self._v, self._k_scale, self._v_scale)
 
 
 def alloc_cache(shape: SagaShape, format: int = SAGA_CACHE_BF16, device=None) -> KVCache:
@@ -464,43 +478,79 @@ def alloc_cache(shape: SagaShape, format: int = SAGA_CACHE_BF16, device=None) ->
                    torch.zeros((B, hv, lc), dtype=torch.float32, device=device))
 
 
-def _rows(t, name: str, B: int, T: int, heads: int, d: int) -> "_Rows":
+# The serving calls below cost a few microseconds on the GPU in their smallest forms, so their checks are written for
+# the case that everything is in order: one expression per tensor, and _expect for what is wrong where it is not.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
+def _dense(t, name: str, dtype, shape, device: int):
+    """The pointer of a dense tensor on `device` (None: no tensor)."""
+    if t is None:
+        return None
+    if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and t.get_device() == device
+            and t.is_contiguous()):
+        _expect(t, name, dtype, shape)
+        raise ValueError(f"{name} is on {t.device}, the cache on cuda:{device}")
+    return t.data_ptr()
+
+
+def _status_word(t, device: int):
+    if t is None:
+        return None
+    _expect(t, "status", torch.uint8)
+    if t.numel() < 4 or t.get_device() != device:
+        raise ValueError("status must hold 4 bytes on the cache's device")
+    return t.data_ptr()
+
+
+def _rows(t, name: str, shape, device: int) -> "_Rows":
     """A [B, T, heads, d] tensor or view whose last dimension is dense."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
-    if t.dtype != torch.bfloat16:
+    if t.dtype is not torch.bfloat16:
         raise TypeError(f"{name} must be torch.bfloat16, got {t.dtype}")
-    if not t.is_cuda:
-        raise ValueError(f"{name} must be a CUDA tensor")
-    if tuple(t.shape) != (B, T, heads, d):
-        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {(B, T, heads, d)}")
-    if t.stride(3) != 1:
+    if t.get_device() != device:
+        raise ValueError(f"{name} must be on the cache's device, got {t.device}")
+    if t.shape != shape:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+    sb, st, sh, s1 = t.stride()
+    if s1 != 1:
         raise ValueError(f"{name}: the elements of a head must be dense (strides {t.stride()})")
     # a dimension of one element has no stride that matters
-    return _Rows(t.data_ptr(), t.stride(0) if B > 1 else 0, t.stride(1) if T > 1 else 0,
-                 t.stride(2) if heads > 1 else 0)
+    return _Rows(t.data_ptr(), sb if shape[0] > 1 else 0, st if shape[1] > 1 else 0, sh if shape[2] > 1 else 0)
 
 
 def _tokens(t, name: str) -> int:
     if not isinstance(t, torch.Tensor) or t.dim() != 4:
         raise ValueError(f"{name} must be a 4-D tensor [batch, tokens, heads, d]")
-    return int(t.shape[1])
+    return t.shape[1]
 
 
-class _on_device:
-    """Makes the tensors' device current for a call; they must all be on one device."""
+def _cache_of(cache, shape: SagaShape):
+    """The cache's C struct and device, its dimensions those of the shape."""
+    if not isinstance(cache, KVCache):
+        raise TypeError("cache must be a KVCache")
+    if cache._dims != (shape.batch, shape.h_k, shape.h_v, shape.d, shape.l_cap):
+        raise ValueError(f"cache has (batch, h_k, h_v, d, l_cap) {cache._dims}, the shape {shape.astuple()}")
+    if cache._device < 0:
+        raise ValueError("cache must hold CUDA tensors")
+    return ctypes.byref(cache._struct), cache._device
 
-    def __init__(self, *tensors):
-        devices = {t.device for t in tensors if t is not None}
-        if len(devices) != 1:
-            raise ValueError(f"tensors on different devices: {sorted(map(str, devices))}")
-        self._guard = torch.cuda.device(devices.pop())
 
-    def __enter__(self):
-        return self._guard.__enter__()
-
-    def __exit__(self, *exc):
-        return self._guard.__exit__(*exc)
+def _call(fn, device: int, stream, *args):
+    """Calls fn(*args, stream) with `device` current, on `stream` or the device's current one."""
+    if device != torch.cuda.current_device():
+        with torch.cuda.device(device):
+            return _call(fn, device, stream, *args)
+    if stream is not None:
+        raw = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+    elif _raw_stream is not None:
+        raw = _raw_stream(device)
+    else:
+        raw = torch.cuda.current_stream(device).cuda_stream
+    rc = fn(*args, raw)
+    if rc != SAGA_OK:
+        _check(rc)
 
 
 def saga_norm_rope_append(shape: SagaShape, q, k, v, cache: KVCache, starts, q_out, positions=None, counts=None,
@@ -510,76 +560,54 @@ def saga_norm_rope_append(shape: SagaShape, q, k, v, cache: KVCache, starts, q_o
     keys, with the append of keys and values at cache rows starts[b] + t.  q, k, v: bf16 [B, T, heads, d], strided
     views allowed; q_out: bf16 [B, T, h_q, d]; starts, counts: int32 [B]; positions: int32 [B, T] (the
     cache row where None); status: a workspace tensor whose word 0 takes SAGA_STATUS_LEN_CLAMPED."""
-    B, hq, hk, hv, d, lc = shape.astuple()
+    c, dev = _cache_of(cache, shape)
+    B, hq, hk, hv, d = shape.batch, shape.h_q, shape.h_k, shape.h_v, shape.d
     T = _tokens(q, "q")
-    rq, rk, rv = _rows(q, "q", B, T, hq, d), _rows(k, "k", B, T, hk, d), _rows(v, "v", B, T, hv, d)
-    _expect(q_out, "q_out", torch.bfloat16, (B, T, hq, d))
-    _expect(starts, "starts", torch.int32, (B,))
-    if positions is not None:
-        _expect(positions, "positions", torch.int32, (B, T))
-    if counts is not None:
-        _expect(counts, "counts", torch.int32, (B,))
+    i32 = torch.int32
+    q_shape = (B, T, hq, d)
+    rq, rk, rv = _rows(q, "q", q_shape, dev), _rows(k, "k", (B, T, hk, d), dev), _rows(v, "v", (B, T, hv, d), dev)
+    if starts is None or q_out is None:
+        raise ValueError("starts and q_out are required")
     if not norm and (q_weight is not None or k_weight is not None):
         raise ValueError("norm weights without norm=True")
-    for name, w in (("q_weight", q_weight), ("k_weight", k_weight)):
-        if w is not None:
-            _expect(w, name, torch.bfloat16, (d,))
     rot = 0
     if inv_freq is not None:
-        _expect(inv_freq, "inv_freq", torch.float32)
-        if inv_freq.dim() != 1:
-            raise ValueError("inv_freq must be 1-D [rot_dim / 2]")
-        rot = 2 * int(inv_freq.shape[0])
-    if status is not None:
-        _expect(status, "status", torch.uint8)
-        if status.numel() < 4:
-            raise ValueError("status must hold 4 bytes")
-    op = _NormRope(1 if norm else 0, float(eps), None if q_weight is None else q_weight.data_ptr(),
-                   None if k_weight is None else k_weight.data_ptr(),
-                   None if inv_freq is None else inv_freq.data_ptr(), rot, 1 if interleaved else 0)
-    c = cache._struct(shape)
-    with _on_device(q, k, v, q_out, starts, positions, counts, q_weight, k_weight, inv_freq, status,
-                    *cache._tensors()):
-        _check(load().saga_norm_rope_append(ctypes.byref(shape), T, ctypes.byref(rq), ctypes.byref(rk),
-                                            ctypes.byref(rv), ctypes.byref(op), _ptr(starts), _ptr(positions),
-                                            _ptr(counts), _ptr(q_out), ctypes.byref(c), _ptr(status),
-                                            _stream(stream)))
+        if not isinstance(inv_freq, torch.Tensor) or inv_freq.dim() != 1:
+            raise ValueError("inv_freq must be a 1-D tensor [rot_dim / 2]")
+        rot = 2 * inv_freq.shape[0]
+    op = _NormRope(1 if norm else 0, eps, _dense(q_weight, "q_weight", torch.bfloat16, (d,), dev),
+                   _dense(k_weight, "k_weight", torch.bfloat16, (d,), dev),
+                   _dense(inv_freq, "inv_freq", torch.float32, (rot // 2,), dev), rot, 1 if interleaved else 0)
+    _call(load().saga_norm_rope_append, dev, stream, ctypes.byref(shape), T, ctypes.byref(rq), ctypes.byref(rk),
+          ctypes.byref(rv), ctypes.byref(op), _dense(starts, "starts", i32, (B,), dev),
+          _dense(positions, "positions", i32, (B, T), dev), _dense(counts, "counts", i32, (B,), dev),
+          _dense(q_out, "q_out", torch.bfloat16, q_shape, dev), c, _status_word(status, dev))
 
 
 def saga_kv_store(shape: SagaShape, k, v, cache: KVCache, starts, counts=None, status=None, stream=None):
     """Appends the new tokens' keys and values (bf16 [B, T, heads, d], strided views allowed) at cache rows
     starts[b] + t, in the cache's format."""
-    B, hq, hk, hv, d, lc = shape.astuple()
+    c, dev = _cache_of(cache, shape)
+    B, d = shape.batch, shape.d
     T = _tokens(k, "k")
-    rk, rv = _rows(k, "k", B, T, hk, d), _rows(v, "v", B, T, hv, d)
-    _expect(starts, "starts", torch.int32, (B,))
-    if counts is not None:
-        _expect(counts, "counts", torch.int32, (B,))
-    if status is not None:
-        _expect(status, "status", torch.uint8)
-        if status.numel() < 4:
-            raise ValueError("status must hold 4 bytes")
-    c = cache._struct(shape)
-    with _on_device(k, v, starts, counts, status, *cache._tensors()):
-        _check(load().saga_kv_store(ctypes.byref(shape), T, ctypes.byref(rk), ctypes.byref(rv), _ptr(starts),
-                                    _ptr(counts), ctypes.byref(c), _ptr(status), _stream(stream)))
+    rk, rv = _rows(k, "k", (B, T, shape.h_k, d), dev), _rows(v, "v", (B, T, shape.h_v, d), dev)
+    if starts is None:
+        raise ValueError("starts is required")
+    _call(load().saga_kv_store, dev, stream, ctypes.byref(shape), T, ctypes.byref(rk), ctypes.byref(rv),
+          _dense(starts, "starts", torch.int32, (B,), dev), _dense(counts, "counts", torch.int32, (B,), dev), c,
+          _status_word(status, dev))
 
 
 def saga_kv_load(shape: SagaShape, cache: KVCache, start: int, rows: int, k_out=None, v_out=None, lens=None,
                  stream=None):
     """Rows [start, start + rows) of an 8-bit cache as bf16 into k_out [B, h_k, rows, d] and v_out [B, h_v, rows, d]
     (either may be None); with lens (int32 [B]) rows at or past lens[b] are left as they are."""
-    B, hq, hk, hv, d, lc = shape.astuple()
-    if k_out is not None:
-        _expect(k_out, "k_out", torch.bfloat16, (B, hk, int(rows), d))
-    if v_out is not None:
-        _expect(v_out, "v_out", torch.bfloat16, (B, hv, int(rows), d))
-    if lens is not None:
-        _expect(lens, "lens", torch.int32, (B,))
-    c = cache._struct(shape)
-    with _on_device(k_out, v_out, lens, *cache._tensors()):
-        _check(load().saga_kv_load(ctypes.byref(shape), ctypes.byref(c), int(start), int(rows), _ptr(lens),
-                                   _ptr(k_out), _ptr(v_out), _stream(stream)))
+    c, dev = _cache_of(cache, shape)
+    B, d = shape.batch, shape.d
+    _call(load().saga_kv_load, dev, stream, ctypes.byref(shape), c, start, rows,
+          _dense(lens, "lens", torch.int32, (B,), dev),
+          _dense(k_out, "k_out", torch.bfloat16, (B, shape.h_k, rows, d), dev),
+          _dense(v_out, "v_out", torch.bfloat16, (B, shape.h_v, rows, d), dev))
 
 
 def saga_tree_workspace_bytes(shape: SagaShape, tokens: int) -> int:
@@ -599,26 +627,26 @@ def saga_tree_attn(shape: SagaShape, q, cache: KVCache, prefix_lens, out, worksp
     """Attention of drafted tokens: q bf16 [B, T, h_q, d] over prefix_lens[b] cached rows and the drafted rows at
     prefix_lens[b] + u that tree_mask (int64 or uint64 words [B, T]; None: u <= t) shows; tau fp32 [B, h_q] keeps
     scores at or above the thresholds.  out: fp32 or bf16 [B, T, h_q, d]."""
-    B, hq, hk, hv, d, lc = shape.astuple()
+    c, dev = _cache_of(cache, shape)
+    B, hq = shape.batch, shape.h_q
     T = _tokens(q, "q")
-    _expect(q, "q", torch.bfloat16, (B, T, hq, d))
-    _expect(prefix_lens, "prefix_lens", torch.int32, (B,))
-    if not isinstance(out, torch.Tensor) or out.dtype not in (torch.float32, torch.bfloat16):
+    if prefix_lens is None or out is None or workspace is None:
+        raise ValueError("prefix_lens, out and workspace are required")
+    dtype = out.dtype
+    if dtype is torch.bfloat16:
+        out_dtype = SAGA_OUT_BF16
+    elif dtype is torch.float32:
+        out_dtype = SAGA_OUT_F32
+    else:
         raise TypeError("out must be float32 or bfloat16")
-    _expect(out, "out", out.dtype, (B, T, hq, d))
-    _expect(workspace, "workspace", torch.uint8)
-    if tree_mask is not None:
-        _expect(tree_mask, "tree_mask", torch.uint64 if tree_mask.dtype == torch.uint64 else torch.int64, (B, T))
-    if counts is not None:
-        _expect(counts, "counts", torch.int32, (B,))
-    if tau is not None:
-        _expect(tau, "tau", torch.float32, (B, hq))
-    c = cache._struct(shape)
-    with _on_device(q, prefix_lens, out, workspace, tree_mask, counts, tau, *cache._tensors()):
-        _check(load().saga_tree_attn(ctypes.byref(shape), T, _ptr(q), ctypes.byref(c), _ptr(prefix_lens),
-                                     _ptr(counts), _ptr(tree_mask), _ptr(tau), _ptr(out),
-                                     SAGA_OUT_BF16 if out.dtype == torch.bfloat16 else SAGA_OUT_F32, _ptr(workspace),
-                                     workspace.numel(), _stream(stream)))
+    q_shape = (B, T, hq, shape.d)
+    words = torch.int64 if tree_mask is None or tree_mask.dtype is torch.int64 else torch.uint64
+    ws_bytes = workspace.numel()
+    _call(load().saga_tree_attn, dev, stream, ctypes.byref(shape), T, _dense(q, "q", torch.bfloat16, q_shape, dev), c,
+          _dense(prefix_lens, "prefix_lens", torch.int32, (B,), dev), _dense(counts, "counts", torch.int32, (B,), dev),
+          _dense(tree_mask, "tree_mask", words, (B, T), dev), _dense(tau, "tau", torch.float32, (B, hq), dev),
+          _dense(out, "out", dtype, q_shape, dev), out_dtype,
+          _dense(workspace, "workspace", torch.uint8, (ws_bytes,), dev), ws_bytes)
 
 
 def read_probe(buf: torch.Tensor, sink: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:

@@ -121,15 +121,71 @@ def test_tree_workspace_refusals(lib):
 def test_binding_refusals(lib):
     s = _shape()
     bf = lambda *shape: torch.zeros(shape, dtype=torch.bfloat16)
-    cpu_cache = saga.alloc_cache(s, saga.SAGA_CACHE_E4M3, device="cpu")
-    i32 = torch.zeros(1, dtype=torch.int32)
     with pytest.raises(ValueError):  # CPU tensors
-        saga.saga_kv_store(s, bf(1, 2, 1, 64), bf(1, 2, 8, 64), cpu_cache, i32)
-    with pytest.raises(TypeError):
-        saga.saga_kv_store(s, torch.zeros(1, 2, 1, 64), bf(1, 2, 8, 64), cpu_cache, i32)
+        saga.alloc_cache(s, saga.SAGA_CACHE_E4M3, device="cpu")
     with pytest.raises(ValueError):
-        saga.saga_kv_store(s, bf(1, 2, 64), bf(1, 2, 8, 64), cpu_cache, i32)
-    with pytest.raises(ValueError):
+        saga.KVCache(bf(1, 1, 4, 64), bf(1, 8, 4, 64))
+    with pytest.raises(ValueError):  # one scale of two
         saga.KVCache(bf(1, 1, 4, 64), bf(1, 8, 4, 64), torch.zeros(1, 1, 4), None)
     with pytest.raises(ValueError):
+        saga.KVCache(bf(1, 4, 64), bf(1, 8, 4, 64))
+    with pytest.raises(ValueError):
         saga.alloc_cache(s, 9, device="cpu")
+    with pytest.raises(TypeError):  # caches are described by a KVCache
+        saga.saga_kv_store(s, bf(1, 2, 1, 64), bf(1, 2, 8, 64), (bf(1, 1, 4, 64), bf(1, 8, 4, 64)), None)
+
+
+@pytest.mark.gpu
+def test_binding_refusals_of_cuda_tensors():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    s = saga.SagaShape.of(2, 8, 1, 8, 64, 32)
+    z = lambda *shape, dtype=torch.bfloat16: torch.zeros(shape, dtype=dtype, device="cuda")
+    cache = saga.alloc_cache(s, saga.SAGA_CACHE_E4M3)
+    starts, q = z(2, dtype=torch.int32), z(2, 3, 8, 64)
+    k, v = z(2, 3, 1, 64), z(2, 3, 8, 64)
+    saga.saga_kv_store(s, k, v, cache, starts)  # in order
+    ws = saga.alloc_tree_workspace(s, 3)
+    saga.saga_tree_attn(s, q, cache, starts, torch.empty_like(q), ws)
+    store = lambda **kw: saga.saga_kv_store(kw.pop("s", s), kw.pop("k", k), kw.pop("v", v), kw.pop("cache", cache),
+                                            kw.pop("starts", starts), **kw)
+    tree = lambda **kw: saga.saga_tree_attn(s, kw.pop("q", q), cache, kw.pop("pl", starts),
+                                            kw.pop("out", torch.empty_like(q)), kw.pop("ws", ws), **kw)
+    with pytest.raises(ValueError):  # another shape's cache
+        store(s=saga.SagaShape.of(2, 8, 1, 8, 64, 33))
+    with pytest.raises(TypeError):
+        store(k=k.float())
+    with pytest.raises(ValueError):
+        store(k=k.cpu())
+    with pytest.raises(ValueError):
+        store(k=z(2, 3, 2, 64))
+    with pytest.raises(ValueError):  # elements of a head not dense
+        store(k=z(2, 3, 64, 2).transpose(2, 3)[:, :, :1])
+    with pytest.raises(TypeError):
+        store(starts=starts.long())
+    with pytest.raises(ValueError):
+        store(starts=None)
+    with pytest.raises(ValueError):
+        store(counts=z(3, dtype=torch.int32))
+    with pytest.raises(saga.SagaError):  # more tokens than rows
+        store(k=z(2, 33, 1, 64), v=z(2, 33, 8, 64))
+    with pytest.raises(saga.SagaError):  # strides of 4 elements
+        store(k=torch.zeros(2 * 3 * 68, dtype=torch.bfloat16, device="cuda").as_strided((2, 3, 1, 64), (204, 68, 64, 1)))
+    with pytest.raises(TypeError):
+        tree(out=q.half())
+    with pytest.raises(ValueError):
+        tree(out=torch.empty((2, 3, 8, 128), dtype=torch.bfloat16, device="cuda"))
+    with pytest.raises(ValueError):
+        tree(q=z(2, 3, 16, 64)[:, :, ::2])
+    with pytest.raises(TypeError):
+        tree(tree_mask=z(2, 3, dtype=torch.int32))
+    with pytest.raises(TypeError):
+        tree(tau=z(2, 8))
+    with pytest.raises(saga.SagaError):
+        tree(ws=ws[:256])
+    with pytest.raises(saga.SagaError):
+        saga.saga_kv_load(s, saga.alloc_cache(s), 0, 4, z(2, 1, 4, 64))  # a bf16 cache
+    with pytest.raises(ValueError):
+        saga.saga_norm_rope_append(s, q, k, v, cache, starts, q.clone(), q_weight=z(64))  # a weight, no norm
+    torch.cuda.synchronize()
+    assert saga.saga_get_status(ws) == 0
