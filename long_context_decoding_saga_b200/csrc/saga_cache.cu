@@ -45,91 +45,115 @@ __device__ __forceinline__ float2 turn_of(int position, float inv_freq) {
   return make_float2(c, s);
 }
 
-// One CTA holds `group` tokens of one batch row and all their heads; a row of
-// a head (d elements) is D / 8 lanes of 16 bytes each, so its sum of squares,
-// its rotation partners and its largest magnitude are shuffles.  The angles
-// are the same for every head: they are computed once per token into shared
-// memory.  Rows are taken head by head, so neighbouring lanes write
-// neighbouring cache rows and scales.
-template <int D, bool E4M3>
-__global__ void __launch_bounds__(kRowThreads) saga_rows_kernel(const RowParams p) {
-  constexpr int LPR = D / 8;  // lanes per row
-  constexpr int RPP = kRowThreads / LPR;  // rows per pass
-  __shared__ float2 turns[kMaxRowTokens * (D / 2)];
-  pdl_trigger();
-  pdl_wait();
-  const int b = blockIdx.x / p.groups;
-  const int t0 = (blockIdx.x - b * p.groups) * p.group;
-  int count = p.counts != nullptr ? p.counts[b] : p.tokens;
-  count = min(max(count, 0), p.tokens);
-  const int nt = min(p.group, count - t0);
-  if (nt <= 0) return;
-  const int start = p.starts[b];
-  const int half = p.rot >> 1;
-  if (p.inv_freq != nullptr) {
-    for (int i = threadIdx.x; i < nt * half; i += kRowThreads) {
-      const int t = i / half, f = i - t * half;
-      const int pos = p.positions != nullptr ? p.positions[(size_t)b * p.tokens + t0 + t]
-                                             : (int)((unsigned)start + (unsigned)(t0 + t));
-      turns[t * half + f] = turn_of(pos, p.inv_freq[f]);
-    }
-    __syncthreads();
+// cos and sin of a token's angles in shared memory, 16 bytes per two angles.
+// Half-split pairs: a lane reads 8 angles, 64 bytes; the 16-byte pieces of
+// neighbouring lanes are rotated against each other, so that four lanes' reads
+// of one piece fall on different banks.
+__device__ __forceinline__ int turn_slot(int f, bool interleaved) {
+  if (interleaved) return f;
+  const int c = f >> 3, j = f >> 1 & 3;
+  return (c << 3) + ((j ^ (c & 3)) << 1) + (f & 1);
+}
+
+// 8 fp32 values as e4m3 codes of x * up.
+__device__ __forceinline__ uint2 codes8(const float* x, float up) {
+  uint32_t w[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    w[i] = __nv_cvt_float2_to_fp8x2(make_float2(x[2 * i] * up, x[2 * i + 1] * up), __NV_SATFINITE, __NV_E4M3);
+  return make_uint2(w[0] | w[1] << 16, w[2] | w[3] << 16);
+}
+
+// A CTA's tokens of one batch row.
+struct Tokens {
+  int b, t0, nt, shift, start;  // shift: log2 nt where that is a power of two, else -1
+  __device__ __forceinline__ void split(int item, int* head, int* t) const {
+    *head = shift >= 0 ? item >> shift : item / nt;
+    *t = item - *head * nt;
   }
-  const int hq = p.q != nullptr ? p.h_q : 0;
-  const int items = (hq + p.h_k + p.h_v) * nt;
-  const int c = threadIdx.x % LPR;
-  for (int base = 0; base < items; base += RPP) {
-    const int item = base + threadIdx.x / LPR;
-    const bool live = item < items;
-    int head = live ? item / nt : 0;
-    const int t = live ? item - head * nt : 0;
-    const uint16_t* src;
-    int kind;  // 0: query, 1: key, 2: value
-    if (head < hq) {
-      kind = 0;
-      src = p.q + b * p.q_bs + (t0 + t) * p.q_ts + head * p.q_hs;
-    } else if (head < hq + p.h_k) {
-      kind = 1;
-      head -= hq;
-      src = p.k + b * p.k_bs + (t0 + t) * p.k_ts + head * p.k_hs;
-    } else {
-      kind = 2;
-      head -= hq + p.h_k;
-      src = p.v + b * p.v_bs + (t0 + t) * p.v_ts + head * p.v_hs;
-    }
+  // The cache row of a token; false if it is none (a start that is no row may wrap: then it does not fit).
+  __device__ __forceinline__ bool slot(const RowParams& p, int t, int* at) const {
+    *at = (int)((unsigned)start + (unsigned)(t0 + t));
+    return (unsigned)*at < (unsigned)p.l_cap;
+  }
+};
+
+__device__ __forceinline__ bool tokens_of(const RowParams& p, Tokens& k) {
+  k.b = blockIdx.x / p.groups;
+  k.t0 = (blockIdx.x - k.b * p.groups) * p.group;
+  const int count = p.counts != nullptr ? p.counts[k.b] : p.tokens;
+  k.start = p.starts[k.b];
+  k.nt = min(p.group, min(max(count, 0), p.tokens) - k.t0);
+  k.shift = k.nt == p.group ? p.group_log2 : -1;
+  return k.nt > 0;
+}
+
+// Rows of one kind in flight: a row of a head is D / 8 lanes of 16 bytes each.
+enum { kQuery, kKey, kValue };
+template <int D, int KIND>
+struct RowFeed {
+  const uint16_t* base;
+  long long ts, hs;
+  int items;
+  __device__ __forceinline__ RowFeed(const RowParams& p, const Tokens& k) {
+    const uint16_t* data = KIND == kQuery ? p.q : KIND == kKey ? p.k : p.v;
+    const long long bs = KIND == kQuery ? p.q_bs : KIND == kKey ? p.k_bs : p.v_bs;
+    ts = KIND == kQuery ? p.q_ts : KIND == kKey ? p.k_ts : p.v_ts;
+    hs = KIND == kQuery ? p.q_hs : KIND == kKey ? p.k_hs : p.v_hs;
+    base = data + k.b * bs + k.t0 * ts;
+    items = (KIND == kQuery ? p.h_q : KIND == kKey ? p.h_k : p.h_v) * k.nt;
+  }
+  __device__ __forceinline__ const uint16_t* at(const Tokens& k, int item) const {
+    int head, t;
+    k.split(item < items ? item : 0, &head, &t);
+    return base + t * ts + head * hs;
+  }
+};
+
+template <int D, bool E4M3, int KIND>
+__device__ __forceinline__ void rows_of(const RowParams& p, const Tokens& k, const RowFeed<D, KIND>& f, uint4 raw,
+                                        const float2* turns) {
+  constexpr int LPR = D / 8, RPP = kRowThreads / LPR;  // lanes per row, rows per pass
+  const int c = threadIdx.x % LPR, r0 = threadIdx.x / LPR;
+  const int half = p.rot >> 1;
+  float w[8];
+  if (KIND != kValue && p.norm) {
+    const uint16_t* wp = KIND == kQuery ? p.q_weight : p.k_weight;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) w[i] = 1.f;
+    if (wp != nullptr) unpack8(__ldg(reinterpret_cast<const uint4*>(wp + c * 8)), w);
+  }
+  for (int base = 0; base < f.items; base += RPP) {
+    const int item = base + r0;
     float x[8];
-    const uint4 raw = *reinterpret_cast<const uint4*>(src + c * 8);
     unpack8(raw, x);
-    if (p.norm) {
+    // the next row's load is in flight while this one is worked on and stored
+    if (base + RPP < f.items) raw = *reinterpret_cast<const uint4*>(f.at(k, item + RPP) + c * 8);
+    int head, t;
+    k.split(item < f.items ? item : 0, &head, &t);
+    if (KIND != kValue && p.norm) {
       float ss = 0.f;
 #pragma unroll
       for (int i = 0; i < 8; ++i) ss = fmaf(x[i], x[i], ss);
 #pragma unroll
       for (int o = LPR / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-      if (kind != 2) {
-        const float r = rsqrtf(ss * (1.f / D) + p.eps);
-        const uint16_t* wp = kind == 0 ? p.q_weight : p.k_weight;
-        float w[8];
-        if (wp != nullptr) {
-          unpack8(*reinterpret_cast<const uint4*>(wp + c * 8), w);
-        } else {
+      const float r = rsqrtf(ss * (1.f / D) + p.eps);
 #pragma unroll
-          for (int i = 0; i < 8; ++i) w[i] = 1.f;
-        }
-#pragma unroll
-        for (int i = 0; i < 8; ++i) x[i] = x[i] * r * w[i];
-      }
+      for (int i = 0; i < 8; ++i) x[i] = x[i] * r * w[i];
     }
-    if (p.inv_freq != nullptr) {
+    if (KIND != kValue && p.inv_freq != nullptr) {
       const float2* tt = turns + t * half;
       if (p.interleaved) {
-        if (kind != 2 && c * 8 < p.rot) {
+        if (c * 8 < p.rot) {
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const float2 cs = tt[c * 4 + i];
-            const float a = x[2 * i], e = x[2 * i + 1];
+          for (int i = 0; i < 4; i += 2) {
+            const float4 cs = *reinterpret_cast<const float4*>(tt + c * 4 + i);
+            float a = x[2 * i], e = x[2 * i + 1];
             x[2 * i] = a * cs.x - e * cs.y;
             x[2 * i + 1] = e * cs.x + a * cs.y;
+            a = x[2 * i + 2], e = x[2 * i + 3];
+            x[2 * i + 2] = a * cs.z - e * cs.w;
+            x[2 * i + 3] = e * cs.z + a * cs.w;
           }
         }
       } else {
@@ -138,60 +162,166 @@ __global__ void __launch_bounds__(kRowThreads) saga_rows_kernel(const RowParams 
         float y[8];
 #pragma unroll
         for (int i = 0; i < 8; ++i) y[i] = __shfl_sync(0xffffffffu, x[i], peer, LPR);
-        if (kind != 2 && c < 2 * rc) {
-          const int f0 = (c < rc ? c : c - rc) * 8;
+        if (c < 2 * rc) {
+          const int fc = c < rc ? c : c - rc;
+          const float sign = c < rc ? -1.f : 1.f;
 #pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            const float2 cs = tt[f0 + i];
-            x[i] = c < rc ? x[i] * cs.x - y[i] * cs.y : x[i] * cs.x + y[i] * cs.y;
+          for (int i = 0; i < 8; i += 2) {
+            const float4 cs = *reinterpret_cast<const float4*>(tt + (fc << 3) + (((i >> 1) ^ (fc & 3)) << 1));
+            x[i] = fmaf(x[i], cs.x, sign * (y[i] * cs.y));
+            x[i + 1] = fmaf(x[i + 1], cs.z, sign * (y[i + 1] * cs.w));
           }
         }
       }
     }
-    const int slot = (int)((unsigned)start + (unsigned)(t0 + t));  // may wrap for a start that is no row: then it does not fit
-    const bool fits = (unsigned)slot < (unsigned)p.l_cap;
     float amax = 0.f;
-    if (E4M3) {
+    if (E4M3 && KIND != kQuery) {
 #pragma unroll
       for (int i = 0; i < 8; ++i) amax = fmaxf(amax, fabsf(x[i]));
 #pragma unroll
       for (int o = LPR / 2; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
       amax = fmaxf(amax, kAmaxFloor);
     }
-    if (!live) continue;
-    if (kind == 0) {
-      *reinterpret_cast<uint4*>(p.q_out + ((size_t)((size_t)b * p.tokens + t0 + t) * p.h_q + head) * D + c * 8) = pack8(x);
+    if (item >= f.items) continue;
+    if (KIND == kQuery) {
+      const size_t row = (size_t)((size_t)k.b * p.tokens + k.t0 + t) * p.h_q + head;
+      *reinterpret_cast<uint4*>(p.q_out + row * D + c * 8) = pack8(x);
       continue;
     }
-    if (!fits) {
+    int slot;
+    if (!k.slot(p, t, &slot)) {
       if (c == 0) flag_status(p.status, SAGA_STATUS_LEN_CLAMPED);
       continue;
     }
-    const size_t row = ((size_t)b * (kind == 1 ? p.h_k : p.h_v) + head) * p.l_cap + slot;
-    void* cache = kind == 1 ? p.k_cache : p.v_cache;
+    const size_t row = ((size_t)k.b * (KIND == kKey ? p.h_k : p.h_v) + head) * p.l_cap + slot;
+    void* cache = KIND == kKey ? p.k_cache : p.v_cache;
     if (E4M3) {
-      const float up = kE4m3Max / amax;
-      uint32_t w[2];
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(x[4 * h] * up, x[4 * h + 1] * up), __NV_SATFINITE, __NV_E4M3);
-        const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(x[4 * h + 2] * up, x[4 * h + 3] * up), __NV_SATFINITE, __NV_E4M3);
-        w[h] = lo | hi << 16;
-      }
-      *reinterpret_cast<uint2*>(static_cast<uint8_t*>(cache) + row * D + c * 8) = make_uint2(w[0], w[1]);
-      if (c == 0) (kind == 1 ? p.k_scale : p.v_scale)[row] = amax / kE4m3Max;
+      *reinterpret_cast<uint2*>(static_cast<uint8_t*>(cache) + row * D + c * 8) = codes8(x, kE4m3Max / amax);
+      if (c == 0) (KIND == kKey ? p.k_scale : p.v_scale)[row] = amax / kE4m3Max;
     } else {
-      // an untouched value row (or key row without norm and rotation) round-trips through fp32 exactly
+      // an untouched row round-trips through fp32 exactly
       *reinterpret_cast<uint4*>(static_cast<uint16_t*>(cache) + row * D + c * 8) = pack8(x);
     }
   }
 }
 
+// One CTA holds `group` tokens of one batch row and all their heads, queries
+// first, then keys, then values, each in a loop of its own without the others'
+// choices.  A row of a head (d elements) is D / 8 lanes of 16 bytes each, so
+// its sum of squares, its rotation partners and its largest magnitude are
+// shuffles.  The angles are the same for every head: they are computed once per
+// token into shared memory, while the first rows of each kind are on their way.
+// Rows are taken head by head, so neighbouring lanes write neighbouring cache
+// rows and scales.  For few tokens the time is that of one chain of loads; for
+// many it is bound by the instructions per row before HBM.
+template <int D, bool E4M3>
+__global__ void __launch_bounds__(kRowThreads) saga_rows_kernel(const RowParams p) {
+  constexpr int LPR = D / 8;
+  __shared__ __align__(16) float2 turns[kMaxRowTokens * (D / 2)];
+  pdl_trigger();
+  pdl_wait();
+  Tokens k;
+  if (!tokens_of(p, k)) return;
+  const int c = threadIdx.x % LPR, r0 = threadIdx.x / LPR;
+  const RowFeed<D, kQuery> fq(p, k);
+  const RowFeed<D, kKey> fk(p, k);
+  const RowFeed<D, kValue> fv(p, k);
+  const uint4 q0 = *reinterpret_cast<const uint4*>(fq.at(k, r0) + c * 8);
+  const uint4 k0 = *reinterpret_cast<const uint4*>(fk.at(k, r0) + c * 8);
+  const uint4 v0 = *reinterpret_cast<const uint4*>(fv.at(k, r0) + c * 8);
+  if (p.inv_freq != nullptr) {
+    const int half = p.rot >> 1;
+    for (int i = threadIdx.x; i < k.nt * half; i += kRowThreads) {
+      const int t = i / half, f = i - t * half;
+      const int pos = p.positions != nullptr ? p.positions[(size_t)k.b * p.tokens + k.t0 + t]
+                                             : (int)((unsigned)k.start + (unsigned)(k.t0 + t));
+      turns[t * half + turn_slot(f, p.interleaved)] = turn_of(pos, p.inv_freq[f]);
+    }
+    __syncthreads();
+  }
+  rows_of<D, E4M3, kQuery>(p, k, fq, q0, turns);
+  rows_of<D, E4M3, kKey>(p, k, fk, k0, turns);
+  rows_of<D, E4M3, kValue>(p, k, fv, v0, turns);
+}
+
+// Keys or values as they are into the cache (saga_kv_store), 32 bytes of a row
+// per thread: the quantisation is bound by its instructions, and a row's
+// magnitude, scale and addresses are then shared by 16 elements.
+template <int D, bool E4M3, int KIND>
+__device__ __forceinline__ void store_rows(const RowParams& p, const Tokens& k, const RowFeed<D, KIND>& f, uint4 a, uint4 b) {
+  constexpr int LPR = D / 16, RPP = kRowThreads / LPR;
+  const int c = threadIdx.x % LPR, r0 = threadIdx.x / LPR;
+  for (int base = 0; base < f.items; base += RPP) {
+    const int item = base + r0;
+    const uint4 now[2] = {a, b};
+    if (base + RPP < f.items) {
+      const uint4* src = reinterpret_cast<const uint4*>(f.at(k, item + RPP) + c * 16);
+      a = src[0];
+      b = src[1];
+    }
+    int head, t, slot;
+    k.split(item < f.items ? item : 0, &head, &t);
+    float amax = 0.f;
+    if (E4M3) {
+      // magnitudes as bf16 pairs: the maximum of two needs no widening
+      const uint32_t w[8] = {now[0].x, now[0].y, now[0].z, now[0].w, now[1].x, now[1].y, now[1].z, now[1].w};
+      uint32_t most = w[0] & 0x7fff7fffu;
+#pragma unroll
+      for (int i = 1; i < 8; ++i) most = __vmaxu2(most, w[i] & 0x7fff7fffu);
+      amax = __uint_as_float(max(most << 16, most & 0xffff0000u));
+#pragma unroll
+      for (int o = LPR / 2; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+      amax = fmaxf(amax, kAmaxFloor);
+    }
+    if (item >= f.items) continue;
+    if (!k.slot(p, t, &slot)) {
+      if (c == 0) flag_status(p.status, SAGA_STATUS_LEN_CLAMPED);
+      continue;
+    }
+    const size_t row = ((size_t)k.b * (KIND == kKey ? p.h_k : p.h_v) + head) * p.l_cap + slot;
+    void* cache = KIND == kKey ? p.k_cache : p.v_cache;
+    if (E4M3) {
+      const float up = kE4m3Max / amax;
+      float x[8];
+      unpack8(now[0], x);
+      const uint2 lo = codes8(x, up);
+      unpack8(now[1], x);
+      const uint2 hi = codes8(x, up);
+      *reinterpret_cast<uint4*>(static_cast<uint8_t*>(cache) + row * D + c * 16) = make_uint4(lo.x, lo.y, hi.x, hi.y);
+      if (c == 0) (KIND == kKey ? p.k_scale : p.v_scale)[row] = amax / kE4m3Max;
+    } else {
+      uint4* dst = reinterpret_cast<uint4*>(static_cast<uint16_t*>(cache) + row * D + c * 16);
+      dst[0] = now[0];
+      dst[1] = now[1];
+    }
+  }
+}
+
+template <int D, bool E4M3>
+__global__ void __launch_bounds__(kRowThreads) saga_store_kernel(const RowParams p) {
+  constexpr int LPR = D / 16;
+  pdl_trigger();
+  pdl_wait();
+  Tokens k;
+  if (!tokens_of(p, k)) return;
+  const int c = threadIdx.x % LPR, r0 = threadIdx.x / LPR;
+  const RowFeed<D, kKey> fk(p, k);
+  const RowFeed<D, kValue> fv(p, k);
+  const uint4* k0 = reinterpret_cast<const uint4*>(fk.at(k, r0) + c * 16);
+  const uint4* v0 = reinterpret_cast<const uint4*>(fv.at(k, r0) + c * 16);
+  const uint4 ka = k0[0], kb = k0[1], va = v0[0], vb = v0[1];
+  store_rows<D, E4M3, kKey>(p, k, fk, ka, kb);
+  store_rows<D, E4M3, kValue>(p, k, fv, va, vb);
+}
+
 // Codes of rows [start, start + rows) times their scales, rounded to bf16:
-// 16 codes per thread.
+// pieces of 8 codes, so that a warp's stores are 512 bytes on end, kPieces of
+// them in flight per thread (bound by HBM).
+constexpr int kPieces = 4;
+
 template <int D>
 __global__ void __launch_bounds__(256) saga_load_kernel(const LoadParams p) {
-  constexpr int TPR = D / 16;
+  constexpr int PPR = D / 8;  // pieces per row
   pdl_trigger();
   pdl_wait();
   int h = blockIdx.y;
@@ -203,23 +333,37 @@ __global__ void __launch_bounds__(256) saga_load_kernel(const LoadParams p) {
   if (out == nullptr) return;
   const int heads = key ? p.h_k : p.h_v;
   const int rows = p.lens != nullptr ? min(p.rows, max(p.lens[b], 0) - p.start) : p.rows;
-  const int r = (int)((blockIdx.x * 256u + threadIdx.x) / TPR), c = threadIdx.x % TPR;
-  if (r >= rows) return;
-  const size_t row = ((size_t)b * heads + h) * p.l_cap + p.start + r;
-  const uint4 u = *reinterpret_cast<const uint4*>((key ? p.k : p.v) + row * D + c * 16);
-  const float s = (key ? p.k_scale : p.v_scale)[row];
-  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-  float x[16];
+  const size_t row0 = ((size_t)b * heads + h) * p.l_cap + p.start;
+  const uint8_t* codes = (key ? p.k : p.v) + row0 * D;
+  const float* scales = (key ? p.k_scale : p.v_scale) + row0;
+  out += ((size_t)b * heads + h) * p.rows * D;
+  const long long pieces = (long long)max(rows, 0) * PPR, first = (long long)blockIdx.x * (256 * kPieces) + threadIdx.x;
+  uint2 u[kPieces];
+  float s[kPieces];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const __half2_raw hr = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(w[i >> 1] >> (16 * (i & 1))), __NV_E4M3);
-    const float2 f = __half22float2(__half2(hr));
-    x[2 * i] = f.x * s;
-    x[2 * i + 1] = f.y * s;
+  for (int i = 0; i < kPieces; ++i) {
+    const long long at = first + i * 256;
+    u[i] = make_uint2(0u, 0u);
+    s[i] = 0.f;
+    if (at < pieces) {
+      u[i] = __ldg(reinterpret_cast<const uint2*>(codes) + at);
+      s[i] = __ldg(scales + at / PPR);
+    }
   }
-  uint4* dst = reinterpret_cast<uint4*>(out + (((size_t)b * heads + h) * p.rows + r) * D + c * 16);
-  dst[0] = pack8(x);
-  dst[1] = pack8(x + 8);
+#pragma unroll
+  for (int i = 0; i < kPieces; ++i) {
+    const long long at = first + i * 256;
+    float x[8];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const uint32_t w = k < 2 ? u[i].x : u[i].y;
+      const __half2_raw hr = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(w >> (16 * (k & 1))), __NV_E4M3);
+      const float2 f = __half22float2(__half2(hr));
+      x[2 * k] = f.x * s[i];
+      x[2 * k + 1] = f.y * s[i];
+    }
+    if (at < pieces) *reinterpret_cast<uint4*>(out + at * 8) = pack8(x);
+  }
 }
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
@@ -316,19 +460,25 @@ int run_rows(const saga_shape* s, int tokens, const saga_rows* q, const saga_row
   int sms = 0;
   rc = api_device_sms(&sms);
   if (rc) return rc;
-  // Few tokens: one CTA each.  Many: up to kMaxRowTokens a CTA, as long as every SM keeps eight CTAs.
+  // Few tokens: one CTA each.  Many: up to `most` a CTA, as long as every SM keeps 8 CTAs.
+  const int most = q == nullptr ? 64 : kMaxRowTokens;
   int group = 1;
-  while (group < kMaxRowTokens && (long long)s->batch * ((tokens + 2 * group - 1) / (2 * group)) >= 8ll * sms) group *= 2;
+  while (group < most && (long long)s->batch * ((tokens + 2 * group - 1) / (2 * group)) >= 8ll * sms) group *= 2;
   p.group = group;
+  for (p.group_log2 = 0; 1 << p.group_log2 < group;) ++p.group_log2;
   p.groups = (tokens + group - 1) / group;
   const long long ctas = (long long)s->batch * p.groups;
   if (ctas >= (1ll << 31)) return api_fail(SAGA_ERR_UNSUPPORTED, "batch * tokens too large");
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   const bool e4m3 = cache->format == SAGA_CACHE_E4M3;
-  auto kernel = s->d == 64 ? (e4m3 ? saga_rows_kernel<64, true> : saga_rows_kernel<64, false>)
-                           : (e4m3 ? saga_rows_kernel<128, true> : saga_rows_kernel<128, false>);
-  static std::atomic<uint64_t> done[4];
-  cudaError_t e = prepare_kernel(reinterpret_cast<const void*>(kernel), 0, done[(s->d == 64 ? 0 : 2) + (e4m3 ? 1 : 0)]);
+  void (*const kernels[8])(RowParams) = {saga_rows_kernel<64, false>,  saga_store_kernel<64, false>,
+                                         saga_rows_kernel<64, true>,   saga_store_kernel<64, true>,
+                                         saga_rows_kernel<128, false>, saga_store_kernel<128, false>,
+                                         saga_rows_kernel<128, true>,  saga_store_kernel<128, true>};
+  const int which = (s->d == 64 ? 0 : 4) + (e4m3 ? 2 : 0) + (q == nullptr ? 1 : 0);
+  const auto kernel = kernels[which];
+  static std::atomic<uint64_t> done[8];
+  cudaError_t e = prepare_kernel(reinterpret_cast<const void*>(kernel), 0, done[which]);
   if (e == cudaSuccess) e = launch_pdl(kernel, dim3((unsigned)ctas), dim3(kRowThreads), 0, st, p);
   if (e != cudaSuccess) return api_cuda_fail(e, "row kernel launch");
   return api_ok();
@@ -385,8 +535,8 @@ int saga_kv_load(const saga_shape* s, const saga_cache* cache, int start, int ro
   p.rows = rows;
   const long long pairs = (long long)s->batch * (s->h_k + s->h_v);
   if (pairs > 65535) return api_fail(SAGA_ERR_UNSUPPORTED, "batch * (h_k + h_v) = %lld exceeds 65535", pairs);
-  const long long threads = (long long)rows * (s->d / 16);
-  const dim3 grid((unsigned)((threads + 255) / 256), (unsigned)pairs);
+  const long long threads = (long long)rows * (s->d / 8);
+  const dim3 grid((unsigned)((threads + 256 * kPieces - 1) / (256 * kPieces)), (unsigned)pairs);
   auto kernel = s->d == 64 ? saga_load_kernel<64> : saga_load_kernel<128>;
   static std::atomic<uint64_t> done[2];
   cudaError_t e = prepare_kernel(reinterpret_cast<const void*>(kernel), 0, done[s->d == 64 ? 0 : 1]);

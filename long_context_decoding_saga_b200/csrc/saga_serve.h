@@ -56,7 +56,8 @@ struct RowParams {
   float eps;
   int norm, rot, interleaved;
   int batch, tokens, h_q, h_k, h_v, l_cap;
-  int group;   // tokens of one CTA
+  int group;   // tokens of one CTA, a power of two
+  int group_log2;
   int groups;  // CTAs per batch row
 };
 
