@@ -28,8 +28,9 @@
 // given in pieces whose products add up in the same accumulators: q, scaled by
 // a power of two, as the sum of two e4m3 numbers (4 + 4 of bf16's 8 bits,
 // exact for all elements but those 2^-14 below the row's largest); the weights
-// as an e5m2 number and what it leaves as e4m3 (off by 2^-7 at most, finer than
-// the values' own 2^-4).  A key row's scale multiplies its scores and a value
+// as an e5m2 number, what it leaves as e4m3, and what that leaves as e4m3 again
+// (2^-3, 2^-4 and 2^-4 of what is left: off by 2^-11 at most.  Without the third
+// the error of an output over a long cache was twice that of rounding it).  A key row's scale multiplies its scores and a value
 // row's scale its weights, both in fp32 and before any rounding; the sums of
 // weights are fp32 sums of the unrounded ones.
 #include <cuda_bf16.h>
@@ -219,6 +220,9 @@ __device__ __forceinline__ uint32_t pack_half(float a, float b) {
 __device__ __forceinline__ uint32_t pack_e4m3(__half2 x) {
   return __nv_cvt_halfraw2_to_fp8x2(static_cast<__half2_raw>(x), __NV_SATFINITE, __NV_E4M3);
 }
+__device__ __forceinline__ __half2 half2_of_e4m3(uint32_t x) {
+  return __half2(__nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)x, __NV_E4M3));
+}
 // Two numbers as an 8-bit format each, in the low 16 bits, and back.
 __device__ __forceinline__ uint32_t pack_8bit(float a, float b, __nv_fp8_interpretation_t f) {
   return __nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, f);
@@ -394,7 +398,7 @@ __device__ __forceinline__ float octet_sum(const float* v, int lane) {
 
 // Weights of a tile into P; returns the largest exponent of the thread's.
 // bf16: a row of P is 16 bytes per 8 columns.  8-bit: 8 bytes per 8 columns of
-// each piece, the second piece `piece` bytes on; and the weights' sums over the
+// each of three pieces, `piece` bytes apart; and the weights' sums over the
 // warp's rows into here[column] (a tile that is done again overwrites them).
 // The pieces are taken in half precision, whose upper byte is an e5m2 number:
 // the first is that byte rounded, the rest an exact subtraction away.  (From
@@ -430,7 +434,7 @@ __device__ __forceinline__ float weigh(uint32_t s_tmem, uint8_t* p_row, int piec
 #pragma unroll
       for (int i = 1; i < 8; ++i) most = fmaxf(most, s[i]);
       top = fmaxf(top, most + __log2f(fmaxf(vs, kMinScale)));
-      uint32_t w[4], z[4];
+      uint32_t w[4], z[4], y[4];
 #pragma unroll
       for (int i = 0; i < 8; ++i) s[i] = ex2(s[i]);
 #pragma unroll
@@ -441,10 +445,12 @@ __device__ __forceinline__ float weigh(uint32_t s_tmem, uint8_t* p_row, int piec
         w[i] = (all + 0x00800080u) & 0xff00ff00u;
         const __half2 rest = __hsub2(as_half2(all), as_half2(w[i]));
         z[i] = pack_e4m3(rest);
+        y[i] = pack_e4m3(__hsub2(rest, half2_of_e4m3(z[i])));
       }
       uint8_t* at = p_row + (col >> 4) * 2048 + (col & 8);
       *reinterpret_cast<uint2*>(at) = make_uint2(__byte_perm(w[0], w[1], 0x7531), __byte_perm(w[2], w[3], 0x7531));
       *reinterpret_cast<uint2*>(at + piece) = make_uint2(z[0] | z[1] << 16, z[2] | z[3] << 16);
+      *reinterpret_cast<uint2*>(at + 2 * piece) = make_uint2(y[0] | y[1] << 16, y[2] | y[3] << 16);
       const float sum = octet_sum(s, lane);
       if ((lane & 3) == 0) here[col + octet_column(lane)] = sum;
     }
@@ -611,7 +617,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
     if (any) {
       const uint32_t id_s = E4M3 ? idesc(kE4m3, kE4m3, kTreeTile, cols, false) : idesc(kBf16, kBf16, kTreeTile, cols, false);
       const uint32_t id_o = E4M3 ? idesc(kE4m3, kE5m2, D, p.plan.nvp, true) : idesc(kBf16, kBf16, 128, p.plan.nvp, true);
-      const uint32_t id_o2 = idesc(kE4m3, kE4m3, D, p.plan.nvp, true);  // the weights' second piece
+      const uint32_t id_o2 = idesc(kE4m3, kE4m3, D, p.plan.nvp, true);  // the weights' other pieces
       const uint32_t id_l = idesc(kBf16, kBf16, 64, cols, true);
       const uint32_t ones = smem_u32(smem + L.ones), ring0 = smem_u32(smem);
       const uint64_t q_desc = desc_rows<D, E4M3>(smem_u32(smem + L.q));
@@ -680,6 +686,9 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
 #pragma unroll
                 for (int k = 0; k < kTreeTile / 32; ++k)
                   umma_8bit(d, a + k * (D * 2), b + cols * 8 + k * 32, id_o2, 1u);
+#pragma unroll
+                for (int k = 0; k < kTreeTile / 32; ++k)
+                  umma_8bit(d, a + k * (D * 2), b + cols * 16 + k * 32, id_o2, 1u);
               } else {
 #pragma unroll
                 for (int k = 0; k < kTreeTile / 16; ++k)

@@ -250,8 +250,8 @@ __host__ __device__ inline bool tree_row(const TreePlan& p, int T, int chunk, in
 }
 
 // Shared memory of the kernel: the tile ring, ones (the operand that adds bf16
-// weights up), Q and two P buffers (16 bits an element: bf16, or two 8-bit
-// pieces one after the other), per-column words, and for 8-bit caches the rows'
+// weights up), Q (bf16, or two 8-bit pieces one after the other), two P buffers
+// (bf16, or three 8-bit pieces), per-column words, and for 8-bit caches the rows'
 // scales of two tiles and the sums of weights.
 struct TreeSmem {
   int stages, stage_bytes;
@@ -262,7 +262,7 @@ __host__ __device__ inline TreeSmem tree_smem(const TreePlan& p, int d, bool e4m
   s.stage_bytes = kTreeTile * d * (e4m3 ? 1 : 2);
   const int budget = 227 * 1024 - 1024;  // less the slack that aligns the base to 1024 bytes
   const int q_bytes = p.cols * d * 2;
-  s.p_bytes = p.cols * kTreeTile * 2;
+  s.p_bytes = p.cols * kTreeTile * (e4m3 ? 3 : 2);
   const int words = p.cols * (8 + 5 * 4 + 4 * 4);
   const int eight = e4m3 ? 2 * p.cols * 4 * 4 + 2 * 2 * (1 + p.nv) * kTreeTile * 4 : 0;
   const int bar_bytes = 8 * (3 * kTreeMaxStages + 16) + 16 + (int)(sizeof(TreeWalk) + sizeof(TreeCut));
