@@ -476,21 +476,23 @@ __device__ __forceinline__ void maxima(uint32_t s_tmem, float* words, Groups g, 
   }
 }
 
-// ------------------------------------------------------------------ the kernel
-// Warp 0: TMA loads of the tiles.  Warp 1: the products, issued by one lane.
-// Warps 4 .. 11: two warpgroups, each half of the column groups of every tile.
-// Ring order: K of tile 0, then for each tile K of the next one and its own
-// value heads, so that the next tile's scores are there while a tile's weights
-// are computed.
-template <int D, bool E4M3>
-__global__ void __launch_bounds__(kTreeThreads, 1)
-    saga_tree_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
-                     const TreeParams p) {
-  extern __shared__ uint8_t smem_raw[];
-  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  const TreeSmem& L = p.smem;
+// ------------------------------------------------------------------ parts of both kernels
+// A CTA's shared memory by name, and its place.
+struct Block {
+  uint8_t* smem;
   Bars bar;
-  bar.full = reinterpret_cast<uint64_t*>(smem + L.bars);
+  uint32_t* tmem_slot;
+  volatile int* abort_flag;
+  TreeWalk* share;  // left == 0: this CTA has no tiles
+  TreeCut* share_cut;
+  int warp, lane;
+};
+
+__device__ __forceinline__ Block block_of(const TreeParams& p, uint8_t* smem_raw) {
+  Block k;
+  k.smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  Bars& bar = k.bar;
+  bar.full = reinterpret_cast<uint64_t*>(k.smem + p.smem.bars);
   bar.empty = bar.full + kTreeMaxStages;
   bar.vfix = bar.empty + kTreeMaxStages;
   bar.s_full = bar.vfix + kTreeMaxStages;
@@ -499,20 +501,24 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
   bar.pv_done = bar.p_full + 2;
   bar.q_full = bar.pv_done + 2;
   bar.drain = bar.q_full + 1;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bar.drain + 1);
-  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
-  TreeWalk* share = reinterpret_cast<TreeWalk*>(tmem_slot + 2);  // left == 0: this CTA has no tiles
-  TreeCut* share_cut = reinterpret_cast<TreeCut*>(share + 1);
-  const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
-  const int stages = L.stages;
-  const int cols = p.plan.cols;
-  // two score buffers, the accumulators, and bf16 weights' sums (d = 64: lanes 64 .. 127 of the accumulators)
-  const int used = (D == 64 || E4M3 ? 3 : 4) * cols;
-  const uint32_t tmem_cols = used <= 64 ? 64u : used <= 128 ? 128u : used <= 256 ? 256u : 512u;
+  k.tmem_slot = reinterpret_cast<uint32_t*>(bar.drain + 1);
+  k.abort_flag = reinterpret_cast<volatile int*>(k.tmem_slot + 1);
+  k.share = reinterpret_cast<TreeWalk*>(k.tmem_slot + 2);
+  k.share_cut = reinterpret_cast<TreeCut*>(k.share + 1);
+  k.warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0);
+  k.lane = threadIdx.x & 31;
+  return k;
+}
 
+// Barriers, TMEM, and after the dependency wait this CTA's run of the line.
+template <int D>
+__device__ __forceinline__ void block_start(const TreeParams& p, const Block& k, const CUtensorMap* kmap,
+                                            const CUtensorMap* vmap, uint32_t tmem_cols) {
+  const Bars& bar = k.bar;
+  const int warp = k.warp, lane = k.lane;
   if (threadIdx.x == 0) {
-    *abort_flag = 0;
-    for (int i = 0; i < stages; ++i) {
+    *k.abort_flag = 0;
+    for (int i = 0; i < p.smem.stages; ++i) {
       mbar_init(&bar.full[i], 1);
       mbar_init(&bar.empty[i], 1);
       mbar_init(&bar.vfix[i], 4);
@@ -526,17 +532,12 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
     mbar_init(bar.q_full, 8);
     mbar_init(bar.drain, 32);
     mbar_init_fence();
-    tma_prefetch_desc(&kmap);
-    tma_prefetch_desc(&vmap);
+    tma_prefetch_desc(kmap);
+    tma_prefetch_desc(vmap);
   }
   if (warp == 1) {
-    tmem_alloc(tmem_slot, tmem_cols);
+    tmem_alloc(k.tmem_slot, tmem_cols);
     tmem_relinquish();
-  }
-  if (warp == 2 || warp == 3) {
-    for (int i = threadIdx.x - 64; i < 2048 / 16; i += 64)
-      *reinterpret_cast<uint4*>(smem + L.ones + i * 16) = make_uint4(0x3f803f80u, 0x3f803f80u, 0x3f803f80u, 0x3f803f80u);
-    fence_proxy_async_shared();
   }
   if (warp == 3) {
     // lines that the start needs, into L2 before the dependency wait: a prefetch moves no values
@@ -558,7 +559,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
     const TreeCut cut = cut_of(line, p.batch, p.ctas, &clamped);
     if (blockIdx.x == 0 && clamped) flag_status(p.status, SAGA_STATUS_LEN_CLAMPED);
     const int at = tree_start(cut, blockIdx.x);
-    if (lane == 0) share->left = 0;
+    if (lane == 0) k.share->left = 0;
     __syncwarp();
     int base = 0;
     for (int b0 = 0; b0 < p.batch && at >= 0; b0 += 32) {
@@ -569,8 +570,8 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
       const unsigned hit = __ballot_sync(0xffffffffu, base + incl > at);
       if (hit != 0u) {
         if (lane == __ffs(hit) - 1) {
-          *share = tree_walk_begin(line, cut, blockIdx.x, b0 + lane, at - (base + incl - mine), P, n);
-          *share_cut = cut;
+          *k.share = tree_walk_begin(line, cut, blockIdx.x, b0 + lane, at - (base + incl - mine), P, n);
+          *k.share_cut = cut;
         }
         break;
       }
@@ -580,39 +581,125 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = *tmem_slot;
+}
+
+// Warp 0: the tiles' loads.  Returns how many were issued.
+template <int D, bool E4M3>
+__device__ __forceinline__ int load_tiles(const TreeParams& p, const Block& k, const CUtensorMap* kmap,
+                                          const CUtensorMap* vmap, TreeWalk w) {
+  int issued = 0;
+  Ring r;
+  bool ok = true;
+  auto load = [&](const CUtensorMap* map, size_t row) {
+    if (!ok) return;
+    if (r.round > 0) ok = __all_sync(0xffffffffu, mbar_wait(&k.bar.empty[r.st], (r.round - 1) & 1, k.abort_flag));
+    if (!ok) return;
+    if (elect_one()) {
+      mbar_arrive_expect_tx(&k.bar.full[r.st], (uint32_t)p.smem.stage_bytes);
+#pragma unroll
+      for (int h = 0; h < (E4M3 ? 1 : D / 64); ++h)
+        tma_load_2d(k.smem + r.st * p.smem.stage_bytes + h * (kTreeTile * 128), map, &k.bar.full[r.st], h * 64, (int)row);
+    }
+    __syncwarp();
+    r.step(p.smem.stages);
+    ++issued;
+  };
+  do {
+    const Heads h = heads_of(p, w);
+    load(kmap, h.key + (size_t)w.t0 * kTreeTile);
+    for (int t = w.t0; t < w.t1; ++t) {
+      if (t + 1 < w.t1) load(kmap, h.key + (size_t)(t + 1) * kTreeTile);
+      for (int v = 0; v < h.nv; ++v) load(vmap, h.value + (size_t)v * p.l_cap + (size_t)t * kTreeTile);
+    }
+  } while (ok && tree_walk_next(line_of(p), w));
+  return issued;
+}
+
+// The first warpgroup, after its part of a tile with rows past the prefix: value
+// rows that no token sees may hold anything, so they become zeros before the
+// product reads them.  `bad`: this thread's row is one; vr: the ring's place of
+// the tile's first value head.
+template <int D, bool E4M3>
+__device__ __forceinline__ void zero_unseen(const TreeParams& p, const Block& k, Ring vr, int nv, int r, bool bad) {
+  for (int v = 0; v < nv; ++v) {
+    if (!__all_sync(0xffffffffu, mbar_wait(&k.bar.full[vr.st], vr.round & 1, k.abort_flag))) break;
+    if (bad) {
+#pragma unroll
+      for (int i = 0; i < (E4M3 ? D / 16 : D / 8); ++i) {  // neighbouring rows at different banks
+        uint8_t* line = k.smem + vr.st * p.smem.stage_bytes +
+                        (E4M3 ? r * D + ((i + r) & (D / 16 - 1)) * 16
+                              : (i >> 3) * (kTreeTile * 128) + r * 128 + ((i + r) & 7) * 16);
+        *reinterpret_cast<uint4*>(line) = make_uint4(0u, 0u, 0u, 0u);
+      }
+      fence_proxy_async_shared();
+    }
+    __syncwarp();
+    if (k.lane == 0) mbar_arrive(&k.bar.vfix[vr.st]);
+    vr.step(p.smem.stages);
+  }
+  __syncwarp();
+}
+
+// Everything has come to its end, or to a wait that gave up: then what is in
+// flight lands before the memory is given back.
+__device__ __forceinline__ void block_end(const TreeParams& p, const Block& k, int issued, uint32_t tmem, uint32_t tmem_cols) {
+  tc_fence_before();
+  __syncthreads();
+  if (*k.abort_flag != 0) {
+    if (threadIdx.x == 0) {
+      flag_status(p.status, SAGA_STATUS_TIMEOUT);
+      // loads still in flight land before the shared memory is given up
+      for (int x = issued > p.smem.stages ? issued - p.smem.stages : 0; x < issued; ++x)
+        mbar_wait_drain(&k.bar.full[x % p.smem.stages], (x / p.smem.stages) & 1);
+    }
+    if (k.warp == 1) {  // and so do the products (every lane may have issued some)
+      umma_commit(k.bar.drain);
+      mbar_wait_drain(k.bar.drain, 0);
+    }
+  }
+  __syncthreads();
+  if (k.warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem, tmem_cols);
+  }
+}
+
+// ------------------------------------------------------------------ the kernel
+// Warp 0: TMA loads of the tiles.  Warp 1: the products, issued by one lane.
+// Warps 4 .. 11: two warpgroups, each half of the column groups of every tile.
+// Ring order: K of tile 0, then for each tile K of the next one and its own
+// value heads, so that the next tile's scores are there while a tile's weights
+// are computed.
+template <int D, bool E4M3>
+__global__ void __launch_bounds__(kTreeThreads, 1)
+    saga_tree_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
+                     const TreeParams p) {
+  extern __shared__ uint8_t smem_raw[];
+  const Block k = block_of(p, smem_raw);
+  const Bars& bar = k.bar;
+  uint8_t* const smem = k.smem;
+  volatile int* const abort_flag = k.abort_flag;
+  const TreeSmem& L = p.smem;
+  const int warp = k.warp, lane = k.lane;
+  const int stages = L.stages;
+  const int cols = p.plan.cols;
+  // two score buffers, the accumulators, and bf16 weights' sums (d = 64: lanes 64 .. 127 of the accumulators)
+  const int used = (D == 64 || E4M3 ? 3 : 4) * cols;
+  const uint32_t tmem_cols = used <= 64 ? 64u : used <= 128 ? 128u : used <= 256 ? 256u : 512u;
+  if (warp == 2 || warp == 3) {
+    for (int i = threadIdx.x - 64; i < 2048 / 16; i += 64)
+      *reinterpret_cast<uint4*>(smem + L.ones + i * 16) = make_uint4(0x3f803f80u, 0x3f803f80u, 0x3f803f80u, 0x3f803f80u);
+    fence_proxy_async_shared();
+  }
+  block_start<D>(p, k, &kmap, &vmap, tmem_cols);
+  const uint32_t tmem = *k.tmem_slot;
   const uint32_t o_tmem = tmem + 2 * cols, l_tmem = tmem + 3 * cols;
   int issued = 0;  // TMA loads (warp 0)
-  TreeWalk w = *share;
+  TreeWalk w = *k.share;
   const bool any = w.left > 0;
 
   if (warp == 0) {
-    if (any) {
-      Ring r;
-      bool ok = true;
-      auto load = [&](const CUtensorMap* map, size_t row) {
-        if (!ok) return;
-        if (r.round > 0) ok = __all_sync(0xffffffffu, mbar_wait(&bar.empty[r.st], (r.round - 1) & 1, abort_flag));
-        if (!ok) return;
-        if (elect_one()) {
-          mbar_arrive_expect_tx(&bar.full[r.st], (uint32_t)L.stage_bytes);
-#pragma unroll
-          for (int h = 0; h < (E4M3 ? 1 : D / 64); ++h)
-            tma_load_2d(smem + r.st * L.stage_bytes + h * (kTreeTile * 128), map, &bar.full[r.st], h * 64, (int)row);
-        }
-        __syncwarp();
-        r.step(stages);
-        ++issued;
-      };
-      do {
-        const Heads h = heads_of(p, w);
-        load(&kmap, h.key + (size_t)w.t0 * kTreeTile);
-        for (int t = w.t0; t < w.t1; ++t) {
-          if (t + 1 < w.t1) load(&kmap, h.key + (size_t)(t + 1) * kTreeTile);
-          for (int v = 0; v < h.nv; ++v) load(&vmap, h.value + (size_t)v * p.l_cap + (size_t)t * kTreeTile);
-        }
-      } while (ok && tree_walk_next(line_of(p), w));
-    }
+    if (any) issued = load_tiles<D, E4M3>(p, k, &kmap, &vmap, w);
   } else if (warp == 1) {
     if (any) {
       const uint32_t id_s = E4M3 ? idesc(kE4m3, kE4m3, kTreeTile, cols, false) : idesc(kBf16, kBf16, kTreeTile, cols, false);
@@ -840,7 +927,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
       // for the join: the CTAs that hold the item (even runs: the line's tile at which it begins is the run's first
       // and what the run has done so far)
       if (et == 0 && w.t0 == 0) {
-        const TreeCut cut = *share_cut;
+        const TreeCut cut = *k.share_cut;
         const int place = cut.by_items ? 0 : tree_even_first(cut, blockIdx.x) + gt;
         p.holders[w.item] = make_int2(blockIdx.x, tree_last_holder(cut, blockIdx.x, w.tiles, place));
       }
@@ -965,27 +1052,9 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
             if (lane < 8) sums[g.col + lane] += sums_here[g.col + lane];
         }
         if (tail && wg == 0) {
-          // value rows that no token sees may hold anything: zero them before the product reads them
-          const bool bad = !row_seen(w, seen, row);
           Ring vr = seg_ring;
           vr.jump(tree_value_place(i, nt, h.nv), stages);
-          for (int v = 0; v < h.nv; ++v) {
-            if (!__all_sync(0xffffffffu, mbar_wait(&bar.full[vr.st], vr.round & 1, abort_flag))) break;
-            if (bad) {
-#pragma unroll
-              for (int k = 0; k < (E4M3 ? D / 16 : D / 8); ++k) {  // neighbouring rows at different banks
-                uint8_t* line = smem + vr.st * L.stage_bytes +
-                                (E4M3 ? r * D + ((k + r) & (D / 16 - 1)) * 16
-                                      : (k >> 3) * (kTreeTile * 128) + r * 128 + ((k + r) & 7) * 16);
-                *reinterpret_cast<uint4*>(line) = make_uint4(0u, 0u, 0u, 0u);
-              }
-              fence_proxy_async_shared();
-            }
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&bar.vfix[vr.st]);
-            vr.step(stages);
-          }
-          __syncwarp();
+          zero_unseen<D, E4M3>(p, k, vr, h.nv, r, !row_seen(w, seen, row));
         }
       }
       if (!ok) break;
@@ -1064,25 +1133,399 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
     } while (tree_walk_next(line_of(p), w));
   }
 
-  tc_fence_before();
-  __syncthreads();
-  if (*abort_flag != 0) {
-    if (threadIdx.x == 0) {
-      flag_status(p.status, SAGA_STATUS_TIMEOUT);
-      // loads still in flight land before the shared memory is given up
-      for (int x = issued > stages ? issued - stages : 0; x < issued; ++x)
-        mbar_wait_drain(&bar.full[x % stages], (x / stages) & 1);
-    }
-    if (warp == 1) {  // and so do the products (every lane may have issued some)
-      umma_commit(bar.drain);
-      mbar_wait_drain(bar.drain, 0);
+  block_end(p, k, issued, tmem, tmem_cols);
+}
+
+// ------------------------------------------------------------------ queries as rows
+// For chunks with many query rows (bf16 caches): the products the other way
+// round,
+//   S[query, row] = q . K      M = 128 queries, N = 128 rows of the tile
+//   O[query, d]  += P V        P from TMEM, where it takes its scores' place,
+// so that a thread has a query and its reference, threshold and sum in
+// registers, no column words are read, and the weights never go through shared
+// memory, which the products' operands fill by then: with 128 columns the
+// kernel above takes 1.6 us per tile of d = 64, two thirds of it the weights'.
+// Each value head of the chunk takes all 128 rows of P and a share of the
+// columns of O, of which its own rows are kept; that costs products, of which
+// there is room.  Two warpgroups, each half of the tile's rows.
+
+__device__ __forceinline__ void umma_bf16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc, uint32_t id, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "r"(a_tmem), "l"(bdesc), "r"(id), "r"(accumulate)
+      : "memory");
+}
+
+// 32 columns of this thread's lane.
+__device__ __forceinline__ void tmem_ld32(uint32_t taddr, float* v) {
+  uint32_t r[32];
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+      "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];\n\t"
+      "tcgen05.wait::ld.sync.aligned;"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
+        "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
+        "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(taddr));
+#pragma unroll
+  for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
+}
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t* r) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
+      "%15};" ::"r"(r[0]),
+      "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]),
+      "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(taddr)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+// A thread's query.
+struct Query {
+  float nm;                // its reference, negated
+  float tau;               // its threshold
+  unsigned long long sees; // of the 64 cache rows in hand, with TEST
+};
+
+// 32 scores into exponents relative to the reference (RELATIVE) or not; bits:
+// which of them the query sees.
+template <bool TEST, bool RELATIVE>
+__device__ __forceinline__ void row_exponents(float* s, const Query& q, uint32_t bits, float scale) {
+  const float f = TEST ? scale : scale * kLog2e, nm = RELATIVE ? q.nm : 0.f;
+  const unsigned long long ff = two(f, f), ll = two(kLog2e, kLog2e), mm = two(nm, nm);
+#pragma unroll
+  for (int i = 0; i < 32; i += 2) {
+    unsigned long long x = two(s[i], s[i + 1]);
+    if (TEST) {
+      x = mul2(x, ff);
+      float a, b;
+      untwo(x, a, b);
+      const bool keep0 = a >= q.tau && (bits >> i & 1u) != 0u, keep1 = b >= q.tau && (bits >> i & 2u) != 0u;
+      x = RELATIVE ? fma2(x, ll, mm) : mul2(x, ll);
+      untwo(x, s[i], s[i + 1]);
+      s[i] = keep0 ? s[i] : -INFINITY;
+      s[i + 1] = keep1 ? s[i + 1] : -INFINITY;
+    } else {
+      x = RELATIVE ? fma2(x, ff, mm) : mul2(x, ff);
+      untwo(x, s[i], s[i + 1]);
     }
   }
-  __syncthreads();
-  if (warp == 1) {
-    tc_fence_after();
-    tmem_dealloc(tmem, tmem_cols);
+}
+
+// 64 scores into 32 words of weights; their sum, and the largest exponent.
+template <bool TEST>
+__device__ __forceinline__ void row_weights(uint32_t s_tmem, const Query& q, float scale, uint32_t* w, float* sum, float* top) {
+  float most = -INFINITY;
+  unsigned long long add[2] = {0ull, 0ull};
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    float s[32];
+    tmem_ld32(s_tmem + h * 32, s);
+    row_exponents<TEST, true>(s, q, (uint32_t)(q.sees >> (h * 32)), scale);
+#pragma unroll
+    for (int i = 0; i < 32; ++i) {
+      most = fmaxf(most, s[i]);
+      s[i] = ex2(s[i]);
+    }
+#pragma unroll
+    for (int i = 0; i < 32; i += 2) {
+      const uint32_t y = pack_bf16(s[i], s[i + 1]);
+      w[h * 16 + (i >> 1)] = y;
+      // the sum of the rounded weights, as the other kernel's row of ones gives it
+      add[i >> 1 & 1] = fma2(two(__uint_as_float(y << 16), __uint_as_float(y & 0xffff0000u)), two(1.f, 1.f), add[i >> 1 & 1]);
+    }
   }
+  float a, b, c, d;
+  untwo(add[0], a, b);
+  untwo(add[1], c, d);
+  *sum = (a + b) + (c + d);
+  *top = most;
+}
+
+template <bool TEST>
+__device__ __forceinline__ float row_maximum(uint32_t s_tmem, const Query& q, float scale) {
+  float most = -INFINITY;
+#pragma unroll 1
+  for (int h = 0; h < 2; ++h) {
+    float s[32];
+    tmem_ld32(s_tmem + h * 32, s);
+    row_exponents<TEST, false>(s, q, (uint32_t)(q.sees >> (h * 32)), scale);
+#pragma unroll
+    for (int i = 0; i < 32; ++i) most = fmaxf(most, s[i]);
+  }
+  return most;
+}
+
+template <int D>
+__global__ void __launch_bounds__(kTreeThreads, 1)
+    saga_tree_rows_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
+                          const TreeParams p) {
+  extern __shared__ uint8_t smem_raw[];
+  const Block k = block_of(p, smem_raw);
+  const Bars& bar = k.bar;
+  uint8_t* const smem = k.smem;
+  volatile int* const abort_flag = k.abort_flag;
+  const TreeSmem& L = p.smem;
+  const int warp = k.warp, lane = k.lane, stages = L.stages;
+  block_start<D>(p, k, &kmap, &vmap, 512);
+  const uint32_t tmem = *k.tmem_slot;
+  const uint32_t o_tmem = tmem + 2 * kTreeTile;  // after two score buffers: d columns for each value head
+  int issued = 0;                                // TMA loads (warp 0)
+  TreeWalk w = *k.share;
+  const bool any = w.left > 0;
+
+  if (warp == 0) {
+    if (any) issued = load_tiles<D, false>(p, k, &kmap, &vmap, w);
+  } else if (warp == 1) {
+    if (any) {
+      const uint32_t id_s = idesc(kBf16, kBf16, 128, kTreeTile, false);
+      const uint32_t id_o = idesc(kBf16, kBf16, 128, D, false) | 1u << 16;  // V as it lies: its rows are the inner dimension
+      const uint32_t ring0 = smem_u32(smem);
+      const uint64_t q_desc = desc_rows<D, false>(smem_u32(smem + L.q));
+      Ring r;
+      uint32_t fixed = 0;  // parity of each stage's vfix barrier
+      int gs = 0, gp = 0, seg = 0;  // score products, value products, segments so far
+      bool ok = true;
+      auto wait = [&](uint64_t* b, uint32_t parity) { return __all_sync(0xffffffffu, mbar_wait(b, parity, abort_flag)); };
+      auto scores = [&]() {
+        if (!wait(&bar.full[r.st], r.round & 1)) return false;
+        // the buffer held the weights of two tiles before, until their product was done
+        if (gs >= 2 && !wait(&bar.pv_done[gs & 1], ((gs >> 1) - 1) & 1)) return false;
+        tc_fence_after();
+        const uint64_t k_desc = desc_rows<D, false>(ring0 + r.st * L.stage_bytes);
+        if (elect_one()) {
+#pragma unroll
+          for (int i = 0; i < D / 16; ++i) {  // 64-column halves 16 KB apart in both
+            const uint32_t at = (i >> 2) * (kTreeTile * 128 / 16) + (i & 3) * 2;
+            umma_bf16(tmem + (gs & 1) * kTreeTile, q_desc + at, k_desc + at, id_s, i > 0);
+          }
+          umma_commit(&bar.empty[r.st]);
+          umma_commit(&bar.s_full[gs & 1]);
+        }
+        __syncwarp();
+        r.step(stages);
+        ++gs;
+        return true;
+      };
+      do {
+        const Heads h = heads_of(p, w);
+        ok = wait(bar.q_full, seg & 1);
+        ++seg;
+        tc_fence_after();
+        ok = ok && scores();
+        for (int t = w.t0; ok && t < w.t1; ++t) {
+          if (t + 1 < w.t1) ok = scores();
+          ok = ok && wait(&bar.p_full[gp & 1], (gp >> 1) & 1);
+          const bool fix = (t + 1) * kTreeTile > w.P;
+          const uint32_t first = t > w.t0 ? 1u : 0u, a = tmem + (gp & 1) * kTreeTile;
+          for (int v = 0; ok && v < h.nv; ++v) {
+            ok = wait(&bar.full[r.st], r.round & 1);
+            if (ok && fix) {
+              ok = wait(&bar.vfix[r.st], fixed >> r.st & 1);
+              fixed ^= 1u << r.st;
+            }
+            if (!ok) break;
+            tc_fence_after();
+            const uint64_t b = desc_v<D, false>(ring0 + r.st * L.stage_bytes, kTreeTile * 128);
+            if (elect_one()) {
+#pragma unroll
+              for (int i = 0; i < kTreeTile / 16; ++i)  // each warpgroup's 64 rows of weights: 32 columns, 64 apart
+                umma_bf16_ts(o_tmem + v * D, a + (i >> 2) * 64 + (i & 3) * 8, b + i * 128, id_o, i > 0 ? 1u : first);
+              umma_commit(&bar.empty[r.st]);
+            }
+            __syncwarp();
+            r.step(stages);
+          }
+          if (!ok) break;
+          if (elect_one()) umma_commit(&bar.pv_done[gp & 1]);
+          __syncwarp();
+          ++gp;
+        }
+      } while (ok && tree_walk_next(line_of(p), w));
+    }
+  } else if (warp >= kEpiWarp0) {
+    const int wg = (warp - kEpiWarp0) >> 2, quarter = warp & 3;
+    const int r = quarter * 32 + lane;            // query row, and the cache row of a tile that this thread may zero
+    const int et = threadIdx.x - kEpiWarp0 * 32;  // 0 .. 255
+    int* out_row = reinterpret_cast<int*>(smem + L.row);
+    float* words = reinterpret_cast<float*>(smem + L.words);  // [2][128]
+    const uint32_t lanes = (uint32_t)(quarter * 32) << 16;
+    const int G = p.h_q / p.h_k;
+    int gt = 0;  // tiles so far
+    Ring seg_ring;
+    bool ok = true;
+    if (any) do {
+      const Heads h = heads_of(p, w);
+      const int nt = w.t1 - w.t0;
+      const unsigned long long all = w.n >= 64 ? ~0ull : (1ull << w.n) - 1ull;
+      int my_row = -1;
+      float my_tau = INFINITY;
+      unsigned long long my_mask = 0ull;
+      {
+        int jj, t;
+        if (tree_row(p.plan, p.tokens, h.chunk, r, &jj, &t) && t < w.n) {
+          my_row = (w.b * p.tokens + t) * p.h_q + h.kh * G + jj;
+          my_tau = p.tau != nullptr ? p.tau[w.b * p.h_q + h.kh * G + jj] : -INFINITY;
+          my_mask = all & (p.mask != nullptr ? p.mask[(size_t)w.b * p.tokens + t] : (2ull << t) - 1ull);
+        }
+      }
+      const bool idle = !__any_sync(0xffffffffu, my_row >= 0);  // a warp without queries: its rows of O are garbage
+      if (wg == 0) out_row[r] = my_row;  // read below only, since the last segment's barriers
+      named_bar_sync(3, kEpiAll);
+      constexpr int LPR = D / 8, STEP = kEpiAll / LPR, FLIGHT = 4;
+      const int c = et % LPR;
+#pragma unroll 1
+      for (int row0 = et / LPR; row0 - et / LPR < kTreeMaxCols; row0 += FLIGHT * STEP) {
+        uint4 x[FLIGHT];
+#pragma unroll
+        for (int i = 0; i < FLIGHT; ++i) {
+          const int row = out_row[row0 + i * STEP];
+          x[i] = make_uint4(0u, 0u, 0u, 0u);
+          if (row >= 0) x[i] = __ldg(reinterpret_cast<const uint4*>(p.q + (size_t)row * D + c * 8));
+        }
+#pragma unroll
+        for (int i = 0; i < FLIGHT; ++i) {
+          const int row = row0 + i * STEP;
+          *reinterpret_cast<uint4*>(smem + L.q + (c >> 3) * (kTreeMaxCols * 128) + row * 128 + (((c & 7) ^ (row & 7)) << 4)) = x[i];
+        }
+      }
+      fence_proxy_async_shared();
+      named_bar_sync(3, kEpiAll);
+      if (lane == 0) mbar_arrive(bar.q_full);
+      if (et == 0 && w.t0 == 0) {  // for the join, as above
+        const TreeCut cut = *k.share_cut;
+        const int place = cut.by_items ? 0 : tree_even_first(cut, blockIdx.x) + gt;
+        p.holders[w.item] = make_int2(blockIdx.x, tree_last_holder(cut, blockIdx.x, w.tiles, place));
+      }
+      unsigned long long seen = 0;
+      if (w.t1 * kTreeTile > w.P) seen = seen_by_any(p, w);
+      Query q;
+      q.nm = my_row >= 0 ? -kUnset : kUnset;  // rows without a query: weights of zero whatever their scores
+      q.tau = my_tau;
+      float l = 0.f;
+
+      for (int i = 0; i < nt; ++i, ++gt) {
+        const int buf = gt & 1, t0 = (w.t0 + i) * kTreeTile;
+        const uint32_t s_tmem = tmem + buf * kTreeTile + wg * 64 + lanes;
+        const bool tail = t0 + kTreeTile > w.P, test = tail || p.tau != nullptr;
+        // of the 64 cache rows in hand: those of the prefix, then the drafted ones that the query sees
+        const int rel = w.P - (t0 + wg * 64);
+        q.sees = rel >= 64 ? ~0ull : rel > 0 ? (~0ull >> (64 - rel)) | my_mask << rel : rel > -64 ? my_mask >> -rel : 0ull;
+        if (my_row < 0) q.sees = 0ull;
+        ok = mbar_wait(&bar.s_full[buf], (gt >> 1) & 1, abort_flag);
+        tc_fence_after();
+        uint32_t weights[32];
+        float sum = 0.f, top = -INFINITY;
+        auto weigh_rows = [&]() {
+          if (idle) return;
+          if (test) row_weights<true>(s_tmem, q, p.scale, weights, &sum, &top);
+          else row_weights<false>(s_tmem, q, p.scale, weights, &sum, &top);
+        };
+        if (i > 0) weigh_rows();
+        else top = INFINITY;  // a segment's first tile: the references come from its maxima
+        if (named_bar_or(3, kEpiAll, top > kOverBf16 || !ok || *abort_flag != 0)) {
+          // new references, or the end of it all: the 256 threads meet at the same barriers, so they go together
+          if (named_bar_or(3, kEpiAll, !ok || *abort_flag != 0)) {
+            ok = false;
+            break;
+          }
+          if (!idle) words[wg * 128 + r] = row_maximum<true>(s_tmem, q, p.scale);
+          named_bar_sync(3, kEpiAll);
+          const float now = fmaxf(words[r], words[128 + r]), old = -q.nm;
+          const float next = !idle && now > -INFINITY ? fmaxf(old, now) : old;
+          const float f = old == kUnset ? 0.f : ex2(old - next);
+          q.nm = -next;
+          l *= f;
+          if (i > 0) {
+            // the products so far must be in the accumulators (a wait that gives up sets the abort flag, which the
+            // next tile sees)
+            mbar_wait(&bar.pv_done[buf ^ 1], ((gt - 1) >> 1) & 1, abort_flag);
+            tc_fence_after();
+            const int half = h.nv * (D / 2);
+#pragma unroll 1
+            for (int x = wg * half; x < (wg + 1) * half; x += 8) {
+              float o[8];
+              tmem_ld8(o_tmem + lanes + x, o);
+#pragma unroll
+              for (int y = 0; y < 8; ++y) o[y] *= f;
+              tmem_st8(o_tmem + lanes + x, o);
+            }
+          }
+          weigh_rows();
+          named_bar_sync(3, kEpiAll);  // the words are read before the next tile's
+        }
+        if (!idle) {
+          l += sum;
+          tmem_st16(s_tmem, weights);
+          tmem_st16(s_tmem + 16, weights + 16);
+          tmem_st_wait();
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bar.p_full[buf]);
+        if (tail && wg == 0) {
+          Ring vr = seg_ring;
+          vr.jump(tree_value_place(i, nt, h.nv), stages);
+          zero_unseen<D, false>(p, k, vr, h.nv, r, !row_seen(w, seen, t0 + r));
+        }
+      }
+      if (!ok) break;
+      seg_ring.jump(nt * (1 + h.nv), stages);
+      // the segment's sums: written out, or left as a partial
+      words[wg * 128 + r] = l;
+      ok = mbar_wait(&bar.pv_done[(gt - 1) & 1], ((gt - 1) >> 1) & 1, abort_flag);
+      if (named_bar_or(3, kEpiAll, !ok || *abort_flag != 0)) {
+        ok = false;
+        break;
+      }
+      tc_fence_after();
+      const bool whole = w.t0 == 0 && w.t1 == w.tiles;
+      const size_t slot = (size_t)blockIdx.x + w.item;
+      const float total = words[r] + words[128 + r];
+      if (!whole && wg == 0 && my_row >= 0) {
+        p.part_l[slot * kTreeMaxCols + r] = total;
+        p.part_m[slot * kTreeMaxCols + r] = -q.nm;
+      }
+      const float inv = total > 0.f ? 1.f / total : 0.f;
+      if (!idle) {
+        const int mine = r / p.plan.rpc;  // this row's value head of the chunk
+        const int v_lo = (quarter * 32) / p.plan.rpc, v_hi = min((quarter * 32 + 31) / p.plan.rpc, h.nv - 1);
+#pragma unroll 1
+        for (int v = v_lo; v <= v_hi; ++v)
+#pragma unroll 1
+          for (int x = wg * (D / 2); x < (wg + 1) * (D / 2); x += 32) {
+            float o[32];
+            tmem_ld32(o_tmem + lanes + v * D + x, o);
+            if (my_row < 0 || v != mine) continue;
+            if (!whole) {
+              float4* dst = reinterpret_cast<float4*>(p.part_o + (slot * kTreeMaxCols + r) * D + x);
+#pragma unroll
+              for (int y = 0; y < 8; ++y) dst[y] = make_float4(o[4 * y], o[4 * y + 1], o[4 * y + 2], o[4 * y + 3]);
+              continue;
+            }
+#pragma unroll
+            for (int y = 0; y < 32; ++y) o[y] = inv > 0.f ? o[y] * inv : 0.f;
+            if (p.out_bf16) {
+              uint4* dst = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.out) + (size_t)my_row * D + x);
+#pragma unroll
+              for (int y = 0; y < 4; ++y)
+                dst[y] = make_uint4(pack_bf16(o[8 * y], o[8 * y + 1]), pack_bf16(o[8 * y + 2], o[8 * y + 3]),
+                                    pack_bf16(o[8 * y + 4], o[8 * y + 5]), pack_bf16(o[8 * y + 6], o[8 * y + 7]));
+            } else {
+              float4* dst = reinterpret_cast<float4*>(static_cast<float*>(p.out) + (size_t)my_row * D + x);
+#pragma unroll
+              for (int y = 0; y < 8; ++y) dst[y] = make_float4(o[4 * y], o[4 * y + 1], o[4 * y + 2], o[4 * y + 3]);
+            }
+          }
+      }
+      tc_fence_before();
+    } while (tree_walk_next(line_of(p), w));
+  }
+
+  block_end(p, k, issued, tmem, 512);
 }
 
 // ------------------------------------------------------------------ the join
@@ -1235,6 +1678,10 @@ TreeSizes tree_sizes(const saga_shape* s, const TreePlan& plan, int ctas) {
   return z;
 }
 
+// Queries as rows from kTreeRows live rows a chunk on.
+constexpr int kTreeRows = 48;
+bool by_rows(const TreePlan& rows) { return tree_live_rows(rows) >= kTreeRows; }
+
 typedef void (*TreeKernel)(CUtensorMap, CUtensorMap, TreeParams);
 
 }  // namespace
@@ -1248,7 +1695,10 @@ size_t saga_tree_workspace_bytes(const saga_shape* s, int tokens) {
   if (validate_tree(s, tokens)) return 0;
   int sms = 0;
   if (api_device_sms(&sms)) return 0;
-  return tree_sizes(s, tree_plan(s->h_q, s->h_k, s->h_v, tokens), std::min(sms, kTreeMaxCtas)).total;
+  const int ctas = std::min(sms, kTreeMaxCtas);
+  const size_t columns = tree_sizes(s, tree_plan(s->h_q, s->h_k, s->h_v, tokens), ctas).total;
+  const TreePlan rows = tree_plan_rows(s->h_q, s->h_k, s->h_v, s->d, tokens);
+  return by_rows(rows) ? std::max(columns, tree_sizes(s, rows, ctas).total) : columns;  // of either format
 }
 
 int saga_tree_attn(const saga_shape* s, int tokens, const void* q, const saga_cache* cache, const int* prefix_lens,
@@ -1267,11 +1717,13 @@ int saga_tree_attn(const saga_shape* s, int tokens, const void* q, const saga_ca
   rc = api_device_sms(&sms);
   if (rc) return rc;
   TreeParams p{};
-  p.plan = tree_plan(s->h_q, s->h_k, s->h_v, tokens);
+  const bool e4m3 = cache->format == SAGA_CACHE_E4M3;
+  const TreePlan rows_plan = tree_plan_rows(s->h_q, s->h_k, s->h_v, s->d, tokens);
+  const bool as_rows = !e4m3 && by_rows(rows_plan);
+  p.plan = as_rows ? rows_plan : tree_plan(s->h_q, s->h_k, s->h_v, tokens);
   const TreeSizes z = tree_sizes(s, p.plan, std::min(sms, kTreeMaxCtas));
   if (ws_bytes < z.total) return api_fail(SAGA_ERR_WORKSPACE, "workspace has %zu bytes, needs %zu", ws_bytes, z.total);
-  const bool e4m3 = cache->format == SAGA_CACHE_E4M3;
-  p.smem = tree_smem(p.plan, s->d, e4m3);
+  p.smem = tree_smem(p.plan, s->d, e4m3, as_rows);
   p.q = static_cast<const uint16_t*>(q);
   p.k = cache->k;
   p.v = cache->v;
@@ -1302,12 +1754,13 @@ int saga_tree_attn(const saga_shape* s, int tokens, const void* q, const saga_ca
   if (rc) return rc;
   rc = api_rows_map(&vm, cache->v, (long long)s->batch * s->h_v * s->l_cap, s->d, e4m3);
   if (rc) return rc;
-  const TreeKernel kernel = s->d == 64 ? (e4m3 ? saga_tree_kernel<64, true> : saga_tree_kernel<64, false>)
-                                       : (e4m3 ? saga_tree_kernel<128, true> : saga_tree_kernel<128, false>);
-  static std::atomic<uint64_t> done[4], done_join[3];
+  const TreeKernel kernel = as_rows      ? (s->d == 64 ? saga_tree_rows_kernel<64> : saga_tree_rows_kernel<128>)
+                            : s->d == 64 ? (e4m3 ? saga_tree_kernel<64, true> : saga_tree_kernel<64, false>)
+                                         : (e4m3 ? saga_tree_kernel<128, true> : saga_tree_kernel<128, false>);
+  static std::atomic<uint64_t> done[6], done_join[3];
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   cudaError_t e = prepare_kernel(reinterpret_cast<const void*>(kernel), 227 * 1024,
-                                 done[(e4m3 ? 1 : 0) + (s->d == 64 ? 0 : 2)]);
+                                 done[(as_rows ? 2 : e4m3 ? 1 : 0) + (s->d == 64 ? 0 : 3)]);
   if (e == cudaSuccess)
     e = launch_pdl(kernel, dim3(p.ctas), dim3(kTreeThreads), p.smem.total, st, km, vm, p);
   if (e != cudaSuccess) return api_cuda_fail(e, "drafted-token attention launch");

@@ -58,6 +58,38 @@ __host__ __device__ inline TreePlan tree_plan(int h_q, int h_k, int h_v, int T) 
   return p;
 }
 
+// The same with queries as the rows of the products (M = 128) and cache rows as
+// their columns: a chunk is up to 128 query rows without padding, of as many
+// value heads as have room for their d columns of sums in TMEM (256).
+__host__ __device__ inline TreePlan tree_plan_rows(int h_q, int h_k, int h_v, int d, int T) {
+  TreePlan p;
+  const int G = h_q / h_k, per_v = h_q / h_v;
+  p.hpv = per_v < G ? per_v : G;
+  p.nvh = G / p.hpv;
+  p.rows = p.hpv * T;
+  if (p.rows <= kTreeMaxCols) {
+    int per = kTreeMaxCols / p.rows;
+    if (per > 256 / d) per = 256 / d;
+    p.chunks = (p.nvh + per - 1) / per;
+    p.nv = (p.nvh + p.chunks - 1) / p.chunks;
+    p.chunks = (p.nvh + p.nv - 1) / p.nv;
+    p.rsplit = 1;
+    p.rpc = p.rows;
+  } else {
+    p.rsplit = (p.rows + kTreeMaxCols - 1) / kTreeMaxCols;
+    p.rpc = (p.rows + p.rsplit - 1) / p.rsplit;
+    p.rsplit = (p.rows + p.rpc - 1) / p.rpc;
+    p.nv = 1;
+    p.chunks = p.nvh * p.rsplit;
+  }
+  p.nvp = p.rpc;
+  p.cols = kTreeMaxCols;
+  p.groups = 0;
+  return p;
+}
+// Query rows of a chunk of that plan.
+__host__ __device__ inline int tree_live_rows(const TreePlan& p) { return p.nv * p.rpc; }
+
 // The work is a line of tiles: batch rows in order, in each its `items`
 // (key head, chunk) items in order, in each its tiles.  It is cut in one of
 // two ways.  Evenly: CTA i takes the i-th of `ctas` runs of tiles whose lengths
@@ -257,12 +289,12 @@ struct TreeSmem {
   int stages, stage_bytes;
   int ones, q, p, p_bytes, mask, m, tau, cs, f, row, words, sums, scales, bars, total;
 };
-__host__ __device__ inline TreeSmem tree_smem(const TreePlan& p, int d, bool e4m3) {
+__host__ __device__ inline TreeSmem tree_smem(const TreePlan& p, int d, bool e4m3, bool by_rows) {
   TreeSmem s;
   s.stage_bytes = kTreeTile * d * (e4m3 ? 1 : 2);
   const int budget = 227 * 1024 - 1024;  // less the slack that aligns the base to 1024 bytes
   const int q_bytes = p.cols * d * 2;
-  s.p_bytes = p.cols * kTreeTile * (e4m3 ? 3 : 2);
+  s.p_bytes = by_rows ? 0 : p.cols * kTreeTile * (e4m3 ? 3 : 2);  // by rows the weights are in TMEM
   const int words = p.cols * (8 + 5 * 4 + 4 * 4);
   const int eight = e4m3 ? 2 * p.cols * 4 * 4 + 2 * 2 * (1 + p.nv) * kTreeTile * 4 : 0;
   const int bar_bytes = 8 * (3 * kTreeMaxStages + 16) + 16 + (int)(sizeof(TreeWalk) + sizeof(TreeCut));

@@ -32,34 +32,36 @@ static void plans() {
       if (h_q % h_k || h_q % h_v || (h_v % h_k && h_k % h_v) || h_q / h_k > (d == 64 ? 64 : 32)) continue;
       if (h_v > h_k && h_v / h_k > 32) continue;
       for (int T : Ts) {
-        const TreePlan p = tree_plan(h_q, h_k, h_v, T);
-        const int G = h_q / h_k;
-        CHECK(p.cols <= kTreeMaxCols && p.cols % 16 == 0 && p.nvp % 16 == 0 && p.nv * p.nvp <= p.cols, "cols");
-        CHECK(p.groups * 8 <= p.nvp && p.groups >= 1, "groups");
-        CHECK(p.hpv * p.nvh == G, "heads");
-        std::map<std::pair<int, int>, int> seen;
-        for (int jj = 0; jj < G; ++jj) for (int t = 0; t < T; ++t) {
-          const TreeSpot s = tree_spot(p, T, jj, t);
-          CHECK(s.chunk >= 0 && s.chunk < p.chunks && s.col >= 0 && s.col < p.nv * p.nvp, "spot of %d %d", jj, t);
-          const int uses = ++seen[std::make_pair(s.chunk, s.col)];
-          CHECK(uses == 1, "two rows in one column");
-          int j2 = -1, t2 = -1;
-          CHECK(tree_row(p, T, s.chunk, s.col, &j2, &t2) && j2 == jj && t2 == t, "row of column");
-          // its value head is the one whose columns these are
-          const int kh = 0, j = kh * G + jj;
-          const int vl = s.col / p.nvp, v0 = p.rsplit == 1 ? s.chunk * p.nv : s.chunk / p.rsplit;
-          CHECK((kh * G + (v0 + vl) * p.hpv) / (h_q / h_v) == j / (h_q / h_v), "value head");
-        }
-        int live = 0;
-        for (int c = 0; c < p.chunks; ++c) for (int col = 0; col < p.cols; ++col) {
-          int a, b;
-          live += tree_row(p, T, c, col, &a, &b);
-        }
-        CHECK(live == G * T, "live columns %d of %d", live, G * T);
-        for (int e = 0; e < 2; ++e) {
-          const TreeSmem s = tree_smem(p, d, e != 0);
-          CHECK(s.stages >= 3 && s.stages <= kTreeMaxStages && s.total <= 227 * 1024, "smem %d stages %d", s.total, s.stages);
-          CHECK(s.ones % 1024 == 0 && s.q % 1024 == 0 && s.p % 1024 == 0 && s.m % 16 == 0 && s.f % 16 == 0 && s.bars % 8 == 0, "smem alignment");
+        for (int by_rows = 0; by_rows < 2; ++by_rows) {
+          const TreePlan p = by_rows ? tree_plan_rows(h_q, h_k, h_v, d, T) : tree_plan(h_q, h_k, h_v, T);
+          const int G = h_q / h_k;
+          CHECK(p.cols <= kTreeMaxCols && p.cols % 16 == 0 && p.nv * p.nvp <= p.cols, "cols");
+          if (by_rows) CHECK(p.nv * d <= 256 && tree_live_rows(p) <= 128, "rows");
+          else CHECK(p.nvp % 16 == 0 && p.groups * 8 <= p.nvp && p.groups >= 1, "groups");
+          CHECK(p.hpv * p.nvh == G, "heads");
+          std::map<std::pair<int, int>, int> seen;
+          for (int jj = 0; jj < G; ++jj) for (int t = 0; t < T; ++t) {
+            const TreeSpot s = tree_spot(p, T, jj, t);
+            CHECK(s.chunk >= 0 && s.chunk < p.chunks && s.col >= 0 && s.col < p.nv * p.nvp, "spot of %d %d", jj, t);
+            const int uses = ++seen[std::make_pair(s.chunk, s.col)];
+            CHECK(uses == 1, "two rows in one column");
+            int j2 = -1, t2 = -1;
+            CHECK(tree_row(p, T, s.chunk, s.col, &j2, &t2) && j2 == jj && t2 == t, "row of column");
+            // its value head is the one whose columns these are
+            const int vl = s.col / p.nvp, v0 = p.rsplit == 1 ? s.chunk * p.nv : s.chunk / p.rsplit;
+            CHECK(((v0 + vl) * p.hpv) / (h_q / h_v) == jj / (h_q / h_v), "value head");
+          }
+          int live = 0;
+          for (int c = 0; c < p.chunks; ++c) for (int col = 0; col < p.cols; ++col) {
+            int a, b;
+            live += tree_row(p, T, c, col, &a, &b);
+          }
+          CHECK(live == G * T, "live columns %d of %d", live, G * T);
+          for (int e = 0; e < (by_rows ? 1 : 2); ++e) {
+            const TreeSmem s = tree_smem(p, d, e != 0, by_rows != 0);
+            CHECK(s.stages >= 3 && s.stages <= kTreeMaxStages && s.total <= 227 * 1024, "smem %d stages %d", s.total, s.stages);
+            CHECK(s.ones % 1024 == 0 && s.q % 1024 == 0 && s.p % 1024 == 0 && s.m % 16 == 0 && s.f % 16 == 0 && s.bars % 8 == 0, "smem alignment");
+          }
         }
       }
     }
