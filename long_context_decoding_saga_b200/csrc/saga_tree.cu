@@ -28,9 +28,8 @@
 // given in pieces whose products add up in the same accumulators: q, scaled by
 // a power of two, as the sum of two e4m3 numbers (4 + 4 of bf16's 8 bits,
 // exact for all elements but those 2^-14 below the row's largest); the weights
-// as an e5m2 number, what it leaves as e4m3, and what that leaves as e4m3 again
-// (2^-3, 2^-4 and 2^-4 of what is left: off by 2^-11 at most.  Without the third
-// the error of an output over a long cache was twice that of rounding it).  A key row's scale multiplies its scores and a value
+// as the sum of three e5m2 numbers (each off by 2^-3 of what is left: 2^-9; with
+// two the error of an output over a long cache was twice that of rounding it).  A key row's scale multiplies its scores and a value
 // row's scale its weights, both in fp32 and before any rounding; the sums of
 // weights are fp32 sums of the unrounded ones.
 #include <cuda_bf16.h>
@@ -217,11 +216,17 @@ __device__ __forceinline__ uint32_t pack_half(float a, float b) {
   const __half2 h = __floats2half2_rn(a, b);
   return reinterpret_cast<const uint32_t&>(h);
 }
-__device__ __forceinline__ uint32_t pack_e4m3(__half2 x) {
-  return __nv_cvt_halfraw2_to_fp8x2(static_cast<__half2_raw>(x), __NV_SATFINITE, __NV_E4M3);
-}
-__device__ __forceinline__ __half2 half2_of_e4m3(uint32_t x) {
-  return __half2(__nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)x, __NV_E4M3));
+// Two weights as three e5m2 numbers each, in the upper bytes of the halves.  An
+// e5m2 number is the upper byte of a half-precision one, so a piece is that
+// byte rounded and the rest an exact subtraction away: no conversions, which
+// were half of a tile's time.
+__device__ __forceinline__ void pieces_of(float a, float b, uint32_t& first, uint32_t& second, uint32_t& third) {
+  const uint32_t all = pack_half(a, b);
+  first = (all + 0x00800080u) & 0xff00ff00u;
+  __half2 rest = __hsub2(as_half2(all), as_half2(first));
+  second = (reinterpret_cast<const uint32_t&>(rest) + 0x00800080u) & 0xff00ff00u;
+  rest = __hsub2(rest, as_half2(second));
+  third = reinterpret_cast<const uint32_t&>(rest) + 0x00800080u;
 }
 // Two numbers as an 8-bit format each, in the low 16 bits, and back.
 __device__ __forceinline__ uint32_t pack_8bit(float a, float b, __nv_fp8_interpretation_t f) {
@@ -400,9 +405,6 @@ __device__ __forceinline__ float octet_sum(const float* v, int lane) {
 // bf16: a row of P is 16 bytes per 8 columns.  8-bit: 8 bytes per 8 columns of
 // each of three pieces, `piece` bytes apart; and the weights' sums over the
 // warp's rows into here[column] (a tile that is done again overwrites them).
-// The pieces are taken in half precision, whose upper byte is an e5m2 number:
-// the first is that byte rounded, the rest an exact subtraction away.  (From
-// fp32, with a conversion each way, a tile of 96 columns took 3.9 us.)
 template <bool E4M3, bool TEST>
 __device__ __forceinline__ float weigh(uint32_t s_tmem, uint8_t* p_row, int piece, float* here, Groups g, const Row& r,
                                        const Columns& c) {
@@ -441,16 +443,12 @@ __device__ __forceinline__ float weigh(uint32_t s_tmem, uint8_t* p_row, int piec
       for (int i = 0; i < 4; ++i) {
         float a, b;
         untwo(mul2(two(s[2 * i], s[2 * i + 1]), two(vs, vs)), a, b);
-        const uint32_t all = pack_half(a, b);
-        w[i] = (all + 0x00800080u) & 0xff00ff00u;
-        const __half2 rest = __hsub2(as_half2(all), as_half2(w[i]));
-        z[i] = pack_e4m3(rest);
-        y[i] = pack_e4m3(__hsub2(rest, half2_of_e4m3(z[i])));
+        pieces_of(a, b, w[i], z[i], y[i]);
       }
       uint8_t* at = p_row + (col >> 4) * 2048 + (col & 8);
       *reinterpret_cast<uint2*>(at) = make_uint2(__byte_perm(w[0], w[1], 0x7531), __byte_perm(w[2], w[3], 0x7531));
-      *reinterpret_cast<uint2*>(at + piece) = make_uint2(z[0] | z[1] << 16, z[2] | z[3] << 16);
-      *reinterpret_cast<uint2*>(at + 2 * piece) = make_uint2(y[0] | y[1] << 16, y[2] | y[3] << 16);
+      *reinterpret_cast<uint2*>(at + piece) = make_uint2(__byte_perm(z[0], z[1], 0x7531), __byte_perm(z[2], z[3], 0x7531));
+      *reinterpret_cast<uint2*>(at + 2 * piece) = make_uint2(__byte_perm(y[0], y[1], 0x7531), __byte_perm(y[2], y[3], 0x7531));
       const float sum = octet_sum(s, lane);
       if ((lane & 3) == 0) here[col + octet_column(lane)] = sum;
     }
@@ -664,6 +662,42 @@ __device__ __forceinline__ void block_end(const TreeParams& p, const Block& k, i
   }
 }
 
+// 8-bit caches: 8 elements of a query (D / 8 neighbouring lanes hold it) as two
+// e4m3 numbers each, scaled by the power of two that brings the query's largest
+// into [128, 256), in a layout of `count` rows of D swizzled bytes; and the
+// query's score factor in powers of two.  Whole warps call; rows past the end
+// are not stored.
+template <int D>
+__device__ __forceinline__ void put_q8(uint8_t* at, int count, int row, int c, const uint4& x, float* factor, float scale) {
+  float f[8];
+  const uint32_t u[4] = {x.x, x.y, x.z, x.w};
+  float amax = 0.f;
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    f[2 * k] = __uint_as_float(u[k] << 16);
+    f[2 * k + 1] = __uint_as_float(u[k] & 0xffff0000u);
+    amax = fmaxf(amax, fmaxf(fabsf(f[2 * k]), fabsf(f[2 * k + 1])));
+  }
+#pragma unroll
+  for (int o = D / 16; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+  const int ex = min(max((int)(__float_as_uint(amax) >> 23) - 127 - 7, -126), 126);  // 2^ex and 2^-ex are normal
+  const float down = __uint_as_float((uint32_t)(127 - ex) << 23);
+  uint32_t y[4], z[4];
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const float a = f[2 * k] * down, b = f[2 * k + 1] * down;
+    y[k] = pack_8bit(a, b, __NV_E4M3);
+    const float2 had = unpack_8bit(y[k], __NV_E4M3);
+    z[k] = pack_8bit(a - had.x, b - had.y, __NV_E4M3);
+  }
+  if (row >= count) return;
+  // half a 16-byte piece of the row
+  at += row * D + (c & 1) * 8 + (((c >> 1) ^ (D == 64 ? row >> 1 & 3 : row & 7)) << 4);
+  *reinterpret_cast<uint2*>(at) = make_uint2(y[0] | y[1] << 16, y[2] | y[3] << 16);
+  *reinterpret_cast<uint2*>(at + count * D) = make_uint2(z[0] | z[1] << 16, z[2] | z[3] << 16);
+  if (c == 0) factor[row] = __uint_as_float((uint32_t)(127 + ex) << 23) * (scale * kLog2e);
+}
+
 // ------------------------------------------------------------------ the kernel
 // Warp 0: TMA loads of the tiles.  Warp 1: the products, issued by one lane.
 // Warps 4 .. 11: two warpgroups, each half of the column groups of every tile.
@@ -704,7 +738,6 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
     if (any) {
       const uint32_t id_s = E4M3 ? idesc(kE4m3, kE4m3, kTreeTile, cols, false) : idesc(kBf16, kBf16, kTreeTile, cols, false);
       const uint32_t id_o = E4M3 ? idesc(kE4m3, kE5m2, D, p.plan.nvp, true) : idesc(kBf16, kBf16, 128, p.plan.nvp, true);
-      const uint32_t id_o2 = idesc(kE4m3, kE4m3, D, p.plan.nvp, true);  // the weights' other pieces
       const uint32_t id_l = idesc(kBf16, kBf16, 64, cols, true);
       const uint32_t ones = smem_u32(smem + L.ones), ring0 = smem_u32(smem);
       const uint64_t q_desc = desc_rows<D, E4M3>(smem_u32(smem + L.q));
@@ -772,10 +805,10 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
                   umma_8bit(d, a + k * (D * 2), b + k * 32, id_o, k > 0 ? 1u : first);
 #pragma unroll
                 for (int k = 0; k < kTreeTile / 32; ++k)
-                  umma_8bit(d, a + k * (D * 2), b + cols * 8 + k * 32, id_o2, 1u);
+                  umma_8bit(d, a + k * (D * 2), b + cols * 8 + k * 32, id_o, 1u);
 #pragma unroll
                 for (int k = 0; k < kTreeTile / 32; ++k)
-                  umma_8bit(d, a + k * (D * 2), b + cols * 16 + k * 32, id_o2, 1u);
+                  umma_8bit(d, a + k * (D * 2), b + cols * 16 + k * 32, id_o, 1u);
               } else {
 #pragma unroll
                 for (int k = 0; k < kTreeTile / 16; ++k)
@@ -881,35 +914,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
         for (int i = 0; i < FLIGHT; ++i) {
           const int col = col0 + i * STEP;
           if (E4M3) {
-            float f[8];
-            const uint32_t u[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
-            float amax = 0.f;
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              f[2 * k] = __uint_as_float(u[k] << 16);
-              f[2 * k + 1] = __uint_as_float(u[k] & 0xffff0000u);
-              amax = fmaxf(amax, fmaxf(fabsf(f[2 * k]), fabsf(f[2 * k + 1])));
-            }
-#pragma unroll
-            for (int o = LPR / 2; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-            // a power of two that brings the row's largest element into [128, 256); both it and its inverse are normal
-            const int ex = min(max((int)(__float_as_uint(amax) >> 23) - 127 - 7, -126), 126);
-            const float down = __uint_as_float((uint32_t)(127 - ex) << 23);
-            uint32_t y[4], z[4];
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              const float a = f[2 * k] * down, b = f[2 * k + 1] * down;
-              y[k] = pack_8bit(a, b, __NV_E4M3);
-              const float2 had = unpack_8bit(y[k], __NV_E4M3);
-              z[k] = pack_8bit(a - had.x, b - had.y, __NV_E4M3);
-            }
-            if (col < cols) {  // 8 of the row's codes: half a 16-byte piece of its swizzled D bytes
-              uint8_t* at = smem + L.q + col * D + (c & 1) * 8 +
-                            (((c >> 1) ^ (D == 64 ? col >> 1 & 3 : col & 7)) << 4);
-              *reinterpret_cast<uint2*>(at) = make_uint2(y[0] | y[1] << 16, y[2] | y[3] << 16);
-              *reinterpret_cast<uint2*>(at + cols * D) = make_uint2(z[0] | z[1] << 16, z[2] | z[3] << 16);
-              if (c == 0) cw.cs[col] = __uint_as_float((uint32_t)(127 + ex) << 23) * (p.scale * kLog2e);
-            }
+            put_q8<D>(smem + L.q, cols, col, c, x[i], cw.cs, p.scale);
           } else if (col < cols) {
             *reinterpret_cast<uint4*>(smem + L.q + (c >> 3) * (cols * 128) + col * 128 + (((c & 7) ^ (col & 7)) << 4)) = x[i];
           }
@@ -1137,7 +1142,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
 }
 
 // ------------------------------------------------------------------ queries as rows
-// For chunks with many query rows (bf16 caches): the products the other way
+// For chunks with many query rows: the products the other way
 // round,
 //   S[query, row] = q . K      M = 128 queries, N = 128 rows of the tile
 //   O[query, d]  += P V        P from TMEM, where it takes its scores' place,
@@ -1147,13 +1152,24 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
 // kernel above takes 1.6 us per tile of d = 64, two thirds of it the weights'.
 // Each value head of the chunk takes all 128 rows of P and a share of the
 // columns of O, of which its own rows are kept; that costs products, of which
-// there is room.  Two warpgroups, each half of the tile's rows.
+// there is room.  Two warpgroups, each half of the tile's rows.  8-bit caches in
+// the same pieces as above; the scales of a tile's rows come to shared memory a
+// tile ahead and are read by all threads alike, and the sums of weights are
+// each thread's own.
 
 __device__ __forceinline__ void umma_bf16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc, uint32_t id, uint32_t accumulate) {
   asm volatile(
       "{\n\t.reg .pred p;\n\t"
       "setp.ne.b32 p, %4, 0;\n\t"
       "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "r"(a_tmem), "l"(bdesc), "r"(id), "r"(accumulate)
+      : "memory");
+}
+__device__ __forceinline__ void umma_8bit_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc, uint32_t id, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
       "r"(a_tmem), "l"(bdesc), "r"(id), "r"(accumulate)
       : "memory");
 }
@@ -1186,80 +1202,112 @@ __device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.
 // A thread's query.
 struct Query {
   float nm;                // its reference, negated
-  float tau;               // its threshold
+  float tau;               // its threshold (8-bit: in powers of two)
+  float scale;             // its score factor (8-bit: in powers of two)
   unsigned long long sees; // of the 64 cache rows in hand, with TEST
+  const float *ks, *vs;    // 8-bit: the scales of those rows as keys, and as values of its value head
 };
 
 // 32 scores into exponents relative to the reference (RELATIVE) or not; bits:
 // which of them the query sees.
-template <bool TEST, bool RELATIVE>
-__device__ __forceinline__ void row_exponents(float* s, const Query& q, uint32_t bits, float scale) {
-  const float f = TEST ? scale : scale * kLog2e, nm = RELATIVE ? q.nm : 0.f;
+template <bool E4M3, bool TEST, bool RELATIVE>
+__device__ __forceinline__ void row_exponents(float* s, const Query& q, int h) {
+  const uint32_t bits = (uint32_t)(q.sees >> (h * 32));
+  const float f = E4M3 || TEST ? q.scale : q.scale * kLog2e, nm = RELATIVE ? q.nm : 0.f;
   const unsigned long long ff = two(f, f), ll = two(kLog2e, kLog2e), mm = two(nm, nm);
 #pragma unroll
-  for (int i = 0; i < 32; i += 2) {
-    unsigned long long x = two(s[i], s[i + 1]);
-    if (TEST) {
-      x = mul2(x, ff);
-      float a, b;
-      untwo(x, a, b);
-      const bool keep0 = a >= q.tau && (bits >> i & 1u) != 0u, keep1 = b >= q.tau && (bits >> i & 2u) != 0u;
-      x = RELATIVE ? fma2(x, ll, mm) : mul2(x, ll);
-      untwo(x, s[i], s[i + 1]);
-      s[i] = keep0 ? s[i] : -INFINITY;
-      s[i + 1] = keep1 ? s[i + 1] : -INFINITY;
-    } else {
-      x = RELATIVE ? fma2(x, ff, mm) : mul2(x, ff);
-      untwo(x, s[i], s[i + 1]);
+  for (int g = 0; g < 8; ++g) {
+    float4 ks;
+    if (E4M3) ks = reinterpret_cast<const float4*>(q.ks + h * 32)[g];
+#pragma unroll
+    for (int i = 4 * g; i < 4 * g + 4; i += 2) {
+      unsigned long long x = two(s[i], s[i + 1]);
+      if (E4M3) x = mul2(x, i & 2 ? two(ks.z, ks.w) : two(ks.x, ks.y));
+      if (TEST) {
+        x = mul2(x, ff);
+        float a, b;
+        untwo(x, a, b);
+        const bool keep0 = a >= q.tau && (bits >> i & 1u) != 0u, keep1 = b >= q.tau && (bits >> i & 2u) != 0u;
+        if (E4M3) x = RELATIVE ? fma2(x, two(1.f, 1.f), mm) : x;
+        else x = RELATIVE ? fma2(x, ll, mm) : mul2(x, ll);
+        untwo(x, s[i], s[i + 1]);
+        s[i] = keep0 ? s[i] : -INFINITY;
+        s[i + 1] = keep1 ? s[i + 1] : -INFINITY;
+      } else {
+        x = RELATIVE ? fma2(x, ff, mm) : mul2(x, ff);
+        untwo(x, s[i], s[i + 1]);
+      }
     }
   }
 }
 
-// 64 scores into 32 words of weights; their sum, and the largest exponent.
-template <bool TEST>
-__device__ __forceinline__ void row_weights(uint32_t s_tmem, const Query& q, float scale, uint32_t* w, float* sum, float* top) {
-  float most = -INFINITY;
+// 64 scores into words of weights (bf16: 32; 8-bit: 16 for each of three
+// pieces); their sum, and how far the largest is above what it may be (over 0).
+template <bool E4M3, bool TEST>
+__device__ __forceinline__ void row_weights(uint32_t s_tmem, const Query& q, uint32_t* w, float* sum, float* over) {
+  float most = E4M3 ? 0.f : -INFINITY;
   unsigned long long add[2] = {0ull, 0ull};
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
     float s[32];
     tmem_ld32(s_tmem + h * 32, s);
-    row_exponents<TEST, true>(s, q, (uint32_t)(q.sees >> (h * 32)), scale);
+    row_exponents<E4M3, TEST, true>(s, q, h);
+    if (!E4M3) {
 #pragma unroll
-    for (int i = 0; i < 32; ++i) {
-      most = fmaxf(most, s[i]);
-      s[i] = ex2(s[i]);
-    }
+      for (int i = 0; i < 32; ++i) {
+        most = fmaxf(most, s[i]);
+        s[i] = ex2(s[i]);
+      }
 #pragma unroll
-    for (int i = 0; i < 32; i += 2) {
-      const uint32_t y = pack_bf16(s[i], s[i + 1]);
-      w[h * 16 + (i >> 1)] = y;
-      // the sum of the rounded weights, as the other kernel's row of ones gives it
-      add[i >> 1 & 1] = fma2(two(__uint_as_float(y << 16), __uint_as_float(y & 0xffff0000u)), two(1.f, 1.f), add[i >> 1 & 1]);
+      for (int i = 0; i < 32; i += 2) {
+        const uint32_t y = pack_bf16(s[i], s[i + 1]);
+        w[h * 16 + (i >> 1)] = y;
+        // the sum of the rounded weights, as the other kernel's row of ones gives it
+        add[i >> 1 & 1] = fma2(two(__uint_as_float(y << 16), __uint_as_float(y & 0xffff0000u)), two(1.f, 1.f), add[i >> 1 & 1]);
+      }
+    } else {
+#pragma unroll
+      for (int g = 0; g < 8; ++g) {
+        const float4 vs = reinterpret_cast<const float4*>(q.vs + h * 32)[g];
+        uint32_t p1[2], p2[2], p3[2];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const unsigned long long x = two(ex2(s[4 * g + 2 * i]), ex2(s[4 * g + 2 * i + 1]));
+          add[i] = fma2(x, two(1.f, 1.f), add[i]);
+          float a, b;
+          untwo(mul2(x, i ? two(vs.z, vs.w) : two(vs.x, vs.y)), a, b);
+          most = fmaxf(most, fmaxf(a, b));
+          pieces_of(a, b, p1[i], p2[i], p3[i]);
+        }
+        w[h * 8 + g] = __byte_perm(p1[0], p1[1], 0x7531);
+        w[16 + h * 8 + g] = __byte_perm(p2[0], p2[1], 0x7531);
+        w[32 + h * 8 + g] = __byte_perm(p3[0], p3[1], 0x7531);
+      }
     }
   }
   float a, b, c, d;
   untwo(add[0], a, b);
   untwo(add[1], c, d);
   *sum = (a + b) + (c + d);
-  *top = most;
+  // 8-bit: a row whose scale lies far below the others' does not show among the scaled weights, but in the sum
+  *over = E4M3 ? (*sum < 1e34f ? most - 32768.f : INFINITY) : most - kOverBf16;
 }
 
-template <bool TEST>
-__device__ __forceinline__ float row_maximum(uint32_t s_tmem, const Query& q, float scale) {
+template <bool E4M3, bool TEST>
+__device__ __forceinline__ float row_maximum(uint32_t s_tmem, const Query& q) {
   float most = -INFINITY;
 #pragma unroll 1
   for (int h = 0; h < 2; ++h) {
     float s[32];
     tmem_ld32(s_tmem + h * 32, s);
-    row_exponents<TEST, false>(s, q, (uint32_t)(q.sees >> (h * 32)), scale);
+    row_exponents<E4M3, TEST, false>(s, q, h);
 #pragma unroll
-    for (int i = 0; i < 32; ++i) most = fmaxf(most, s[i]);
+    for (int i = 0; i < 32; ++i) most = fmaxf(most, E4M3 ? s[i] + __log2f(fmaxf(q.vs[h * 32 + i], kMinScale)) : s[i]);
   }
   return most;
 }
 
-template <int D>
+template <int D, bool E4M3>
 __global__ void __launch_bounds__(kTreeThreads, 1)
     saga_tree_rows_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
                           const TreeParams p) {
@@ -1278,13 +1326,14 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
   const bool any = w.left > 0;
 
   if (warp == 0) {
-    if (any) issued = load_tiles<D, false>(p, k, &kmap, &vmap, w);
+    if (any) issued = load_tiles<D, E4M3>(p, k, &kmap, &vmap, w);
   } else if (warp == 1) {
     if (any) {
-      const uint32_t id_s = idesc(kBf16, kBf16, 128, kTreeTile, false);
-      const uint32_t id_o = idesc(kBf16, kBf16, 128, D, false) | 1u << 16;  // V as it lies: its rows are the inner dimension
+      const uint32_t id_s = E4M3 ? idesc(kE4m3, kE4m3, 128, kTreeTile, false) : idesc(kBf16, kBf16, 128, kTreeTile, false);
+      // V as it lies: its rows are the inner dimension
+      const uint32_t id_o = (E4M3 ? idesc(kE5m2, kE4m3, 128, D, false) : idesc(kBf16, kBf16, 128, D, false)) | 1u << 16;
       const uint32_t ring0 = smem_u32(smem);
-      const uint64_t q_desc = desc_rows<D, false>(smem_u32(smem + L.q));
+      const uint64_t q_desc = desc_rows<D, E4M3>(smem_u32(smem + L.q));
       Ring r;
       uint32_t fixed = 0;  // parity of each stage's vfix barrier
       int gs = 0, gp = 0, seg = 0;  // score products, value products, segments so far
@@ -1295,12 +1344,20 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
         // the buffer held the weights of two tiles before, until their product was done
         if (gs >= 2 && !wait(&bar.pv_done[gs & 1], ((gs >> 1) - 1) & 1)) return false;
         tc_fence_after();
-        const uint64_t k_desc = desc_rows<D, false>(ring0 + r.st * L.stage_bytes);
+        const uint64_t k_desc = desc_rows<D, E4M3>(ring0 + r.st * L.stage_bytes);
         if (elect_one()) {
+          const uint32_t d = tmem + (gs & 1) * kTreeTile;
+          if (E4M3) {
 #pragma unroll
-          for (int i = 0; i < D / 16; ++i) {  // 64-column halves 16 KB apart in both
-            const uint32_t at = (i >> 2) * (kTreeTile * 128 / 16) + (i & 3) * 2;
-            umma_bf16(tmem + (gs & 1) * kTreeTile, q_desc + at, k_desc + at, id_s, i > 0);
+            for (int i = 0; i < D / 32; ++i) umma_8bit(d, q_desc + i * 2, k_desc + i * 2, id_s, i > 0);
+#pragma unroll
+            for (int i = 0; i < D / 32; ++i) umma_8bit(d, q_desc + kTreeMaxCols * (D / 16) + i * 2, k_desc + i * 2, id_s, 1u);
+          } else {
+#pragma unroll
+            for (int i = 0; i < D / 16; ++i) {  // 64-column halves 16 KB apart in both
+              const uint32_t at = (i >> 2) * (kTreeTile * 128 / 16) + (i & 3) * 2;
+              umma_bf16(d, q_desc + at, k_desc + at, id_s, i > 0);
+            }
           }
           umma_commit(&bar.empty[r.st]);
           umma_commit(&bar.s_full[gs & 1]);
@@ -1318,28 +1375,43 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
         ok = ok && scores();
         for (int t = w.t0; ok && t < w.t1; ++t) {
           if (t + 1 < w.t1) ok = scores();
-          ok = ok && wait(&bar.p_full[gp & 1], (gp >> 1) & 1);
+          // the values first, which come early (the ring holds a tile's: at most 4 of 8 stages, or 2 of 4), then the
+          // weights: the products of a tile then follow one another without a pause
           const bool fix = (t + 1) * kTreeTile > w.P;
-          const uint32_t first = t > w.t0 ? 1u : 0u, a = tmem + (gp & 1) * kTreeTile;
+          Ring at = r;
           for (int v = 0; ok && v < h.nv; ++v) {
-            ok = wait(&bar.full[r.st], r.round & 1);
+            ok = wait(&bar.full[at.st], at.round & 1);
             if (ok && fix) {
-              ok = wait(&bar.vfix[r.st], fixed >> r.st & 1);
-              fixed ^= 1u << r.st;
+              ok = wait(&bar.vfix[at.st], fixed >> at.st & 1);
+              fixed ^= 1u << at.st;
             }
-            if (!ok) break;
-            tc_fence_after();
-            const uint64_t b = desc_v<D, false>(ring0 + r.st * L.stage_bytes, kTreeTile * 128);
+            at.step(stages);
+          }
+          ok = ok && wait(&bar.p_full[gp & 1], (gp >> 1) & 1);
+          if (!ok) break;
+          tc_fence_after();
+          const uint32_t first = t > w.t0 ? 1u : 0u, a = tmem + (gp & 1) * kTreeTile;
+          for (int v = 0; v < h.nv; ++v) {
+            const uint64_t b = desc_v<D, E4M3>(ring0 + r.st * L.stage_bytes, kTreeTile * 128);
             if (elect_one()) {
+              // each warpgroup's 64 rows of weights lie 64 columns apart: 32 columns of bf16, or 16 for each piece
+              if (E4M3) {
 #pragma unroll
-              for (int i = 0; i < kTreeTile / 16; ++i)  // each warpgroup's 64 rows of weights: 32 columns, 64 apart
-                umma_bf16_ts(o_tmem + v * D, a + (i >> 2) * 64 + (i & 3) * 8, b + i * 128, id_o, i > 0 ? 1u : first);
+                for (int piece = 0; piece < 3; ++piece)
+#pragma unroll
+                  for (int i = 0; i < kTreeTile / 32; ++i)
+                    umma_8bit_ts(o_tmem + v * D, a + (i >> 1) * 64 + (i & 1) * 8 + piece * 16, b + i * (D * 2), id_o,
+                                 piece + i > 0 ? 1u : first);
+              } else {
+#pragma unroll
+                for (int i = 0; i < kTreeTile / 16; ++i)
+                  umma_bf16_ts(o_tmem + v * D, a + (i >> 2) * 64 + (i & 3) * 8, b + i * 128, id_o, i > 0 ? 1u : first);
+              }
               umma_commit(&bar.empty[r.st]);
             }
             __syncwarp();
             r.step(stages);
           }
-          if (!ok) break;
           if (elect_one()) umma_commit(&bar.pv_done[gp & 1]);
           __syncwarp();
           ++gp;
@@ -1372,6 +1444,24 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
           my_mask = all & (p.mask != nullptr ? p.mask[(size_t)w.b * p.tokens + t] : (2ull << t) - 1ull);
         }
       }
+      unsigned long long seen = 0;
+      if (w.t1 * kTreeTile > w.P) seen = seen_by_any(p, w);
+      // 8-bit: the scales of a tile's rows, of the key head and of the chunk's value heads, a tile ahead; rows that no
+      // token sees get zeros
+      float* scales = reinterpret_cast<float*>(smem + L.scales);
+      const int scale_slot = (1 + p.plan.nv) * kTreeTile;
+      auto fetch_scales = [&](int i) {  // of the segment's tile i
+        if (!E4M3) return;
+        float* dst = scales + (i & 1) * scale_slot;
+        for (int x = et; x < (1 + h.nv) * kTreeTile; x += kEpiAll) {
+          const int which = x / kTreeTile, row = (w.t0 + i) * kTreeTile + x % kTreeTile;
+          const bool there = row_seen(w, seen, row);
+          const float* src = which == 0 ? p.k_scale + h.key : p.v_scale + h.value + (size_t)(which - 1) * p.l_cap;
+          cp_async4_zfill(dst + x, src + (there ? row : 0), there);
+        }
+        cp_async_commit();
+      };
+      fetch_scales(0);
       const bool idle = !__any_sync(0xffffffffu, my_row >= 0);  // a warp without queries: its rows of O are garbage
       if (wg == 0) out_row[r] = my_row;  // read below only, since the last segment's barriers
       named_bar_sync(3, kEpiAll);
@@ -1389,10 +1479,12 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
 #pragma unroll
         for (int i = 0; i < FLIGHT; ++i) {
           const int row = row0 + i * STEP;
-          *reinterpret_cast<uint4*>(smem + L.q + (c >> 3) * (kTreeMaxCols * 128) + row * 128 + (((c & 7) ^ (row & 7)) << 4)) = x[i];
+          if (E4M3) put_q8<D>(smem + L.q, kTreeMaxCols, row, c, x[i], reinterpret_cast<float*>(smem + L.cs), p.scale);
+          else *reinterpret_cast<uint4*>(smem + L.q + (c >> 3) * (kTreeMaxCols * 128) + row * 128 + (((c & 7) ^ (row & 7)) << 4)) = x[i];
         }
       }
       fence_proxy_async_shared();
+      if (E4M3) cp_async_wait_all();
       named_bar_sync(3, kEpiAll);
       if (lane == 0) mbar_arrive(bar.q_full);
       if (et == 0 && w.t0 == 0) {  // for the join, as above
@@ -1400,11 +1492,11 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
         const int place = cut.by_items ? 0 : tree_even_first(cut, blockIdx.x) + gt;
         p.holders[w.item] = make_int2(blockIdx.x, tree_last_holder(cut, blockIdx.x, w.tiles, place));
       }
-      unsigned long long seen = 0;
-      if (w.t1 * kTreeTile > w.P) seen = seen_by_any(p, w);
       Query q;
       q.nm = my_row >= 0 ? -kUnset : kUnset;  // rows without a query: weights of zero whatever their scores
-      q.tau = my_tau;
+      q.tau = E4M3 ? my_tau * kLog2e : my_tau;
+      q.scale = E4M3 ? reinterpret_cast<const float*>(smem + L.cs)[r] : p.scale;
+      const int my_head = min(r / p.plan.rpc, h.nv - 1);  // of the chunk's value heads
       float l = 0.f;
 
       for (int i = 0; i < nt; ++i, ++gt) {
@@ -1415,26 +1507,33 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
         const int rel = w.P - (t0 + wg * 64);
         q.sees = rel >= 64 ? ~0ull : rel > 0 ? (~0ull >> (64 - rel)) | my_mask << rel : rel > -64 ? my_mask >> -rel : 0ull;
         if (my_row < 0) q.sees = 0ull;
+        if (E4M3) {
+          q.ks = scales + (i & 1) * scale_slot + wg * 64;
+          q.vs = q.ks + (1 + my_head) * kTreeTile;
+          if (i + 1 < nt) fetch_scales(i + 1);
+        }
         ok = mbar_wait(&bar.s_full[buf], (gt >> 1) & 1, abort_flag);
         tc_fence_after();
-        uint32_t weights[32];
-        float sum = 0.f, top = -INFINITY;
+        constexpr int WORDS = E4M3 ? 48 : 32;
+        uint32_t weights[WORDS];
+        float sum = 0.f, over = -INFINITY;
         auto weigh_rows = [&]() {
           if (idle) return;
-          if (test) row_weights<true>(s_tmem, q, p.scale, weights, &sum, &top);
-          else row_weights<false>(s_tmem, q, p.scale, weights, &sum, &top);
+          if (test) row_weights<E4M3, true>(s_tmem, q, weights, &sum, &over);
+          else row_weights<E4M3, false>(s_tmem, q, weights, &sum, &over);
         };
         if (i > 0) weigh_rows();
-        else top = INFINITY;  // a segment's first tile: the references come from its maxima
-        if (named_bar_or(3, kEpiAll, top > kOverBf16 || !ok || *abort_flag != 0)) {
+        else over = INFINITY;  // a segment's first tile: the references come from its maxima
+        if (E4M3) cp_async_wait_all();  // the next tile's scales, seen by all after the vote
+        if (named_bar_or(3, kEpiAll, over > 0.f || !ok || *abort_flag != 0)) {
           // new references, or the end of it all: the 256 threads meet at the same barriers, so they go together
           if (named_bar_or(3, kEpiAll, !ok || *abort_flag != 0)) {
             ok = false;
             break;
           }
-          if (!idle) words[wg * 128 + r] = row_maximum<true>(s_tmem, q, p.scale);
+          if (!idle) words[wg * 128 + r] = row_maximum<E4M3, true>(s_tmem, q);
           named_bar_sync(3, kEpiAll);
-          const float now = fmaxf(words[r], words[128 + r]), old = -q.nm;
+          const float now = fmaxf(words[r], words[128 + r]) - (E4M3 ? kTopE5m2 : 0.f), old = -q.nm;
           const float next = !idle && now > -INFINITY ? fmaxf(old, now) : old;
           const float f = old == kUnset ? 0.f : ex2(old - next);
           q.nm = -next;
@@ -1459,8 +1558,8 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
         }
         if (!idle) {
           l += sum;
-          tmem_st16(s_tmem, weights);
-          tmem_st16(s_tmem + 16, weights + 16);
+#pragma unroll
+          for (int x = 0; x < WORDS; x += 16) tmem_st16(s_tmem + x, weights + x);
           tmem_st_wait();
         }
         tc_fence_before();
@@ -1469,7 +1568,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
         if (tail && wg == 0) {
           Ring vr = seg_ring;
           vr.jump(tree_value_place(i, nt, h.nv), stages);
-          zero_unseen<D, false>(p, k, vr, h.nv, r, !row_seen(w, seen, t0 + r));
+          zero_unseen<D, E4M3>(p, k, vr, h.nv, r, !row_seen(w, seen, t0 + r));
         }
       }
       if (!ok) break;
@@ -1678,9 +1777,14 @@ TreeSizes tree_sizes(const saga_shape* s, const TreePlan& plan, int ctas) {
   return z;
 }
 
-// Queries as rows from kTreeRows live rows a chunk on.
-constexpr int kTreeRows = 48;
-bool by_rows(const TreePlan& rows) { return tree_live_rows(rows) >= kTreeRows; }
+// Queries as rows from so many live rows a chunk on.  A tree of T tokens over
+// 32K rows of 32/2/8 heads of 64 (16 T live rows up to 128), as columns and as
+// rows: bf16 T = 4 20.3 and 20.8 us, T = 6 21.9 and 21.3; 8-bit T = 2 22.7 and
+// 25.7, T = 4 27.2 and 26.9.  Over 16K rows of 32/8/8 heads (4 T live rows):
+// bf16 T = 16 23.3 and 23.8, T = 24 29.0 and 26.9; 8-bit T = 12 32.5 and 33.8,
+// T = 16 37.3 and 34.5.
+constexpr int kTreeRowsBf16 = 80, kTreeRowsE4m3 = 56;
+bool by_rows(const TreePlan& rows, bool e4m3) { return tree_live_rows(rows) >= (e4m3 ? kTreeRowsE4m3 : kTreeRowsBf16); }
 
 typedef void (*TreeKernel)(CUtensorMap, CUtensorMap, TreeParams);
 
@@ -1698,7 +1802,7 @@ size_t saga_tree_workspace_bytes(const saga_shape* s, int tokens) {
   const int ctas = std::min(sms, kTreeMaxCtas);
   const size_t columns = tree_sizes(s, tree_plan(s->h_q, s->h_k, s->h_v, tokens), ctas).total;
   const TreePlan rows = tree_plan_rows(s->h_q, s->h_k, s->h_v, s->d, tokens);
-  return by_rows(rows) ? std::max(columns, tree_sizes(s, rows, ctas).total) : columns;  // of either format
+  return by_rows(rows, true) ? std::max(columns, tree_sizes(s, rows, ctas).total) : columns;  // of either format
 }
 
 int saga_tree_attn(const saga_shape* s, int tokens, const void* q, const saga_cache* cache, const int* prefix_lens,
@@ -1719,7 +1823,7 @@ int saga_tree_attn(const saga_shape* s, int tokens, const void* q, const saga_ca
   TreeParams p{};
   const bool e4m3 = cache->format == SAGA_CACHE_E4M3;
   const TreePlan rows_plan = tree_plan_rows(s->h_q, s->h_k, s->h_v, s->d, tokens);
-  const bool as_rows = !e4m3 && by_rows(rows_plan);
+  const bool as_rows = by_rows(rows_plan, e4m3);
   p.plan = as_rows ? rows_plan : tree_plan(s->h_q, s->h_k, s->h_v, tokens);
   const TreeSizes z = tree_sizes(s, p.plan, std::min(sms, kTreeMaxCtas));
   if (ws_bytes < z.total) return api_fail(SAGA_ERR_WORKSPACE, "workspace has %zu bytes, needs %zu", ws_bytes, z.total);
@@ -1754,13 +1858,14 @@ int saga_tree_attn(const saga_shape* s, int tokens, const void* q, const saga_ca
   if (rc) return rc;
   rc = api_rows_map(&vm, cache->v, (long long)s->batch * s->h_v * s->l_cap, s->d, e4m3);
   if (rc) return rc;
-  const TreeKernel kernel = as_rows      ? (s->d == 64 ? saga_tree_rows_kernel<64> : saga_tree_rows_kernel<128>)
+  const TreeKernel kernel = as_rows      ? (s->d == 64 ? (e4m3 ? saga_tree_rows_kernel<64, true> : saga_tree_rows_kernel<64, false>)
+                                                       : (e4m3 ? saga_tree_rows_kernel<128, true> : saga_tree_rows_kernel<128, false>))
                             : s->d == 64 ? (e4m3 ? saga_tree_kernel<64, true> : saga_tree_kernel<64, false>)
                                          : (e4m3 ? saga_tree_kernel<128, true> : saga_tree_kernel<128, false>);
-  static std::atomic<uint64_t> done[6], done_join[3];
+  static std::atomic<uint64_t> done[8], done_join[3];
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   cudaError_t e = prepare_kernel(reinterpret_cast<const void*>(kernel), 227 * 1024,
-                                 done[(as_rows ? 2 : e4m3 ? 1 : 0) + (s->d == 64 ? 0 : 3)]);
+                                 done[(as_rows ? 4 : 0) + (e4m3 ? 2 : 0) + (s->d == 64 ? 0 : 1)]);
   if (e == cudaSuccess)
     e = launch_pdl(kernel, dim3(p.ctas), dim3(kTreeThreads), p.smem.total, st, km, vm, p);
   if (e != cudaSuccess) return api_cuda_fail(e, "drafted-token attention launch");

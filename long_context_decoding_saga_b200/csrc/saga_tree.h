@@ -296,7 +296,8 @@ __host__ __device__ inline TreeSmem tree_smem(const TreePlan& p, int d, bool e4m
   const int q_bytes = p.cols * d * 2;
   s.p_bytes = by_rows ? 0 : p.cols * kTreeTile * (e4m3 ? 3 : 2);  // by rows the weights are in TMEM
   const int words = p.cols * (8 + 5 * 4 + 4 * 4);
-  const int eight = e4m3 ? 2 * p.cols * 4 * 4 + 2 * 2 * (1 + p.nv) * kTreeTile * 4 : 0;
+  const int sums = by_rows || !e4m3 ? 0 : 2 * p.cols * 4 * 4;
+  const int eight = e4m3 ? sums + 2 * (by_rows ? 1 : 2) * (1 + p.nv) * kTreeTile * 4 : 0;
   const int bar_bytes = 8 * (3 * kTreeMaxStages + 16) + 16 + (int)(sizeof(TreeWalk) + sizeof(TreeCut));
   const int fixed = 2048 + q_bytes + 2 * s.p_bytes + words + eight + bar_bytes;
   s.stages = (budget - fixed) / s.stage_bytes;
@@ -312,7 +313,7 @@ __host__ __device__ inline TreeSmem tree_smem(const TreePlan& p, int d, bool e4m
   s.row = s.f + p.cols * 4;
   s.words = s.row + p.cols * 4;
   s.sums = s.words + p.cols * 16;
-  s.scales = s.sums + (e4m3 ? p.cols * 32 : 0);
+  s.scales = s.sums + sums;
   s.bars = s.words + p.cols * 16 + eight;
   s.total = s.bars + bar_bytes + 1024;
   return s;

@@ -5,14 +5,13 @@ Bound, element by element, with w the exact softmax weights: a score is off by a
 (fp32 sums in any order with truncating tensor-core steps, the products with the scales), which changes weights by
 a factor of at most e^(2 es).  bf16 caches: the weights are rounded to bf16, w' = w (1 + d) with |d| <= 2^-8, and
 divided by the sum of the rounded ones, so sum w' v / sum w' is off by at most sum w |v| (2^-8 + 2^-8) to first order
-(2^-14 covers the second).  8-bit caches: a weight is an e5m2 number (off by 2^-3 at most), what that leaves as e4m3
-(2^-4 of it) and what is left then as e4m3 (2^-4): off by 2^-11, to which half precision, in which they are taken, adds
-2^-11; and divided by the exact sum; what is below e4m3's smallest number, 2^-10 where the largest weight is 2^10 or
-more, is 2^-20 of that for each of L rows.  q is two e4m3 numbers there, with elements below 2^-14 of the row's largest
-off by up to 2^-17 of it, which es includes.  The exponential and the fp32 sums over L rows add 2^-20 + L 2^-23, and a
-bf16 output 2^-8 of the value:
-  |out - exact| <= sum w |v| ([bf16] 2^-7 + 2^-14, [8-bit] 2^-10, + e^(2 es) - 1 + 2^-20 + L 2^-23)
-                   + [8-bit] L 2^-20 max |v|  (+ 2^-8 |exact| for bf16).
+(2^-14 covers the second).  8-bit caches: a weight is the sum of three e5m2 numbers, each off by at most 2^-3 of what
+is left (2^-9), taken in half precision (2^-11), and divided by the exact sum; what is below half of e5m2's smallest
+number, 2^-17 where the largest weight is 2^10 or more, is 2^-27 of that for each of L rows.  q is two e4m3 numbers
+there, with elements below 2^-14 of the row's largest off by up to 2^-17 of it, which es includes.  The exponential and
+the fp32 sums over L rows add 2^-20 + L 2^-23, and a bf16 output 2^-8 of the value:
+  |out - exact| <= sum w |v| ([bf16] 2^-7 + 2^-14, [8-bit] 2^-9 + 2^-10, + e^(2 es) - 1 + 2^-20 + L 2^-23)
+                   + [8-bit] L 2^-27 max |v|  (+ 2^-8 |exact| for bf16).
 Thresholds are placed so that every score is more than es from them: a score that is off by at most es is then on
 the same side of its threshold.
 """
@@ -86,8 +85,8 @@ def _bounds(q, K, V, prefix, n, masks, tau, D, fmt):
     es = ((D + 64) * 2.0 ** -23 + 2.0 ** -21) * dots / np.sqrt(d)
     if fmt == E4M3:
         es += 2.0 ** -17 * np.abs(q[:n]).max() * np.abs(K[:, :L]).sum(-1).max() / np.sqrt(d)
-    rel = (2.0 ** -7 + 2.0 ** -14 if fmt == BF16 else 2.0 ** -10) + np.expm1(2 * es) + 2.0 ** -20 + L * 2.0 ** -23
-    lost = L * 2.0 ** -20 * np.abs(V[:, :L]).max() if fmt == E4M3 else 0.0
+    rel = (2.0 ** -7 + 2.0 ** -14 if fmt == BF16 else 2.0 ** -9 + 2.0 ** -10) + np.expm1(2 * es) + 2.0 ** -20 + L * 2.0 ** -23
+    lost = L * 2.0 ** -27 * np.abs(V[:, :L]).max() if fmt == E4M3 else 0.0
     return exact, spread * rel + lost, border, es
 
 

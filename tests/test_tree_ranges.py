@@ -57,7 +57,7 @@ static void plans() {
             live += tree_row(p, T, c, col, &a, &b);
           }
           CHECK(live == G * T, "live columns %d of %d", live, G * T);
-          for (int e = 0; e < (by_rows ? 1 : 2); ++e) {
+          for (int e = 0; e < 2; ++e) {
             const TreeSmem s = tree_smem(p, d, e != 0, by_rows != 0);
             CHECK(s.stages >= 3 && s.stages <= kTreeMaxStages && s.total <= 227 * 1024, "smem %d stages %d", s.total, s.stages);
             CHECK(s.ones % 1024 == 0 && s.q % 1024 == 0 && s.p % 1024 == 0 && s.m % 16 == 0 && s.f % 16 == 0 && s.bars % 8 == 0, "smem alignment");
