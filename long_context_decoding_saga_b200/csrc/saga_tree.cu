@@ -29,9 +29,10 @@
 // a power of two, as the sum of two e4m3 numbers (4 + 4 of bf16's 8 bits,
 // exact for all elements but those 2^-14 below the row's largest); the weights
 // as the sum of three e5m2 numbers (each off by 2^-3 of what is left: 2^-9; with
-// two the error of an output over a long cache was twice that of rounding it).  A key row's scale multiplies its scores and a value
-// row's scale its weights, both in fp32 and before any rounding; the sums of
-// weights are fp32 sums of the unrounded ones.
+// two the error of an output over a long cache was twice that of rounding it).
+// A key row's scale multiplies its scores and a value row's scale its weights,
+// both in fp32 and before any rounding; the sums of weights are fp32 sums of the
+// unrounded ones (so a NaN score, whose pieces would be zeros, still shows).
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>
@@ -962,15 +963,9 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
         ok = mbar_wait(&bar.s_full[buf], (gt >> 1) & 1, abort_flag) &&
              (gt < 2 || mbar_wait(&bar.pv_done[buf], ((gt >> 1) - 1) & 1, abort_flag));
         tc_fence_after();
-        auto weights = [&]() {
-          uint8_t* at = p_buf + r * 16;
-          return test ? weigh<E4M3, true>(s_tmem, at, cols * kTreeTile, sums_here, mine, rw, cw)
-                      : weigh<E4M3, false>(s_tmem, at, cols * kTreeTile, sums_here, mine, rw, cw);
-        };
         // A segment's first tile.  bf16: any score that every column sees is a good enough reference, so the tile's
         // first row's; where that is a drafted row, the exact maxima.  8-bit weights want the maxima.
         const bool common = !E4M3 && (w.t0 + i) * kTreeTile < w.P;
-        float top = INFINITY;
         if (i == 0 && common) {
           if (quarter == 0) {
             Groups g = mine;
@@ -1001,49 +996,63 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
           }
           named_bar_sync(1 + wg, 128);
         }
-        if (i > 0 || common) top = weights();
-        if (named_bar_or(3, kEpiAll, top > kOver || !ok || *abort_flag != 0)) {
+        // One place for the weights' code (a kernel's first tiles pay for fetching it): a tile is weighed against the
+        // references as they are, and again after moving them if a score is too far above.
+        bool redo = i == 0 && !common;
+        if (redo && named_bar_or(3, kEpiAll, !ok || *abort_flag != 0)) {
+          ok = false;
+          break;
+        }
+        while (true) {
+          if (redo) {
+            // the general test serves every tile here: rows of a tile without drafted ones are seen by all
+            maxima<E4M3>(s_tmem, words, mine, rw, cw);
+            named_bar_sync(1 + wg, 128);
+            for (int c = et & 127; c < mine.count * 8; c += 128) {
+              const int ag = g0 + (c >> 3), col = ag / mine.groups * mine.nvp + ag % mine.groups * 8 + (c & 7);
+              const float4 x = *reinterpret_cast<const float4*>(words + col * 4);
+              const float now = fmaxf(fmaxf(x.x, x.y), fmaxf(x.z, x.w)) - (E4M3 ? kTopE5m2 : 0.f);
+              const float old = -cw.m[col], next = now > -INFINITY ? fmaxf(old, now) : old;
+              cw.m[col] = -next;
+              fac[col] = old == kUnset ? 0.f : ex2(old - next);
+            }
+            if (i > 0) {
+              // the products so far must be in the accumulators (a wait that gives up sets the abort flag, which the
+              // next tile sees)
+              mbar_wait(&bar.pv_done[buf ^ 1], ((gt - 1) >> 1) & 1, abort_flag);
+              tc_fence_after();
+            }
+            named_bar_sync(1 + wg, 128);
+            if (i > 0) {
+              Groups g = mine;
+#pragma unroll 1
+              for (int n = g.count; n > 0; --n, g.step()) {
+#pragma unroll
+                for (int part = 0; part < (D == 64 || E4M3 ? 1 : 2); ++part) {
+                  const uint32_t at = (part == 0 ? o_tmem : l_tmem) + lanes + g.col;
+                  float o[8];
+                  tmem_ld8(at, o);
+#pragma unroll
+                  for (int x = 0; x < 8; ++x) o[x] *= fac[g.col + x];
+                  tmem_st8(at, o);
+                }
+                if (E4M3 && lane < 8) sums[g.col + lane] *= fac[g.col + lane];
+              }
+            }
+          }
+          uint8_t* at = p_buf + r * 16;
+          const float top = test ? weigh<E4M3, true>(s_tmem, at, cols * kTreeTile, sums_here, mine, rw, cw)
+                                 : weigh<E4M3, false>(s_tmem, at, cols * kTreeTile, sums_here, mine, rw, cw);
+          if (redo) break;
+          if (!named_bar_or(3, kEpiAll, top > kOver || !ok || *abort_flag != 0)) break;
           // new references, or the end of it all: the 256 threads meet at the same barriers, so they go together
           if (named_bar_or(3, kEpiAll, !ok || *abort_flag != 0)) {
             ok = false;
             break;
           }
-          // the general test serves every tile here: rows of a tile without drafted ones are seen by all
-          maxima<E4M3>(s_tmem, words, mine, rw, cw);
-          named_bar_sync(1 + wg, 128);
-          for (int c = et & 127; c < mine.count * 8; c += 128) {
-            const int ag = g0 + (c >> 3), col = ag / mine.groups * mine.nvp + ag % mine.groups * 8 + (c & 7);
-            const float4 x = *reinterpret_cast<const float4*>(words + col * 4);
-            const float now = fmaxf(fmaxf(x.x, x.y), fmaxf(x.z, x.w)) - (E4M3 ? kTopE5m2 : 0.f);
-            const float old = -cw.m[col], next = now > -INFINITY ? fmaxf(old, now) : old;
-            cw.m[col] = -next;
-            fac[col] = old == kUnset ? 0.f : ex2(old - next);
-          }
-          if (i > 0) {
-            // the products so far must be in the accumulators (a wait that gives up sets the abort flag, which the
-            // next tile sees)
-            mbar_wait(&bar.pv_done[buf ^ 1], ((gt - 1) >> 1) & 1, abort_flag);
-            tc_fence_after();
-          }
-          named_bar_sync(1 + wg, 128);
-          if (i > 0) {
-            Groups g = mine;
-#pragma unroll 1
-            for (int n = g.count; n > 0; --n, g.step()) {
-#pragma unroll
-              for (int part = 0; part < (D == 64 || E4M3 ? 1 : 2); ++part) {
-                const uint32_t at = (part == 0 ? o_tmem : l_tmem) + lanes + g.col;
-                float o[8];
-                tmem_ld8(at, o);
-#pragma unroll
-                for (int k = 0; k < 8; ++k) o[k] *= fac[g.col + k];
-                tmem_st8(at, o);
-              }
-              if (E4M3 && lane < 8) sums[g.col + lane] *= fac[g.col + lane];
-            }
-          }
-          weights();
+          redo = true;
         }
+        if (!ok) break;
         fence_proxy_async_shared();
         tc_fence_before();
         __syncwarp();
@@ -1302,7 +1311,15 @@ __device__ __forceinline__ float row_maximum(uint32_t s_tmem, const Query& q) {
     tmem_ld32(s_tmem + h * 32, s);
     row_exponents<E4M3, TEST, false>(s, q, h);
 #pragma unroll
-    for (int i = 0; i < 32; ++i) most = fmaxf(most, E4M3 ? s[i] + __log2f(fmaxf(q.vs[h * 32 + i], kMinScale)) : s[i]);
+    for (int g = 0; g < 8; ++g) {
+      float4 lv = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (E4M3) {
+        const float4 vs = reinterpret_cast<const float4*>(q.vs + h * 32)[g];
+        lv = make_float4(__log2f(fmaxf(vs.x, kMinScale)), __log2f(fmaxf(vs.y, kMinScale)), __log2f(fmaxf(vs.z, kMinScale)),
+                         __log2f(fmaxf(vs.w, kMinScale)));
+      }
+      most = fmaxf(most, fmaxf(fmaxf(s[4 * g] + lv.x, s[4 * g + 1] + lv.y), fmaxf(s[4 * g + 2] + lv.z, s[4 * g + 3] + lv.w)));
+    }
   }
   return most;
 }
@@ -1484,9 +1501,9 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
         }
       }
       fence_proxy_async_shared();
-      if (E4M3) cp_async_wait_all();
       named_bar_sync(3, kEpiAll);
       if (lane == 0) mbar_arrive(bar.q_full);
+      if (E4M3) cp_async_wait_all();  // the first tile's scales, seen by all after its first barrier
       if (et == 0 && w.t0 == 0) {  // for the join, as above
         const TreeCut cut = *k.share_cut;
         const int place = cut.by_items ? 0 : tree_even_first(cut, blockIdx.x) + gt;
@@ -1517,20 +1534,16 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
         constexpr int WORDS = E4M3 ? 48 : 32;
         uint32_t weights[WORDS];
         float sum = 0.f, over = -INFINITY;
+        // A tile is weighed against the references as they are, and again after moving them if a score is too far
+        // above; a segment's first tile, which has none, after taking them from its maxima.
         auto weigh_rows = [&]() {
-          if (idle) return;
-          if (test) row_weights<E4M3, true>(s_tmem, q, weights, &sum, &over);
-          else row_weights<E4M3, false>(s_tmem, q, weights, &sum, &over);
-        };
-        if (i > 0) weigh_rows();
-        else over = INFINITY;  // a segment's first tile: the references come from its maxima
-        if (E4M3) cp_async_wait_all();  // the next tile's scales, seen by all after the vote
-        if (named_bar_or(3, kEpiAll, over > 0.f || !ok || *abort_flag != 0)) {
-          // new references, or the end of it all: the 256 threads meet at the same barriers, so they go together
-          if (named_bar_or(3, kEpiAll, !ok || *abort_flag != 0)) {
-            ok = false;
-            break;
+          if (!idle) {
+            if (test) row_weights<E4M3, true>(s_tmem, q, weights, &sum, &over);
+            else row_weights<E4M3, false>(s_tmem, q, weights, &sum, &over);
           }
+          if (E4M3) cp_async_wait_all();  // the next tile's scales, seen by all after the vote
+        };
+        auto move_references = [&]() {
           if (!idle) words[wg * 128 + r] = row_maximum<E4M3, true>(s_tmem, q);
           named_bar_sync(3, kEpiAll);
           const float now = fmaxf(words[r], words[128 + r]) - (E4M3 ? kTopE5m2 : 0.f), old = -q.nm;
@@ -1553,8 +1566,45 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
               tmem_st8(o_tmem + lanes + x, o);
             }
           }
-          weigh_rows();
-          named_bar_sync(3, kEpiAll);  // the words are read before the next tile's
+        };
+        // the 256 threads meet at the same barriers, so they give up together
+        auto given_up = [&]() { return named_bar_or(3, kEpiAll, !ok || *abort_flag != 0); };
+        auto vote = [&]() { return named_bar_or(3, kEpiAll, over > 0.f || !ok || *abort_flag != 0); };
+        if (!E4M3) {
+          if (i > 0) weigh_rows();
+          else over = INFINITY;
+          if (vote()) {
+            if (given_up()) {
+              ok = false;
+              break;
+            }
+            move_references();
+            weigh_rows();
+            named_bar_sync(3, kEpiAll);  // the words are read before they are written again
+          }
+        } else {
+          // one place for the weights' code, long as it is: the first tiles pay for fetching it (60 -> 57 us for a tree
+          // of 16 over 128K rows; with bf16 the same costs 5 %)
+          bool moved = i == 0;
+          if (moved && given_up()) {
+            ok = false;
+            break;
+          }
+          while (true) {
+            if (moved) move_references();
+            weigh_rows();
+            if (moved) {
+              named_bar_sync(3, kEpiAll);
+              break;
+            }
+            if (!vote()) break;
+            if (given_up()) {
+              ok = false;
+              break;
+            }
+            moved = true;
+          }
+          if (!ok) break;
         }
         if (!idle) {
           l += sum;
