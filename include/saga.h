@@ -371,7 +371,7 @@ SAGA_API int saga_norm_rope_append(const saga_shape* s, int tokens, const saga_r
                                    unsigned* status, void* stream);
 
 /* The append alone: cache rows starts[b] + t of present tokens = k[b, t],
- * v[b, t], into either format. */
+ * v[b, t], into either format.  The rows and the cache do not overlap. */
 SAGA_API int saga_kv_store(const saga_shape* s, int tokens, const saga_rows* k, const saga_rows* v,
                            const int* starts, const int* counts, const saga_cache* cache, unsigned* status,
                            void* stream);
@@ -398,13 +398,14 @@ SAGA_API int saga_kv_load(const saga_shape* s, const saga_cache* cache, int star
  *   tree_mask uint64 [B, tokens]; bits at or past counts[b] are ignored;
  *   1 <= tokens <= SAGA_TREE_MAX_TOKENS.
  * Scores, softmax statistics and sums are fp32; the softmax weights are rounded
- * to 16 bits before the product with the values.  Rows of absent tokens of out
- * are left as they are.  Cache rows that no present token sees may hold
+ * before the product with the values, to 8 significant bits (bf16 caches) or 9
+ * (8-bit caches).  Rows of absent tokens of out are left as they are.  Cache rows that no present token sees may hold
  * anything; a row that some token sees must be finite.  A prefix outside
  * [0, l_cap - counts[b]] is clamped and flagged in the status word (word 0 of
- * the workspace, saga_get_status).  workspace: saga_tree_workspace_bytes(s,
- * tokens) bytes of device memory, 256-byte aligned, zero-filled once before
- * first use; calls on one workspace must not overlap in time. */
+ * the workspace, saga_get_status).  out overlaps no other argument.
+ * workspace: saga_tree_workspace_bytes(s, tokens) bytes of device memory,
+ * 256-byte aligned, zero-filled once before first use; it serves calls of the
+ * shape with up to `tokens` tokens, which must not overlap in time. */
 #define SAGA_TREE_MAX_TOKENS 64
 SAGA_API size_t saga_tree_workspace_bytes(const saga_shape* s, int tokens);
 SAGA_API int saga_tree_attn(const saga_shape* s, int tokens, const void* q, const saga_cache* cache,

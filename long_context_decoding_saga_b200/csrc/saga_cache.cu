@@ -401,6 +401,10 @@ int run_rows(const saga_shape* s, int tokens, const saga_rows* q, const saga_row
     rc = check_rows(q, "q");
     if (rc) return rc;
     if (q_out == nullptr || !aligned16(q_out)) return api_fail(SAGA_ERR_ARG, "q_out must be a 16-byte aligned buffer");
+    // in place, a row must be written where it was read
+    if (q_out == q->data && ((s->h_q > 1 && q->head_stride != s->d) || (tokens > 1 && q->token_stride != (long long)s->h_q * s->d) ||
+                             (s->batch > 1 && q->batch_stride != (long long)tokens * s->h_q * s->d)))
+      return api_fail(SAGA_ERR_ARG, "q_out may be q only where q is dense");
   }
   rc = check_rows(k, "k");
   if (rc) return rc;
@@ -409,6 +413,7 @@ int run_rows(const saga_shape* s, int tokens, const saga_rows* q, const saga_row
   rc = check_cache(s, cache);
   if (rc) return rc;
   if (starts == nullptr) return api_fail(SAGA_ERR_ARG, "starts is NULL");
+  if ((reinterpret_cast<uintptr_t>(status) & 3u) != 0) return api_fail(SAGA_ERR_ARG, "status must be 4-byte aligned");
   RowParams p{};
   p.q = q != nullptr ? static_cast<const uint16_t*>(q->data) : nullptr;
   p.k = static_cast<const uint16_t*>(k->data);

@@ -1066,6 +1066,11 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
             if (lane < 8) sums[g.col + lane] += sums_here[g.col + lane];
         }
         if (tail && wg == 0) {
+          // a barrier's phase is known by its parity only, so what its stage held before must have been read: the
+          // values of the tile before, and the keys of the next
+          if (i > 0) mbar_wait(&bar.pv_done[buf ^ 1], ((gt - 1) >> 1) & 1, abort_flag);
+          if (i + 1 < nt) mbar_wait(&bar.s_full[buf ^ 1], ((gt + 1) >> 1) & 1, abort_flag);
+          __syncwarp();
           Ring vr = seg_ring;
           vr.jump(tree_value_place(i, nt, h.nv), stages);
           zero_unseen<D, E4M3>(p, k, vr, h.nv, r, !row_seen(w, seen, row));
@@ -1616,6 +1621,8 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
         __syncwarp();
         if (lane == 0) mbar_arrive(&bar.p_full[buf]);
         if (tail && wg == 0) {
+          // (the ring has at least 2 nv + 1 stages here, so these stages held something before this tile's keys, which
+          // have been read, and their barriers' phases cannot be mistaken)
           Ring vr = seg_ring;
           vr.jump(tree_value_place(i, nt, h.nv), stages);
           zero_unseen<D, E4M3>(p, k, vr, h.nv, r, !row_seen(w, seen, t0 + r));
@@ -1850,9 +1857,13 @@ size_t saga_tree_workspace_bytes(const saga_shape* s, int tokens) {
   int sms = 0;
   if (api_device_sms(&sms)) return 0;
   const int ctas = std::min(sms, kTreeMaxCtas);
-  const size_t columns = tree_sizes(s, tree_plan(s->h_q, s->h_k, s->h_v, tokens), ctas).total;
-  const TreePlan rows = tree_plan_rows(s->h_q, s->h_k, s->h_v, s->d, tokens);
-  return by_rows(rows, true) ? std::max(columns, tree_sizes(s, rows, ctas).total) : columns;  // of either format
+  size_t most = 0;  // of calls with fewer tokens too (padding makes some of them the larger), of either format
+  for (int t = 1; t <= tokens; ++t) {
+    most = std::max(most, tree_sizes(s, tree_plan(s->h_q, s->h_k, s->h_v, t), ctas).total);
+    const TreePlan rows = tree_plan_rows(s->h_q, s->h_k, s->h_v, s->d, t);
+    if (by_rows(rows, true)) most = std::max(most, tree_sizes(s, rows, ctas).total);
+  }
+  return most;
 }
 
 int saga_tree_attn(const saga_shape* s, int tokens, const void* q, const saga_cache* cache, const int* prefix_lens,

@@ -216,35 +216,7 @@ __host__ __device__ inline int tree_last_holder(const TreeCut& c, int i, int til
 }
 
 // The order of a segment's loads: K(t0), then for every t: K(t + 1) if there
-// is one, V(t, 0), V(t, 1), ...  v = -1 stands for the keys.
-struct TreeFeed {
-  int t, v;
-};
-__host__ __device__ inline TreeFeed tree_feed(const TreeWalk& w) { return TreeFeed{w.t0, -1}; }
-__host__ __device__ inline bool tree_feed_next(const TreeWalk& w, int nv, TreeFeed& f) {
-  if (f.v < 0) {
-    if (f.t == w.t0 && f.t + 1 < w.t1) {
-      ++f.t;
-    } else {
-      if (f.t > w.t0) --f.t;
-      f.v = 0;
-    }
-    return true;
-  }
-  if (++f.v < nv) return true;
-  if (f.t + 2 < w.t1) {
-    f.t += 2;
-    f.v = -1;
-    return true;
-  }
-  if (f.t + 1 < w.t1) {
-    ++f.t;
-    f.v = 0;
-    return true;
-  }
-  return false;
-}
-// Where V(t0 + i, 0) stands in that order.
+// is one, V(t, 0), V(t, 1), ...  Where V(t0 + i, 0) stands in that order:
 __host__ __device__ inline int tree_value_place(int i, int tiles, int nv) { return 1 + i * nv + (i + 1 < tiles ? i + 1 : tiles - 1); }
 
 // Where a query row (head jj of its key head's group, token t) sits.

@@ -91,7 +91,7 @@ def _bounds(q, K, V, prefix, n, masks, tau, D, fmt):
 
 
 def _check(heads, fmt, prefixes, T, masks=None, counts=None, tau_n=0, out_dtype=torch.float32, seed=0, l_cap=None,
-           spread=1.0, row_spread=0.0, q_scale=1.0, poison=False, tau_value=None):
+           spread=1.0, row_spread=0.0, q_scale=1.0, poison=False, tau_value=None, tau_rank=0):
     h_q, h_k, h_v, d = heads
     B = len(prefixes)
     l_cap = max(prefixes) + T + 3 if l_cap is None else l_cap
@@ -106,12 +106,12 @@ def _check(heads, fmt, prefixes, T, masks=None, counts=None, tau_n=0, out_dtype=
     tau = None
     if tau_value is not None:
         tau = np.full((B, h_q), tau_value, np.float32)
-    elif tau_n:
+    elif tau_n or tau_rank:
         tau = np.zeros((B, h_q), np.float32)
         for b in range(B):
             for j in range(h_q):
                 a = np.sort((K[b, j * h_k // h_q, :prefixes[b] + n[b]] @ qe[b, :max(n[b], 1), j].T).ravel() / np.sqrt(d))[::-1]
-                m = min(tau_n * max(n[b], 1), len(a) - 2)
+                m = min(tau_rank or tau_n * max(n[b], 1), len(a) - 2)
                 lo, hi = max(0, m - 20), min(len(a) - 1, m + 20)
                 gaps = a[lo:hi] - a[lo + 1:hi + 1]
                 i = lo + int(gaps.argmax())
@@ -142,7 +142,7 @@ def _check(heads, fmt, prefixes, T, masks=None, counts=None, tau_n=0, out_dtype=
     for b in range(B):
         exact, bound, border, es = _bounds(qe[b], K[b], V[b], prefixes[b], n[b], None if masks is None else masks[b],
                                            None if tau is None else tau[b].astype(np.float64), d, fmt)
-        if tau_n:
+        if tau_n or tau_rank:
             assert border > es, "the thresholds of this test are too near a score"
         got = out[b, :n[b]].double().cpu().numpy()
         if out_dtype == torch.bfloat16:
@@ -375,3 +375,173 @@ def test_a_served_step(fmt):
         assert (np.abs(outs["kept"][0].double().cpu().numpy() - exact) <= bound).all()
     counts = (K[0, 0, :P + 1] @ qg[0].T / np.sqrt(d) >= te).sum(axis=0)
     assert (counts >= 64).all()
+
+
+@pytest.mark.parametrize("fmt", [BF16, E4M3])
+@pytest.mark.parametrize("heads", [(8, 1, 8, 128), (16, 1, 16, 64), (16, 1, 16, 128)])
+@pytest.mark.parametrize("T,prefix", [(1, 9000), (16, 9000), (16, 8953), (3, 40)])
+def test_more_value_heads_than_tiles_in_flight(heads, T, prefix, fmt):
+    """Value heads of a chunk that do not fit the ring of tiles at once, with the drafted rows in a last tile that
+    has others before it (long runs), or in the last two; rows that nobody sees hold NaN."""
+    masks = [[0b1 if t == 0 else 1 << t | 1 for t in range(T)]]
+    if T > 2:
+        masks[0][2] = 0
+        masks[0][T - 1] &= ~4
+    _check(heads, fmt, [prefix] * 4, T, masks=masks * 4, seed=T, poison=True)
+
+
+# ---- chunks of many query rows: the other of the two kernels (see the rule in the source) for both formats
+MANY = [((32, 2, 8, 64), 12), ((12, 1, 4, 128), 40), ((32, 1, 32, 64), 33), ((64, 1, 8, 64), 16), ((3, 3, 1, 128), 64)]
+
+
+@pytest.mark.parametrize("fmt", [BF16, E4M3])
+@pytest.mark.parametrize("heads,T", MANY)
+@pytest.mark.parametrize("rank", [4, 200])
+def test_thresholds_of_many_rows(heads, T, rank, fmt):
+    """Thresholds at a rank among all scores of a head (with so many scores, those of higher ranks lie closer together
+    than es): some drafted tokens keep nothing, others several rows."""
+    _check(heads, fmt, [700], T, masks="tree", tau_rank=rank, seed=T + rank)
+
+
+@pytest.mark.parametrize("fmt", [BF16, E4M3])
+@pytest.mark.parametrize("heads,T", MANY)
+def test_many_rows_and_rows_that_nobody_sees(heads, T, fmt):
+    """Unseen rows hold NaN; some drafted tokens see a few rows, some none, and batch rows hold fewer tokens."""
+    masks = [[0 if t % 5 == 3 else 1 << t | (1 << (t // 2)) for t in range(T)] for _ in range(4)]
+    for row in masks:  # token 1's row is seen by nobody
+        for t in range(T):
+            row[t] &= ~2
+    _check(heads, fmt, [0, 126, 500, 1], T, masks=masks, counts=[T, T - 3, 5, T], seed=T, poison=True)
+
+
+@pytest.mark.parametrize("fmt", [BF16, E4M3])
+@pytest.mark.parametrize("heads,T", MANY[:3])
+@pytest.mark.parametrize("q_scale,spread,row_spread", [(12.0, 4.0, 0.0), (1e-3, 1.0, 0.0), (1.0, 1.0, 2.0),
+                                                       (2.0 ** 40, 2.0 ** -40, 0.0)])
+def test_magnitudes_of_many_rows(heads, T, q_scale, spread, row_spread, fmt):
+    _check(heads, fmt, [600], T, seed=11, q_scale=q_scale, spread=spread, row_spread=row_spread)
+
+
+@pytest.mark.parametrize("fmt", [BF16, E4M3])
+@pytest.mark.parametrize("T", [2, 20])
+def test_batch_rows_beyond_a_warp(T, fmt):
+    """More batch rows than a warp has lanes, many of them empty, of very different lengths."""
+    g = torch.Generator().manual_seed(12)
+    prefixes = [int(x) ** 2 // 40 for x in torch.randint(0, 200, (75,), generator=g)]
+    counts = [int(x) for x in torch.randint(-2, T + 1, (75,), generator=g)]
+    counts[:33] = [0] * 33
+    counts[-1] = T
+    _check((16, 2, 4, 128), fmt, prefixes, T, masks="tree", counts=counts, seed=13, l_cap=max(prefixes) + T)
+
+
+@pytest.mark.parametrize("value", [float("-inf"), float("inf"), float("nan")])
+@pytest.mark.parametrize("fmt", [BF16, E4M3])
+def test_threshold_that_keeps_all_or_nothing_of_many_rows(fmt, value):
+    _check((32, 2, 8, 64), fmt, [300], 12, tau_value=value, seed=14)
+
+
+@pytest.mark.parametrize("fmt", [BF16, E4M3])
+@pytest.mark.parametrize("T", [1, 16])
+def test_rows_beyond_32_bits_of_elements(T, fmt):
+    """The last batch row of a cache of more than 2^31 elements."""
+    heads, B, l_cap, P = (8, 1, 8, 128), 40, 66000, 65000
+    h_q, h_k, h_v, d = heads
+    assert B * h_v * l_cap * d > 2 ** 31
+    shape = saga.SagaShape.of(B, *heads, l_cap)
+    one = saga.SagaShape.of(1, *heads, l_cap)
+    g = torch.Generator().manual_seed(15)
+    small, K, V = _fill(one, fmt, g)
+    cache = saga.alloc_cache(shape, fmt)
+    for a, b in zip(cache._tensors(), small._tensors()):
+        if a is not None:
+            a[B - 1:].view(torch.uint8).copy_(b.view(torch.uint8))
+    q = torch.randn((B, T, h_q, d), generator=g).to(torch.bfloat16)
+    pl = torch.zeros(B, dtype=torch.int32)
+    pl[B - 1] = P
+    counts = torch.zeros(B, dtype=torch.int32)
+    counts[B - 1] = T
+    out = torch.zeros((B, T, h_q, d), device="cuda")
+    ws = saga.alloc_tree_workspace(shape, T)
+    saga.saga_tree_attn(shape, q.cuda(), cache, pl.cuda(), out, ws, counts=counts.cuda())
+    exact, bound, _, _ = _bounds(q[B - 1].double().numpy(), K[0], V[0], P, T, None, None, d, fmt)
+    assert (np.abs(out[B - 1].double().cpu().numpy() - exact) <= bound).all()
+    assert saga.saga_get_status(ws) == 0
+    # and its rows stored and read back there
+    x = torch.randn((B, 3, h_k + h_v, d), generator=g).to(torch.bfloat16).cuda()
+    starts = torch.full((B,), l_cap - 3, dtype=torch.int32).cuda()
+    saga.saga_kv_store(shape, x[:, :, :h_k], x[:, :, h_k:], cache, starts)
+    saga.saga_kv_store(one, x[B - 1:, :, :h_k], x[B - 1:, :, h_k:], small, starts[:1])
+    for a, b in zip(cache._tensors(), small._tensors()):
+        if a is not None:
+            assert torch.equal(a[B - 1:].view(torch.uint8), b.view(torch.uint8))
+    if fmt == E4M3:
+        outs = [torch.empty((s.batch, h_v, 1000, d), dtype=torch.bfloat16, device="cuda") for s in (shape, one)]
+        saga.saga_kv_load(shape, cache, l_cap - 1000, 1000, v_out=outs[0])
+        saga.saga_kv_load(one, small, l_cap - 1000, 1000, v_out=outs[1])
+        assert torch.equal(outs[0][B - 1:], outs[1])
+
+
+@pytest.mark.parametrize("fmt", [BF16, E4M3])
+def test_a_workspace_serves_fewer_tokens(fmt):
+    """A workspace for 64 tokens, reused from call to call, gives what a fresh one gives."""
+    heads = (32, 2, 8, 64)
+    shape = saga.SagaShape.of(2, *heads, 700)
+    g = torch.Generator().manual_seed(16)
+    cache, _, _ = _fill(shape, fmt, g)
+    pl = torch.tensor([600, 31], dtype=torch.int32).cuda()
+    ws = saga.alloc_tree_workspace(shape, 64)
+    for T in (64, 1, 33, 2, 5, 17, 6, 64, 9, 3):
+        q = torch.randn((2, T, 32, 64), generator=g).to(torch.bfloat16).cuda()
+        got, want = (torch.empty((2, T, 32, 64), device="cuda") for _ in range(2))
+        saga.saga_tree_attn(shape, q, cache, pl, got, ws)
+        saga.saga_tree_attn(shape, q, cache, pl, want, saga.alloc_tree_workspace(shape, T))
+        assert torch.equal(got, want)
+    assert saga.saga_get_status(ws) == 0
+    sizes = [saga.saga_tree_workspace_bytes(shape, t) for t in range(1, 65)]
+    assert sizes == sorted(sizes)
+
+
+@pytest.mark.parametrize("fmt", [BF16, E4M3])
+def test_two_graphs_on_one_workspace(fmt):
+    """Captured calls of both kernels that share a workspace, replayed in turn at other lengths."""
+    heads = (32, 2, 8, 64)
+    shape = saga.SagaShape.of(1, *heads, 2000)
+    g = torch.Generator().manual_seed(17)
+    cache, _, _ = _fill(shape, fmt, g)
+    pl = torch.zeros(1, dtype=torch.int32).cuda()
+    ws = saga.alloc_tree_workspace(shape, 16)
+    calls = []
+    for T in (2, 16):
+        q = torch.randn((1, T, 32, 64), generator=g).to(torch.bfloat16).cuda()
+        out = torch.zeros((1, T, 32, 64), device="cuda")
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            saga.saga_tree_attn(shape, q, cache, pl, out, ws)
+        calls.append((T, q, out, graph))
+    for P in (0, 1900, 130):
+        pl.fill_(P)
+        for _, _, _, graph in calls + calls:
+            graph.replay()
+        for T, q, out, _ in calls:
+            want = torch.empty_like(out)
+            saga.saga_tree_attn(shape, q, cache, pl, want, saga.alloc_tree_workspace(shape, T))
+            assert torch.equal(out, want)
+
+
+def test_rows_of_a_bf16_cache_as_tokens():
+    """A bf16 cache's rows, token and head dimensions exchanged, quantised into an 8-bit cache: the same codes as from
+    dense rows; and rows that several heads or tokens share (strides of zero)."""
+    heads, L = (8, 2, 8, 128), 300
+    shape = saga.SagaShape.of(2, *heads, L)
+    src, _, _ = _fill(shape, BF16, torch.Generator().manual_seed(18))
+    zero = torch.zeros(2, dtype=torch.int32).cuda()
+    a, b, c = (saga.alloc_cache(shape, E4M3) for _ in range(3))
+    k, v = src.k.transpose(1, 2), src.v.transpose(1, 2)
+    saga.saga_kv_store(shape, k, v, a, zero)
+    saga.saga_kv_store(shape, k.contiguous(), v.contiguous(), b, zero)
+    for x, y in zip(a._tensors(), b._tensors()):
+        assert torch.equal(x.view(torch.uint8), y.view(torch.uint8))
+    one = k[:1, :1, :1]
+    saga.saga_kv_store(shape, one.expand(2, L, 2, 128), one.expand(2, L, 8, 128), c, zero)
+    for x, y in ((c.k, a.k), (c.v, a.k), (c.k_scale, a.k_scale), (c.v_scale, a.k_scale)):
+        assert (x.view(torch.uint8) == y[:1, :1, :1].view(torch.uint8)).all() if x.dim() == 4 else (x == y[0, 0, 0]).all()

@@ -76,6 +76,19 @@ def test_append_refusals(lib, kw, code):
     assert lib.saga_last_error()
 
 
+@pytest.mark.parametrize("q", [_rows(8, head_stride=128, token_stride=1024), _rows(8, token_stride=640)])
+def test_in_place_needs_dense_queries(lib, q):
+    assert _append(lib, q=q) == saga.SAGA_ERR_ARG
+    assert b"dense" in lib.saga_last_error()
+
+
+def test_status_must_be_aligned(lib):
+    ref = ctypes.byref
+    assert lib.saga_kv_store(ref(_shape()), 2, ref(_rows(1)), ref(_rows(8)), FAKE, None, ref(_cache()), FAKE + 2,
+                             None) == saga.SAGA_ERR_ARG
+    assert b"status" in lib.saga_last_error()
+
+
 def test_load_refusals(lib):
     ref, s = ctypes.byref, _shape()
     call = lambda cache=_cache(), start=0, rows=4, ko=FAKE, vo=FAKE: lib.saga_kv_load(ref(s), ref(cache), start, rows, None, ko, vo, None)
