@@ -212,8 +212,11 @@ __device__ __forceinline__ void rows_of(const RowParams& p, const Tokens& k, con
 // shuffles.  The angles are the same for every head: they are computed once per
 // token into shared memory, while the first rows of each kind are on their way.
 // Rows are taken head by head, so neighbouring lanes write neighbouring cache
-// rows and scales.  For few tokens the time is that of one chain of loads; for
-// many it is bound by the instructions per row before HBM.
+// rows and scales.  For few tokens the time is that of one chain of loads (one
+// token: 3.3 us in a graph); for many it is bound by the instructions per row
+// before HBM (8191 tokens of 42 heads of 64 normed and rotated, 88 MB: 28 us,
+// 48 % of the copy rate; two prompts of up to 4097 tokens of 17 heads of 128,
+// half rotated, into an 8-bit cache, 56 MB: 18 us).
 template <int D, bool E4M3>
 __global__ void __launch_bounds__(kRowThreads) saga_rows_kernel(const RowParams p) {
   constexpr int LPR = D / 8;
@@ -246,7 +249,9 @@ __global__ void __launch_bounds__(kRowThreads) saga_rows_kernel(const RowParams 
 
 // Keys or values as they are into the cache (saga_kv_store), 32 bytes of a row
 // per thread: the quantisation is bound by its instructions, and a row's
-// magnitude, scale and addresses are then shared by 16 elements.
+// magnitude, scale and addresses are then shared by 16 elements (131072 tokens
+// of 5 heads of 128 into an 8-bit cache, 254 MB: 49 us, 80 % of the copy rate;
+// with 16 bytes per thread 74).
 template <int D, bool E4M3, int KIND>
 __device__ __forceinline__ void store_rows(const RowParams& p, const Tokens& k, const RowFeed<D, KIND>& f, uint4 a, uint4 b) {
   constexpr int LPR = D / 16, RPP = kRowThreads / LPR;
@@ -316,7 +321,8 @@ __global__ void __launch_bounds__(kRowThreads) saga_store_kernel(const RowParams
 
 // Codes of rows [start, start + rows) times their scales, rounded to bf16:
 // pieces of 8 codes, so that a warp's stores are 512 bytes on end, kPieces of
-// them in flight per thread (bound by HBM).
+// them in flight per thread.  Bound by HBM: 1.0 million rows of 64, 197 MB: 36 us,
+// 83 % of the copy rate (with pieces of 16 codes 41).
 constexpr int kPieces = 4;
 
 template <int D>
