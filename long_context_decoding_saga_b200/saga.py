@@ -10,6 +10,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 from typing import Optional
 
 import torch
@@ -143,7 +144,7 @@ def load(path: Optional[str] = None):
     lib.saga_read_probe.restype = _I
     lib.saga_noalloc_last_error.argtypes = []
     lib.saga_noalloc_last_error.restype = ctypes.c_char_p
-    cp, rp, np_ = ctypes.POINTER(_Cache), ctypes.POINTER(_Rows), ctypes.POINTER(_NormRope)
+    cp, rp, np_ = ctypes.POINTER(_Cache), _P, _P  # _Rows and _NormRope by reference or as bytes
     lib.saga_norm_rope_append.argtypes = [sp, _I, rp, rp, rp, np_, _P, _P, _P, _P, cp, _P, _P]
     lib.saga_norm_rope_append.restype = _I
     lib.saga_kv_store.argtypes = [sp, _I, rp, rp, _P, _P, cp, _P, _P]
@@ -481,17 +482,23 @@ def alloc_cache(shape: SagaShape, format: int = SAGA_CACHE_BF16, device=None) ->
 # The serving calls below cost a few microseconds on the GPU in their smallest forms, so their checks are written for
 # the case that everything is in order: one expression per tensor, and _expect for what is wrong where it is not.
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+# _Rows and _NormRope as bytes: a packed string costs half of a ctypes structure
+_pack_rows = struct.Struct("@Pqqq").pack
+_pack_norm_rope = struct.Struct("@ifPPPii").pack
 
 
 def _dense(t, name: str, dtype, shape, device: int):
     """The pointer of a dense tensor on `device` (None: no tensor)."""
     if t is None:
         return None
-    if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and t.get_device() == device
-            and t.is_contiguous()):
-        _expect(t, name, dtype, shape)
-        raise ValueError(f"{name} is on {t.device}, the cache on cuda:{device}")
-    return t.data_ptr()
+    try:
+        if t.dtype is dtype and t.shape == shape and t.get_device() == device and t.is_contiguous():
+            return t.data_ptr()
+    except AttributeError:  # no tensor
+        pass
+    _expect(t, name, dtype, shape)
+    raise ValueError(f"{name} is on {t.device}, the cache on cuda:{device}")
 
 
 def _status_word(t, device: int):
@@ -503,8 +510,8 @@ def _status_word(t, device: int):
     return t.data_ptr()
 
 
-def _rows(t, name: str, shape, device: int) -> "_Rows":
-    """A [B, T, heads, d] tensor or view whose last dimension is dense."""
+def _rows(t, name: str, shape, device: int) -> bytes:
+    """The _Rows of a [B, T, heads, d] tensor or view whose last dimension is dense."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if t.dtype is not torch.bfloat16:
@@ -517,7 +524,7 @@ def _rows(t, name: str, shape, device: int) -> "_Rows":
     if s1 != 1:
         raise ValueError(f"{name}: the elements of a head must be dense (strides {t.stride()})")
     # a dimension of one element has no stride that matters
-    return _Rows(t.data_ptr(), sb if shape[0] > 1 else 0, st if shape[1] > 1 else 0, sh if shape[2] > 1 else 0)
+    return _pack_rows(t.data_ptr(), sb if shape[0] > 1 else 0, st if shape[1] > 1 else 0, sh if shape[2] > 1 else 0)
 
 
 def _tokens(t, name: str) -> int:
@@ -539,7 +546,7 @@ def _cache_of(cache, shape: SagaShape):
 
 def _call(fn, device: int, stream, *args):
     """Calls fn(*args, stream) with `device` current, on `stream` or the device's current one."""
-    if device != torch.cuda.current_device():
+    if device != _current_device():
         with torch.cuda.device(device):
             return _call(fn, device, stream, *args)
     if stream is not None:
@@ -575,13 +582,12 @@ def saga_norm_rope_append(shape: SagaShape, q, k, v, cache: KVCache, starts, q_o
         if not isinstance(inv_freq, torch.Tensor) or inv_freq.dim() != 1:
             raise ValueError("inv_freq must be a 1-D tensor [rot_dim / 2]")
         rot = 2 * inv_freq.shape[0]
-    op = _NormRope(1 if norm else 0, eps, _dense(q_weight, "q_weight", torch.bfloat16, (d,), dev),
-                   _dense(k_weight, "k_weight", torch.bfloat16, (d,), dev),
-                   _dense(inv_freq, "inv_freq", torch.float32, (rot // 2,), dev), rot, 1 if interleaved else 0)
-    _call(load().saga_norm_rope_append, dev, stream, ctypes.byref(shape), T, ctypes.byref(rq), ctypes.byref(rk),
-          ctypes.byref(rv), ctypes.byref(op), _dense(starts, "starts", i32, (B,), dev),
-          _dense(positions, "positions", i32, (B, T), dev), _dense(counts, "counts", i32, (B,), dev),
-          _dense(q_out, "q_out", torch.bfloat16, q_shape, dev), c, _status_word(status, dev))
+    op = _pack_norm_rope(1 if norm else 0, eps, _dense(q_weight, "q_weight", torch.bfloat16, (d,), dev) or 0,
+                         _dense(k_weight, "k_weight", torch.bfloat16, (d,), dev) or 0,
+                         _dense(inv_freq, "inv_freq", torch.float32, (rot // 2,), dev) or 0, rot, 1 if interleaved else 0)
+    _call(load().saga_norm_rope_append, dev, stream, ctypes.byref(shape), T, rq, rk, rv, op,
+          _dense(starts, "starts", i32, (B,), dev), _dense(positions, "positions", i32, (B, T), dev),
+          _dense(counts, "counts", i32, (B,), dev), _dense(q_out, "q_out", torch.bfloat16, q_shape, dev), c, _status_word(status, dev))
 
 
 def saga_kv_store(shape: SagaShape, k, v, cache: KVCache, starts, counts=None, status=None, stream=None):
@@ -593,7 +599,7 @@ def saga_kv_store(shape: SagaShape, k, v, cache: KVCache, starts, counts=None, s
     rk, rv = _rows(k, "k", (B, T, shape.h_k, d), dev), _rows(v, "v", (B, T, shape.h_v, d), dev)
     if starts is None:
         raise ValueError("starts is required")
-    _call(load().saga_kv_store, dev, stream, ctypes.byref(shape), T, ctypes.byref(rk), ctypes.byref(rv),
+    _call(load().saga_kv_store, dev, stream, ctypes.byref(shape), T, rk, rv,
           _dense(starts, "starts", torch.int32, (B,), dev), _dense(counts, "counts", torch.int32, (B,), dev), c,
           _status_word(status, dev))
 

@@ -202,3 +202,15 @@ def test_binding_refusals_of_cuda_tensors():
         saga.saga_norm_rope_append(s, q, k, v, cache, starts, q.clone(), q_weight=z(64))  # a weight, no norm
     torch.cuda.synchronize()
     assert saga.saga_get_status(ws) == 0
+
+
+def test_packed_structures_are_the_headers():
+    """The binding's packed strings have the layout of the C structures."""
+    import struct
+    rows = saga._Rows.from_buffer_copy(saga._pack_rows(FAKE, 1 << 40, 8, 64))
+    assert struct.calcsize("@Pqqq") == ctypes.sizeof(saga._Rows)
+    assert (rows.data, rows.batch_stride, rows.token_stride, rows.head_stride) == (FAKE, 1 << 40, 8, 64)
+    op = saga._NormRope.from_buffer_copy(saga._pack_norm_rope(1, 0.5, FAKE, 0, FAKE + 16, 64, 1))
+    assert struct.calcsize("@ifPPPii") == ctypes.sizeof(saga._NormRope)
+    assert (op.norm, op.eps, op.q_weight, op.k_weight, op.inv_freq, op.rot_dim, op.interleaved) == \
+        (1, 0.5, FAKE, None, FAKE + 16, 64, 1)
