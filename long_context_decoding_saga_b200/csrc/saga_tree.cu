@@ -1180,8 +1180,8 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
 // slots, 41 % of the exponentials' pipe and 21 % of the tensor pipe.  Leaving out
 // the exponentials, the sums or the products changes it by less than 5 %; twice
 // the warps with half of the scores each take 8 % more (bf16; 8-bit ones spill).
-// 64 tokens over 8 ragged rows of up to 16K of 32/8/8 heads of 64: 107 us; 16
-// tokens over 128K 8-bit rows of 12/1/4 heads of 128: 57 us.
+// 64 tokens over 8 ragged rows of up to 16K of 32/8/8 heads of 64: 105 us; 16
+// tokens over 128K 8-bit rows of 12/1/4 heads of 128: 55 us.
 
 __device__ __forceinline__ void umma_bf16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc, uint32_t id, uint32_t accumulate) {
   asm volatile(
@@ -1234,17 +1234,17 @@ struct Query {
   const float *ks, *vs;    // 8-bit: the scales of those rows as keys, and as values of its value head
 };
 
-// 32 scores into exponents relative to the reference (RELATIVE) or not; bits:
-// which of them the query sees.
-template <bool E4M3, bool TEST, bool RELATIVE>
-__device__ __forceinline__ void row_exponents(float* s, const Query& q, int h) {
-  const uint32_t bits = (uint32_t)(q.sees >> (h * 32));
+// N scores from the `first`-th of the 64 on into exponents relative to the
+// reference (RELATIVE) or not.
+template <bool E4M3, bool TEST, bool RELATIVE, int N>
+__device__ __forceinline__ void row_exponents(float* s, const Query& q, int first) {
+  const uint32_t bits = (uint32_t)(q.sees >> first);
   const float f = E4M3 || TEST ? q.scale : q.scale * kLog2e, nm = RELATIVE ? q.nm : 0.f;
   const unsigned long long ff = two(f, f), ll = two(kLog2e, kLog2e), mm = two(nm, nm);
 #pragma unroll
-  for (int g = 0; g < 8; ++g) {
+  for (int g = 0; g < N / 4; ++g) {
     float4 ks;
-    if (E4M3) ks = reinterpret_cast<const float4*>(q.ks + h * 32)[g];
+    if (E4M3) ks = reinterpret_cast<const float4*>(q.ks + first)[g];
 #pragma unroll
     for (int i = 4 * g; i < 4 * g + 4; i += 2) {
       unsigned long long x = two(s[i], s[i + 1]);
@@ -1277,7 +1277,7 @@ __device__ __forceinline__ void row_weights(uint32_t s_tmem, const Query& q, uin
   for (int h = 0; h < 2; ++h) {
     float s[32];
     tmem_ld32(s_tmem + h * 32, s);
-    row_exponents<E4M3, TEST, true>(s, q, h);
+    row_exponents<E4M3, TEST, true, 32>(s, q, h * 32);
     if (!E4M3) {
 #pragma unroll
       for (int i = 0; i < 32; ++i) {
@@ -1319,24 +1319,18 @@ __device__ __forceinline__ void row_weights(uint32_t s_tmem, const Query& q, uin
   *over = E4M3 ? (*sum < 1e34f ? most - 32768.f : INFINITY) : most - kOverBf16;
 }
 
-template <bool E4M3, bool TEST>
+// The largest of the 64, in powers of two.  Once per segment, so its code is
+// kept short: a kernel's first tile waits for it to be fetched.
+template <bool E4M3>
 __device__ __forceinline__ float row_maximum(uint32_t s_tmem, const Query& q) {
   float most = -INFINITY;
 #pragma unroll 1
-  for (int h = 0; h < 2; ++h) {
-    float s[32];
-    tmem_ld32(s_tmem + h * 32, s);
-    row_exponents<E4M3, TEST, false>(s, q, h);
+  for (int h = 0; h < 64; h += 8) {
+    float s[8];
+    tmem_ld8(s_tmem + h, s);
+    row_exponents<E4M3, true, false, 8>(s, q, h);
 #pragma unroll
-    for (int g = 0; g < 8; ++g) {
-      float4 lv = make_float4(0.f, 0.f, 0.f, 0.f);
-      if (E4M3) {
-        const float4 vs = reinterpret_cast<const float4*>(q.vs + h * 32)[g];
-        lv = make_float4(__log2f(fmaxf(vs.x, kMinScale)), __log2f(fmaxf(vs.y, kMinScale)), __log2f(fmaxf(vs.z, kMinScale)),
-                         __log2f(fmaxf(vs.w, kMinScale)));
-      }
-      most = fmaxf(most, fmaxf(fmaxf(s[4 * g] + lv.x, s[4 * g + 1] + lv.y), fmaxf(s[4 * g + 2] + lv.z, s[4 * g + 3] + lv.w)));
-    }
+    for (int i = 0; i < 8; ++i) most = fmaxf(most, E4M3 ? s[i] + __log2f(fmaxf(q.vs[h + i], kMinScale)) : s[i]);
   }
   return most;
 }
@@ -1500,6 +1494,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
       if (wg == 0) out_row[r] = my_row;  // read below only, since the last segment's barriers
       named_bar_sync(3, kEpiAll);
       constexpr int LPR = D / 8, STEP = kEpiAll / LPR, FLIGHT = 4;
+      static_assert(kTreeMaxCols % (FLIGHT * STEP) == 0, "no row past the last is looked up");
       const int c = et % LPR;
 #pragma unroll 1
       for (int row0 = et / LPR; row0 - et / LPR < kTreeMaxCols; row0 += FLIGHT * STEP) {
@@ -1561,7 +1556,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
           if (E4M3) cp_async_wait_all();  // the next tile's scales, seen by all after the vote
         };
         auto move_references = [&]() {
-          if (!idle) words[wg * 128 + r] = row_maximum<E4M3, true>(s_tmem, q);
+          if (!idle) words[wg * 128 + r] = row_maximum<E4M3>(s_tmem, q);
           named_bar_sync(3, kEpiAll);
           const float now = fmaxf(words[r], words[128 + r]) - (E4M3 ? kTopE5m2 : 0.f), old = -q.nm;
           const float next = !idle && now > -INFINITY ? fmaxf(old, now) : old;
