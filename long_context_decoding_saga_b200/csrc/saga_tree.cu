@@ -25,11 +25,14 @@
 //
 // 8-bit caches: the codes go to the tensor cores as they are (kind::f8f6f4), so
 // a tile is read once, by TMA, and nothing is widened.  The other operands are
-// given in pieces whose products add up in the same accumulators: q, scaled by
-// a power of two, as the sum of two e4m3 numbers (4 + 4 of bf16's 8 bits,
-// exact for all elements but those 2^-14 below the row's largest); the weights
-// as the sum of three e5m2 numbers (each off by 2^-3 of what is left: 2^-9; with
-// two the error of an output over a long cache was twice that of rounding it).
+// given in pieces: q, scaled by a power of two, as the sum of two e4m3 numbers
+// (4 + 4 of bf16's 8 bits, exact for all elements but those 2^-14 below the
+// row's largest), whose products add up in the same accumulators; the weights as
+// the sum of three e5m2 numbers (each off by 2^-3 of what is left: 2^-9; with two
+// the error of an output over a long cache was twice that of rounding it).  With
+// queries as columns the pieces are columns of one product, added at a segment's
+// end: a product of 48 columns takes little longer than one of 16 (one token
+// over 128K rows 34.9 -> 30.7 us).
 // A key row's scale multiplies its scores and a value row's scale its weights,
 // both in fp32 and before any rounding; the sums of weights are fp32 sums of the
 // unrounded ones (so a NaN score, whose pieces would be zeros, still shows).
@@ -276,14 +279,17 @@ struct Bars {
 // warpgroup: `count` of them from `col` on, `groups` to a value head of `nvp`
 // columns, the first of them the `at`-th of its value head; v counts the value
 // heads from the warpgroup's first on.
+// pcol: the group's first column among the 8-bit weights' first pieces.
 struct Groups {
-  int col, at, v, count, groups, nvp;
+  int col, at, v, count, groups, nvp, pcol, pcols;
   __device__ __forceinline__ void step() {
     col += 8;
+    pcol += 8;
     if (++at == groups) {
       at = 0;
       ++v;
       col += nvp - groups * 8;
+      pcol += pcols - groups * 8;
     }
   }
 };
@@ -404,10 +410,10 @@ __device__ __forceinline__ float octet_sum(const float* v, int lane) {
 
 // Weights of a tile into P; returns the largest exponent of the thread's.
 // bf16: a row of P is 16 bytes per 8 columns.  8-bit: 8 bytes per 8 columns of
-// each of three pieces, `piece` bytes apart; and the weights' sums over the
-// warp's rows into here[column] (a tile that is done again overwrites them).
+// each of three pieces, which are columns of their own; and the weights' sums
+// over the warp's rows into here[column] (a tile that is done again overwrites them).
 template <bool E4M3, bool TEST>
-__device__ __forceinline__ float weigh(uint32_t s_tmem, uint8_t* p_row, int piece, float* here, Groups g, const Row& r,
+__device__ __forceinline__ float weigh(uint32_t s_tmem, uint8_t* p_row, float* here, Groups g, const Row& r,
                                        const Columns& c) {
   float top = -INFINITY;
   const int lane = lane_id();
@@ -417,7 +423,7 @@ __device__ __forceinline__ float weigh(uint32_t s_tmem, uint8_t* p_row, int piec
   for (int n = g.count; n > 0; --n) {
     float s[8];
     tmem_ld8_end(raw, s);
-    const int col = g.col;
+    const int col = g.col, pcol = g.pcol;
     const float vs = E4M3 && r.live ? r.scale[g.v * kTreeTile] : 0.f;
     g.step();
     if (n > 1) tmem_ld8_start(s_tmem + g.col, raw);  // the next group's scores, while this one's are weighed
@@ -446,10 +452,12 @@ __device__ __forceinline__ float weigh(uint32_t s_tmem, uint8_t* p_row, int piec
         untwo(mul2(two(s[2 * i], s[2 * i + 1]), two(vs, vs)), a, b);
         pieces_of(a, b, w[i], z[i], y[i]);
       }
-      uint8_t* at = p_row + (col >> 4) * 2048 + (col & 8);
-      *reinterpret_cast<uint2*>(at) = make_uint2(__byte_perm(w[0], w[1], 0x7531), __byte_perm(w[2], w[3], 0x7531));
-      *reinterpret_cast<uint2*>(at + piece) = make_uint2(__byte_perm(z[0], z[1], 0x7531), __byte_perm(z[2], z[3], 0x7531));
-      *reinterpret_cast<uint2*>(at + 2 * piece) = make_uint2(__byte_perm(y[0], y[1], 0x7531), __byte_perm(y[2], y[3], 0x7531));
+      auto put = [&](int c, const uint32_t* x) {
+        *reinterpret_cast<uint2*>(p_row + (c >> 4) * 2048 + (c & 8)) = make_uint2(__byte_perm(x[0], x[1], 0x7531), __byte_perm(x[2], x[3], 0x7531));
+      };
+      put(pcol, w);
+      put(pcol + g.groups * 8, z);
+      put(pcol + g.groups * 16, y);
       const float sum = octet_sum(s, lane);
       if ((lane & 3) == 0) here[col + octet_column(lane)] = sum;
     }
@@ -708,7 +716,7 @@ __device__ __forceinline__ void put_q8(uint8_t* at, int count, int row, int c, c
 // A tile of few columns is bound by its loads and one chain (scores, weights,
 // products); about 8 us go before the first product and to the end of the
 // join.  12/1/4 heads of 128 over 128K rows: one token from an 8-bit cache
-// (87 MB) 36 us, 4 tokens under thresholds from a bf16 cache (168 MB) 40 us,
+// (87 MB) 31 us, 4 tokens under thresholds from a bf16 cache (168 MB) 40 us,
 // 4.1 TB/s; 4 tokens over 1K rows of 8/1/8 heads of 64 15 us.
 template <int D, bool E4M3>
 __global__ void __launch_bounds__(kTreeThreads, 1)
@@ -723,8 +731,9 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
   const int warp = k.warp, lane = k.lane;
   const int stages = L.stages;
   const int cols = p.plan.cols;
+  const int pcols = tree_piece_cols(p.plan.groups);
   // two score buffers, the accumulators, and bf16 weights' sums (d = 64: lanes 64 .. 127 of the accumulators)
-  const int used = (D == 64 || E4M3 ? 3 : 4) * cols;
+  const int used = E4M3 ? 2 * cols + p.plan.nv * pcols : (D == 64 ? 3 : 4) * cols;
   const uint32_t tmem_cols = used <= 64 ? 64u : used <= 128 ? 128u : used <= 256 ? 256u : 512u;
   if (warp == 2 || warp == 3) {
     for (int i = threadIdx.x - 64; i < 2048 / 16; i += 64)
@@ -743,7 +752,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
   } else if (warp == 1) {
     if (any) {
       const uint32_t id_s = E4M3 ? idesc(kE4m3, kE4m3, kTreeTile, cols, false) : idesc(kBf16, kBf16, kTreeTile, cols, false);
-      const uint32_t id_o = E4M3 ? idesc(kE4m3, kE5m2, D, p.plan.nvp, true) : idesc(kBf16, kBf16, 128, p.plan.nvp, true);
+      const uint32_t id_o = E4M3 ? idesc(kE4m3, kE5m2, D, pcols, true) : idesc(kBf16, kBf16, 128, p.plan.nvp, true);
       const uint32_t id_l = idesc(kBf16, kBf16, 64, cols, true);
       const uint32_t ones = smem_u32(smem + L.ones), ring0 = smem_u32(smem);
       const uint64_t q_desc = desc_rows<D, E4M3>(smem_u32(smem + L.q));
@@ -799,22 +808,16 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
             }
             if (!ok) break;
             tc_fence_after();
-            const uint32_t a0 = ring0 + r.st * L.stage_bytes, d = o_tmem + v * p.plan.nvp;
+            const uint32_t a0 = ring0 + r.st * L.stage_bytes, d = o_tmem + v * (E4M3 ? pcols : p.plan.nvp);
             // bf16, d = 64: the block of ones stays where it is while the tile's rows go by
             const uint64_t a = desc_v<D, E4M3>(a0, E4M3 ? 0 : D == 64 ? ones - a0 : kTreeTile * 128);
-            const uint64_t b = p_desc + v * (p.plan.nvp >> (E4M3 ? 4 : 3)) * 128;
+            const uint64_t b = p_desc + v * (E4M3 ? pcols >> 4 : p.plan.nvp >> 3) * 128;
             constexpr uint64_t kStep = D == 64 ? 128ull - (128ull << 16) : 128ull;
             if (elect_one()) {
               if (E4M3) {  // 32 rows a step: 4 groups of 8
 #pragma unroll
                 for (int k = 0; k < kTreeTile / 32; ++k)
                   umma_8bit(d, a + k * (D * 2), b + k * 32, id_o, k > 0 ? 1u : first);
-#pragma unroll
-                for (int k = 0; k < kTreeTile / 32; ++k)
-                  umma_8bit(d, a + k * (D * 2), b + cols * 8 + k * 32, id_o, 1u);
-#pragma unroll
-                for (int k = 0; k < kTreeTile / 32; ++k)
-                  umma_8bit(d, a + k * (D * 2), b + cols * 16 + k * 32, id_o, 1u);
               } else {
 #pragma unroll
                 for (int k = 0; k < kTreeTile / 16; ++k)
@@ -870,6 +873,8 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
       mine.v = 0;
       const int v_first = g0 / mine.groups;
       mine.col = v_first * mine.nvp + mine.at * 8;
+      mine.pcols = pcols;
+      mine.pcol = v_first * pcols + mine.at * 8;
       const int nt = w.t1 - w.t0;
       // 8-bit: the scales of this thread's row, of the key head and of the warpgroup's value heads, a tile ahead
       const int v_count = mine.count > 0 ? (g0 + mine.count - 1) / mine.groups - v_first + 1 : 0;
@@ -1033,8 +1038,8 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
 #pragma unroll 1
               for (int n = g.count; n > 0; --n, g.step()) {
 #pragma unroll
-                for (int part = 0; part < (D == 64 || E4M3 ? 1 : 2); ++part) {
-                  const uint32_t at = (part == 0 ? o_tmem : l_tmem) + lanes + g.col;
+                for (int part = 0; part < (E4M3 ? 3 : D == 64 ? 1 : 2); ++part) {
+                  const uint32_t at = lanes + (E4M3 ? o_tmem + g.pcol + part * g.groups * 8 : (part == 0 ? o_tmem : l_tmem) + g.col);
                   float o[8];
                   tmem_ld8(at, o);
 #pragma unroll
@@ -1046,8 +1051,8 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
             }
           }
           uint8_t* at = p_buf + r * 16;
-          const float top = test ? weigh<E4M3, true>(s_tmem, at, cols * kTreeTile, sums_here, mine, rw, cw)
-                                 : weigh<E4M3, false>(s_tmem, at, cols * kTreeTile, sums_here, mine, rw, cw);
+          const float top = test ? weigh<E4M3, true>(s_tmem, at, sums_here, mine, rw, cw)
+                                 : weigh<E4M3, false>(s_tmem, at, sums_here, mine, rw, cw);
           if (redo) break;
           if (!named_bar_or(3, kEpiAll, top > kOver || !ok || *abort_flag != 0)) break;
           // new references, or the end of it all: the 256 threads meet at the same barriers, so they go together
@@ -1135,7 +1140,16 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
 #pragma unroll 1
         for (int n = g.count; n > 0; --n, g.step()) {
           float o[8];
-          tmem_ld8(o_tmem + lanes + g.col, o);
+          tmem_ld8(o_tmem + lanes + (E4M3 ? g.pcol : g.col), o);
+          if (E4M3) {
+#pragma unroll
+            for (int part = 1; part < 3; ++part) {
+              float more[8];
+              tmem_ld8(o_tmem + lanes + g.pcol + part * g.groups * 8, more);
+#pragma unroll
+              for (int k = 0; k < 8; ++k) o[k] += more[k];
+            }
+          }
           if (!has_d) continue;
           if (!whole) {  // padding too: nobody reads it
             float* dst = p.part_o + (slot * cols + g.col) * D + dd;
@@ -1845,10 +1859,10 @@ TreeSizes tree_sizes(const saga_shape* s, const TreePlan& plan, int ctas) {
 
 // Queries as rows from so many live rows a chunk on.  A tree of T tokens over
 // 32K rows of 32/2/8 heads of 64 (16 T live rows up to 128), as columns and as
-// rows: bf16 T = 4 20.3 and 20.8 us, T = 6 21.9 and 21.3; 8-bit T = 2 22.7 and
-// 25.7, T = 4 27.2 and 26.9.  Over 16K rows of 32/8/8 heads (4 T live rows):
-// bf16 T = 16 23.3 and 23.8, T = 24 29.0 and 26.9; 8-bit T = 12 32.5 and 33.8,
-// T = 16 37.3 and 34.5.
+// rows: bf16 T = 4 20.3 and 20.8 us, T = 6 21.9 and 21.3; 8-bit T = 2 21.7 and
+// 25.5, T = 4 26.4 and 26.2.  Over 16K rows of 32/8/8 heads (4 T live rows):
+// bf16 T = 16 23.3 and 23.8, T = 24 29.0 and 26.9; 8-bit T = 12 32.3 and 32.8,
+// T = 16 37.2 and 33.4.
 constexpr int kTreeRowsBf16 = 80, kTreeRowsE4m3 = 56;
 bool by_rows(const TreePlan& rows, bool e4m3) { return tree_live_rows(rows) >= (e4m3 ? kTreeRowsE4m3 : kTreeRowsBf16); }
 
@@ -1868,7 +1882,7 @@ size_t saga_tree_workspace_bytes(const saga_shape* s, int tokens) {
   const int ctas = std::min(sms, kTreeMaxCtas);
   size_t most = 0;  // of calls with fewer tokens too (padding makes some of them the larger), of either format
   for (int t = 1; t <= tokens; ++t) {
-    most = std::max(most, tree_sizes(s, tree_plan(s->h_q, s->h_k, s->h_v, t), ctas).total);
+    for (bool e4m3 : {false, true}) most = std::max(most, tree_sizes(s, tree_plan(s->h_q, s->h_k, s->h_v, t, e4m3), ctas).total);
     const TreePlan rows = tree_plan_rows(s->h_q, s->h_k, s->h_v, s->d, t);
     if (by_rows(rows, true)) most = std::max(most, tree_sizes(s, rows, ctas).total);
   }
@@ -1894,7 +1908,7 @@ int saga_tree_attn(const saga_shape* s, int tokens, const void* q, const saga_ca
   const bool e4m3 = cache->format == SAGA_CACHE_E4M3;
   const TreePlan rows_plan = tree_plan_rows(s->h_q, s->h_k, s->h_v, s->d, tokens);
   const bool as_rows = by_rows(rows_plan, e4m3);
-  p.plan = as_rows ? rows_plan : tree_plan(s->h_q, s->h_k, s->h_v, tokens);
+  p.plan = as_rows ? rows_plan : tree_plan(s->h_q, s->h_k, s->h_v, tokens, e4m3);
   const TreeSizes z = tree_sizes(s, p.plan, std::min(sms, kTreeMaxCtas));
   if (ws_bytes < z.total) return api_fail(SAGA_ERR_WORKSPACE, "workspace has %zu bytes, needs %zu", ws_bytes, z.total);
   p.smem = tree_smem(p.plan, s->d, e4m3, as_rows);

@@ -29,7 +29,13 @@ struct TreePlan {
   int groups;  // 8-column groups with a live column, per value head of a chunk
 };
 
-__host__ __device__ inline TreePlan tree_plan(int h_q, int h_k, int h_v, int T) {
+// 8-bit weights: the columns of a value head in the second product, which are
+// its column groups in three pieces one after the other, padded.
+__host__ __device__ inline int tree_piece_cols(int groups) { return (3 * 8 * groups + 15) / 16 * 16; }
+
+// 8-bit: the accumulators, which have a column per piece, and two buffers of
+// scores fit the 512 columns of TMEM.
+__host__ __device__ inline TreePlan tree_plan(int h_q, int h_k, int h_v, int T, bool e4m3) {
   TreePlan p;
   const int G = h_q / h_k, per_v = h_q / h_v;
   p.hpv = per_v < G ? per_v : G;
@@ -38,7 +44,9 @@ __host__ __device__ inline TreePlan tree_plan(int h_q, int h_k, int h_v, int T) 
   const int unit = 16;  // columns that a product with M = 128 is made of
   const int padded = (p.rows + unit - 1) / unit * unit;
   if (padded <= kTreeMaxCols) {
-    const int per = kTreeMaxCols / padded;
+    int per = kTreeMaxCols / padded;
+    const int room = 512 / (2 * padded + tree_piece_cols((p.rows + 7) / 8));
+    if (e4m3 && per > room) per = room > 0 ? room : 1;
     p.chunks = (p.nvh + per - 1) / per;
     p.nv = (p.nvh + p.chunks - 1) / p.chunks;
     p.chunks = (p.nvh + p.nv - 1) / p.nv;
@@ -266,7 +274,8 @@ __host__ __device__ inline TreeSmem tree_smem(const TreePlan& p, int d, bool e4m
   s.stage_bytes = kTreeTile * d * (e4m3 ? 1 : 2);
   const int budget = 227 * 1024 - 1024;  // less the slack that aligns the base to 1024 bytes
   const int q_bytes = p.cols * d * 2;
-  s.p_bytes = by_rows ? 0 : p.cols * kTreeTile * (e4m3 ? 3 : 2);  // by rows the weights are in TMEM
+  // by rows the weights are in TMEM
+  s.p_bytes = by_rows ? 0 : kTreeTile * (e4m3 ? p.nv * tree_piece_cols(p.groups) : p.cols * 2);
   const int words = p.cols * (8 + 5 * 4 + 4 * 4);
   const int sums = by_rows || !e4m3 ? 0 : 2 * p.cols * 4 * 4;
   const int eight = e4m3 ? sums + 2 * (by_rows ? 1 : 2) * (1 + p.nv) * kTreeTile * 4 : 0;

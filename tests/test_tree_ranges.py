@@ -32,8 +32,15 @@ static void plans() {
       if (h_q % h_k || h_q % h_v || (h_v % h_k && h_k % h_v) || h_q / h_k > (d == 64 ? 64 : 32)) continue;
       if (h_v > h_k && h_v / h_k > 32) continue;
       for (int T : Ts) {
-        for (int by_rows = 0; by_rows < 2; ++by_rows) {
-          const TreePlan p = by_rows ? tree_plan_rows(h_q, h_k, h_v, d, T) : tree_plan(h_q, h_k, h_v, T);
+        for (int which = 0; which < 3; ++which) {  // columns, columns of 8-bit weights, rows
+          const bool by_rows = which == 2;
+          const TreePlan p = by_rows ? tree_plan_rows(h_q, h_k, h_v, d, T) : tree_plan(h_q, h_k, h_v, T, which == 1);
+          // 8-bit weights come as columns only where a chunk by rows has fewer than 56 rows
+          if (which == 1) {
+            if (tree_live_rows(tree_plan_rows(h_q, h_k, h_v, d, T)) >= 56) continue;
+            const int pieces = tree_piece_cols(p.groups);
+            CHECK(pieces <= 256 && pieces >= 24 * p.groups && 2 * p.cols + p.nv * pieces <= 512, "pieces");
+          }
           const int G = h_q / h_k;
           CHECK(p.cols <= kTreeMaxCols && p.cols % 16 == 0 && p.nv * p.nvp <= p.cols, "cols");
           if (by_rows) CHECK(p.nv * d <= 256 && tree_live_rows(p) <= 128, "rows");
@@ -58,6 +65,7 @@ static void plans() {
           }
           CHECK(live == G * T, "live columns %d of %d", live, G * T);
           for (int e = 0; e < 2; ++e) {
+            if (which < 2 && e != which) continue;
             const TreeSmem s = tree_smem(p, d, e != 0, by_rows != 0);
             // rows: what the stages of a tile's values held before is older than the tile's keys
             if (by_rows) CHECK(s.stages >= 2 * p.nv + 1, "stages %d of %d value heads", s.stages, p.nv);
