@@ -215,8 +215,8 @@ __device__ __forceinline__ void rows_of(const RowParams& p, const Tokens& k, con
 // Rows are taken head by head, so neighbouring lanes write neighbouring cache
 // rows and scales.  For few tokens the time is that of one chain of loads (one
 // token: 3.3 us in a graph); for many it is bound by the instructions per row
-// before HBM (8191 tokens of 42 heads of 64 normed and rotated, 88 MB: 28 us,
-// 48 % of the copy rate; two prompts of up to 4097 tokens of 17 heads of 128,
+// before HBM (8191 tokens of 42 heads of 64 normed and rotated, 88 MB: 25 us,
+// 54 % of the copy rate; two prompts of up to 4097 tokens of 17 heads of 128,
 // half rotated, into an 8-bit cache, 56 MB: 18 us).
 template <int D, bool E4M3>
 __global__ void __launch_bounds__(kRowThreads) saga_rows_kernel(const RowParams p) {
