@@ -21,7 +21,9 @@
 //
 // bf16 caches: weights are rounded to bf16, and what they are divided by is the
 // sum of the rounded weights: a row of ones beside V in the second product adds
-// them up in fp32.
+// them up in fp32.  Where a value head has at most 8 columns, half of its 16 are
+// padding, and what a weight lost in rounding goes there as a second bf16 number:
+// the same products then give outputs as exact as fp32 weights do.
 //
 // 8-bit caches: the codes go to the tensor cores as they are (kind::f8f6f4), so
 // a tile is read once, by TMA, and nothing is widened.  The other operands are
@@ -438,6 +440,13 @@ __device__ __forceinline__ float weigh(uint32_t s_tmem, uint8_t* p_row, float* h
 #pragma unroll
       for (int i = 0; i < 4; ++i) w[i] = pack_bf16(s[2 * i], s[2 * i + 1]);
       *reinterpret_cast<uint4*>(p_row + (col >> 3) * 2048) = make_uint4(w[0], w[1], w[2], w[3]);
+      if (g.groups == 1) {  // what was rounded off, into the padding
+        uint32_t z[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          z[i] = pack_bf16(s[2 * i] - __uint_as_float(w[i] << 16), s[2 * i + 1] - __uint_as_float(w[i] & 0xffff0000u));
+        *reinterpret_cast<uint4*>(p_row + ((col >> 3) + 1) * 2048) = make_uint4(z[0], z[1], z[2], z[3]);
+      }
     } else {
       float most = s[0];
 #pragma unroll
@@ -1038,8 +1047,10 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
 #pragma unroll 1
               for (int n = g.count; n > 0; --n, g.step()) {
 #pragma unroll
-                for (int part = 0; part < (E4M3 ? 3 : D == 64 ? 1 : 2); ++part) {
-                  const uint32_t at = lanes + (E4M3 ? o_tmem + g.pcol + part * g.groups * 8 : (part == 0 ? o_tmem : l_tmem) + g.col);
+                for (int part = 0; part < (E4M3 ? 3 : D == 64 ? 2 : 4); ++part) {
+                  if (!E4M3 && (part & 1) != 0 && g.groups > 1) continue;
+                  const uint32_t at = lanes + (E4M3 ? o_tmem + g.pcol + part * g.groups * 8
+                                                    : (part < 2 ? o_tmem : l_tmem) + g.col + (part & 1) * 8);
                   float o[8];
                   tmem_ld8(at, o);
 #pragma unroll
@@ -1118,6 +1129,12 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
         for (int n = g.count; n > 0; --n, g.step()) {
           float l[8];
           tmem_ld8((D == 64 ? o_tmem : l_tmem) + lanes + g.col, l);
+          if (g.groups == 1) {
+            float more[8];
+            tmem_ld8((D == 64 ? o_tmem : l_tmem) + lanes + g.col + 8, more);
+#pragma unroll
+            for (int k = 0; k < 8; ++k) l[k] += more[k];
+          }
           float sum = l[0];
 #pragma unroll
           for (int k = 1; k < 8; ++k) sum = lane == k ? l[k] : sum;
@@ -1141,14 +1158,13 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
         for (int n = g.count; n > 0; --n, g.step()) {
           float o[8];
           tmem_ld8(o_tmem + lanes + (E4M3 ? g.pcol : g.col), o);
-          if (E4M3) {
+          const int parts = E4M3 ? 3 : g.groups == 1 ? 2 : 1;
+#pragma unroll 1
+          for (int part = 1; part < parts; ++part) {
+            float more[8];
+            tmem_ld8(o_tmem + lanes + (E4M3 ? g.pcol : g.col) + part * g.groups * 8, more);
 #pragma unroll
-            for (int part = 1; part < 3; ++part) {
-              float more[8];
-              tmem_ld8(o_tmem + lanes + g.pcol + part * g.groups * 8, more);
-#pragma unroll
-              for (int k = 0; k < 8; ++k) o[k] += more[k];
-            }
+            for (int k = 0; k < 8; ++k) o[k] += more[k];
           }
           if (!has_d) continue;
           if (!whole) {  // padding too: nobody reads it
