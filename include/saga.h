@@ -399,7 +399,8 @@ SAGA_API int saga_kv_load(const saga_shape* s, const saga_cache* cache, int star
  *   1 <= tokens <= SAGA_TREE_MAX_TOKENS.
  * Scores, softmax statistics and sums are fp32; the softmax weights are rounded
  * before the product with the values, to 8 significant bits or more (bf16
- * caches) or 9 (8-bit caches).  Rows of absent tokens of out are left as they are.  Cache rows that no present token sees may hold
+ * caches) or 9 (8-bit caches).  Rows of absent tokens of out are left as they
+ * are.  Cache rows that no present token sees may hold
  * anything; a row that some token sees must be finite.  A prefix outside
  * [0, l_cap - counts[b]] is clamped and flagged in the status word (word 0 of
  * the workspace, saga_get_status).  out overlaps no other argument.

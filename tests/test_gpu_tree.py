@@ -390,6 +390,26 @@ def test_more_value_heads_than_tiles_in_flight(heads, T, prefix, fmt):
     _check(heads, fmt, [prefix] * 4, T, masks=masks * 4, seed=T, poison=True)
 
 
+@pytest.mark.parametrize("heads,T", [((8, 1, 8, 64), 4), ((8, 1, 8, 128), 1), ((12, 1, 4, 128), 2), ((32, 2, 8, 64), 2)])
+def test_few_columns_lose_nothing_to_bf16_weights(heads, T):
+    """Up to 8 columns of a value head: a weight is two bf16 numbers, off by 2^-8 of 2^-8 of it, and so is the sum it is
+    divided by: 2^-15 in place of 2^-7 in the bound."""
+    h_q, h_k, h_v, d = heads
+    assert h_q // h_v * T <= 8
+    P = 900
+    shape = saga.SagaShape.of(1, *heads, P + T)
+    g = torch.Generator().manual_seed(19)
+    cache, K, V = _fill(shape, BF16, g)
+    q = torch.randn((1, T, h_q, d), generator=g).to(torch.bfloat16)
+    out = torch.empty((1, T, h_q, d), device="cuda")
+    saga.saga_tree_attn(shape, q.cuda(), cache, torch.tensor([P], dtype=torch.int32).cuda(), out,
+                        saga.alloc_tree_workspace(shape, T))
+    exact, bound, _, _ = _bounds(q[0].double().numpy(), K[0], V[0], P, T, None, None, d, BF16)
+    spread, _ = so.attend(q[0].double().numpy(), K[0], np.abs(V[0]), P, T, None, None)
+    bound = bound - spread * (2.0 ** -7 + 2.0 ** -14 - 2.0 ** -15 - 2.0 ** -28)
+    assert (np.abs(out[0].double().cpu().numpy() - exact) <= bound).all()
+
+
 # ---- chunks of many query rows: the other of the two kernels (see the rule in the source) for both formats
 MANY = [((32, 2, 8, 64), 12), ((12, 1, 4, 128), 40), ((32, 1, 32, 64), 33), ((64, 1, 8, 64), 16), ((3, 3, 1, 128), 64)]
 
