@@ -483,7 +483,8 @@ __device__ __forceinline__ void maxima(uint32_t s_tmem, float* words, Groups g, 
     float s[8];
     tmem_ld8(s_tmem + g.col, s);
     exponents<E4M3, true, false>(s, r, g.col, c);
-    const float lv = E4M3 ? __log2f(fmaxf(r.scale[g.v * kTreeTile], kMinScale)) : 0.f;
+    // (the scale of a row that no token sees may be anything, an infinity too)
+    const float lv = E4M3 && r.live ? __log2f(fmaxf(r.scale[g.v * kTreeTile], kMinScale)) : 0.f;
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       const uint32_t k = __reduce_max_sync(0xffffffffu, float_key(s[i] + lv));
