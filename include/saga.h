@@ -401,7 +401,8 @@ SAGA_API int saga_kv_load(const saga_shape* s, const saga_cache* cache, int star
  * before the product with the values, to 8 significant bits or more (bf16
  * caches) or 9 (8-bit caches).  Rows of absent tokens of out are left as they
  * are.  Cache rows that no present token sees may hold
- * anything; a row that some token sees must be finite.  A prefix outside
+ * anything; a row that some token sees must be finite (a NaN in it
+ * makes the outputs that it belongs to NaN).  A prefix outside
  * [0, l_cap - counts[b]] is clamped and flagged in the status word (word 0 of
  * the workspace, saga_get_status).  out overlaps no other argument.
  * workspace: saga_tree_workspace_bytes(s, tokens) bytes of device memory,

@@ -217,6 +217,14 @@ __device__ __forceinline__ float ex2(float x) {
   return y;
 }
 
+// A threshold that is no number keeps nothing.
+__device__ __forceinline__ float threshold(float tau) { return tau == tau ? tau : INFINITY; }
+
+// What a row's products are multiplied by, from the sum of its weights: 0 where
+// nothing was kept, and NaN where the sum is no number, so that a NaN among what
+// the row sees shows in its output.
+__device__ __forceinline__ float inverse_of(float sum) { return sum == 0.f ? 0.f : sum < INFINITY ? 1.f / sum : NAN; }
+
 __device__ __forceinline__ __half2 as_half2(uint32_t x) { return reinterpret_cast<const __half2&>(x); }
 __device__ __forceinline__ uint32_t pack_half(float a, float b) {
   const __half2 h = __floats2half2_rn(a, b);
@@ -369,8 +377,8 @@ __device__ __forceinline__ void exponents(float* s, const Row& r, int col, const
       if (E4M3) x = mul2(x, two(cc[i], cc[i + 1]));
       float a, b;
       untwo(x, a, b);
-      keep0 = a >= tt[i] && (seen >> i & 1u) != 0u;
-      keep1 = b >= tt[i + 1] && (seen >> i & 2u) != 0u;
+      keep0 = !(a < tt[i]) && (seen >> i & 1u) != 0u;  // a NaN stays, so that it shows
+      keep1 = !(b < tt[i + 1]) && (seen >> i & 2u) != 0u;
       if (RELATIVE) x = fma2(x, E4M3 ? two(1.f, 1.f) : ll, two(mm[i], mm[i + 1]));
       else if (!E4M3) x = mul2(x, ll);
     } else if (E4M3) {
@@ -910,7 +918,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
         int jj, t;
         if (tree_row(p.plan, p.tokens, h.chunk, et, &jj, &t) && t < w.n) {
           my_row = (w.b * p.tokens + t) * p.h_q + h.kh * G + jj;
-          my_tau = p.tau != nullptr ? p.tau[w.b * p.h_q + h.kh * G + jj] : -INFINITY;
+          my_tau = p.tau != nullptr ? threshold(p.tau[w.b * p.h_q + h.kh * G + jj]) : -INFINITY;
           my_mask = p.mask != nullptr ? p.mask[(size_t)w.b * p.tokens + t] : (2ull << t) - 1ull;
         }
       }
@@ -1118,7 +1126,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
           const float* x = reinterpret_cast<const float*>(smem + L.sums) + col;
           const float sum = (x[0] + x[cols]) + (x[2 * cols] + x[3 * cols]);
           if (whole) {
-            fac[col] = sum > 0.f ? 1.f / sum : 0.f;
+            fac[col] = inverse_of(sum);
           } else {
             p.part_l[slot * cols + col] = sum;
             p.part_m[slot * cols + col] = -cw.m[col];
@@ -1141,7 +1149,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
           for (int k = 1; k < 8; ++k) sum = lane == k ? l[k] : sum;
           if (lane < 8) {
             if (whole) {
-              fac[g.col + lane] = sum > 0.f ? 1.f / sum : 0.f;
+              fac[g.col + lane] = inverse_of(sum);
             } else {
               p.part_l[slot * cols + g.col + lane] = sum;
               p.part_m[slot * cols + g.col + lane] = -cw.m[g.col + lane];
@@ -1178,7 +1186,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
           for (int k = 0; k < 8; ++k) {
             const int row = out_row[g.col + k];
             if (row < 0) continue;
-            const float f = fac[g.col + k], y = f > 0.f ? o[k] * f : 0.f;
+            const float f = fac[g.col + k], y = f == 0.f ? 0.f : o[k] * f;
             if (p.out_bf16) static_cast<__nv_bfloat16*>(p.out)[(size_t)row * D + dd] = __float2bfloat16(y);
             else static_cast<float*>(p.out)[(size_t)row * D + dd] = y;
           }
@@ -1284,7 +1292,7 @@ __device__ __forceinline__ void row_exponents(float* s, const Query& q, int firs
         x = mul2(x, ff);
         float a, b;
         untwo(x, a, b);
-        const bool keep0 = a >= q.tau && (bits >> i & 1u) != 0u, keep1 = b >= q.tau && (bits >> i & 2u) != 0u;
+        const bool keep0 = !(a < q.tau) && (bits >> i & 1u) != 0u, keep1 = !(b < q.tau) && (bits >> i & 2u) != 0u;
         if (E4M3) x = RELATIVE ? fma2(x, two(1.f, 1.f), mm) : x;
         else x = RELATIVE ? fma2(x, ll, mm) : mul2(x, ll);
         untwo(x, s[i], s[i + 1]);
@@ -1499,7 +1507,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
         int jj, t;
         if (tree_row(p.plan, p.tokens, h.chunk, r, &jj, &t) && t < w.n) {
           my_row = (w.b * p.tokens + t) * p.h_q + h.kh * G + jj;
-          my_tau = p.tau != nullptr ? p.tau[w.b * p.h_q + h.kh * G + jj] : -INFINITY;
+          my_tau = p.tau != nullptr ? threshold(p.tau[w.b * p.h_q + h.kh * G + jj]) : -INFINITY;
           my_mask = all & (p.mask != nullptr ? p.mask[(size_t)w.b * p.tokens + t] : (2ull << t) - 1ull);
         }
       }
@@ -1683,7 +1691,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
         p.part_l[slot * kTreeMaxCols + r] = total;
         p.part_m[slot * kTreeMaxCols + r] = -q.nm;
       }
-      const float inv = total > 0.f ? 1.f / total : 0.f;
+      const float inv = inverse_of(total);
       if (!idle) {
         const int mine = r / p.plan.rpc;  // this row's value head of the chunk
         const int v_lo = (quarter * 32) / p.plan.rpc, v_hi = min((quarter * 32 + 31) / p.plan.rpc, h.nv - 1);
@@ -1701,7 +1709,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
               continue;
             }
 #pragma unroll
-            for (int y = 0; y < 32; ++y) o[y] = inv > 0.f ? o[y] * inv : 0.f;
+            for (int y = 0; y < 32; ++y) o[y] = inv == 0.f ? 0.f : o[y] * inv;
             if (p.out_bf16) {
               uint4* dst = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.out) + (size_t)my_row * D + x);
 #pragma unroll
@@ -1774,8 +1782,8 @@ __global__ void __launch_bounds__(kJoinThreads) saga_tree_join_kernel(const Tree
       pm = p.part_m[slot0 * p.plan.cols + spot.col + (base + lane) * step];
       pl = p.part_l[slot0 * p.plan.cols + spot.col + (base + lane) * step];
     }
-    const float now = fmaxf(top, warp_max(pl > 0.f ? pm : kUnset));
-    const float f = ex2(top - now), wt = pl > 0.f ? ex2(pm - now) : 0.f;
+    const float now = fmaxf(top, warp_max(pl != 0.f ? pm : kUnset));
+    const float f = ex2(top - now), wt = pl != 0.f ? ex2(pm - now) : 0.f;
     top = now;
     float add = wt * pl;
 #pragma unroll
@@ -1794,7 +1802,7 @@ __global__ void __launch_bounds__(kJoinThreads) saga_tree_join_kernel(const Tree
       for (int k = 0; k < BATCH; ++k) {
         const int i = i0 + k * AT_ONCE + sub;
         const float fw = __shfl_sync(0xffffffffu, wt, i & 31);
-        if (i < here && fw > 0.f) {  // a partial without weights may hold anything
+        if (i < here && fw != 0.f) {  // a partial without weights may hold anything
           o.x = fmaf(fw, x[k].x, o.x);
           o.y = fmaf(fw, x[k].y, o.y);
           o.z = fmaf(fw, x[k].z, o.z);
@@ -1834,7 +1842,7 @@ __global__ void __launch_bounds__(kJoinThreads) saga_tree_join_kernel(const Tree
     }
   }
   if (lane >= LANES) return;
-  const float inv = sum > 0.f ? 1.f / sum : 0.f;
+  const float inv = inverse_of(sum);
   const size_t at = (size_t)row * d + blockIdx.y * COLS + l4 * 4;
   if (p.out_bf16) {
     *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.out) + at) =

@@ -62,3 +62,45 @@ def test_rows_that_nobody_sees_may_hold_anything(q_scale, spread, heads, T, fmt,
         off = np.abs(got - exact)
         assert (off <= bound).all(), (b, float((off - bound).max()))
     assert saga.saga_get_status(ws) == 0
+
+
+@pytest.mark.parametrize("fmt", [BF16, E4M3])
+@pytest.mark.parametrize("heads,T", [((12, 1, 4, 128), 2), ((8, 1, 8, 64), 2), ((32, 2, 8, 64), 16), ((8, 1, 1, 128), 16)])
+@pytest.mark.parametrize("what,row", [("k", 0), ("k", 130), ("k", 2999), ("v", 131)])
+@pytest.mark.parametrize("thresholds", [False, True])
+def test_a_nan_that_is_seen_shows(thresholds, heads, T, fmt, what, row):
+    """Seen rows have to be finite; a NaN among them makes the outputs that it belongs to NaN, never finite numbers,
+    where one CTA holds the item (a batch row of few tiles) and where several do."""
+    h_q, h_k, h_v, d = heads
+    prefixes = [3000, 200] if row < 200 else [3000, 3000]
+    shape = saga.SagaShape.of(2, *heads, 3000 + T)
+    g = torch.Generator().manual_seed(50 + T)
+    cache, K, V = tree._fill(shape, fmt, g)
+    q = torch.randn((2, T, h_q, d), generator=g).to(torch.bfloat16)
+    # thresholds below every score
+    tau = torch.full((2, h_q), -1e4, device="cuda") if thresholds else None
+    calls = []
+    for b in range(2):  # the batch row that holds the NaN
+        c = saga.KVCache(*[t.clone() for t in cache._tensors() if t is not None])
+        t = c.k if what == "k" else c.v
+        if fmt == E4M3:
+            t.view(torch.uint8)[b, 0, row, 5] = 0x7F
+        else:
+            t[b, 0, row, 5] = float("nan")
+        out = torch.zeros((2, T, h_q, d), device="cuda")
+        ws = saga.alloc_tree_workspace(shape, T)
+        saga.saga_tree_attn(shape, q.cuda(), c, _i32(prefixes), out, ws, tau=tau)
+        assert saga.saga_get_status(ws) == 0
+        calls.append(out.cpu())
+    clean = torch.zeros((2, T, h_q, d), device="cuda")
+    saga.saga_tree_attn(shape, q.cuda(), cache, _i32(prefixes), clean, saga.alloc_tree_workspace(shape, T), tau=tau)
+    clean = clean.cpu()
+    assert torch.isfinite(clean).all()
+    for b, out in enumerate(calls):
+        hit = torch.zeros((2, T, h_q, d), dtype=torch.bool)
+        if what == "k":
+            hit[b, :, :h_q // h_k] = True  # every output of the key head's queries
+        else:
+            hit[b, :, :h_q // h_v, 5] = True
+        assert torch.isnan(out[hit]).all(), (b, int(torch.isfinite(out[hit]).sum()))
+        assert torch.equal(out[~hit], clean[~hit])
