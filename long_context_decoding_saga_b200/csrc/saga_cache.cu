@@ -353,8 +353,8 @@ __global__ void __launch_bounds__(256) saga_load_kernel(const LoadParams p) {
     u[i] = make_uint2(0u, 0u);
     s[i] = 0.f;
     if (at < pieces) {
-      u[i] = __ldg(reinterpret_cast<const uint2*>(codes) + at);
-      s[i] = __ldg(scales + at / PPR);
+      u[i] = reinterpret_cast<const uint2*>(codes)[at];
+      s[i] = scales[at / PPR];
     }
   }
 #pragma unroll

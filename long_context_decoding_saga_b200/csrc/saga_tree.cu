@@ -937,7 +937,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
         for (int i = 0; i < FLIGHT; ++i) {
           const int row = col0 + i * STEP < cols ? out_row[col0 + i * STEP] : -1;
           x[i] = make_uint4(0u, 0u, 0u, 0u);
-          if (row >= 0) x[i] = __ldg(reinterpret_cast<const uint4*>(p.q + (size_t)row * D + c * 8));
+          if (row >= 0) x[i] = *reinterpret_cast<const uint4*>(p.q + (size_t)row * D + c * 8);
         }
 #pragma unroll
         for (int i = 0; i < FLIGHT; ++i) {
@@ -1542,7 +1542,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
         for (int i = 0; i < FLIGHT; ++i) {
           const int row = out_row[row0 + i * STEP];
           x[i] = make_uint4(0u, 0u, 0u, 0u);
-          if (row >= 0) x[i] = __ldg(reinterpret_cast<const uint4*>(p.q + (size_t)row * D + c * 8));
+          if (row >= 0) x[i] = *reinterpret_cast<const uint4*>(p.q + (size_t)row * D + c * 8);
         }
 #pragma unroll
         for (int i = 0; i < FLIGHT; ++i) {
