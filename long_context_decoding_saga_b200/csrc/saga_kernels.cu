@@ -71,13 +71,13 @@ __device__ __forceinline__ void load_bf16(const uint16_t* src, float (&v)[N]) {
 template <int N>
 __device__ __forceinline__ void load_bf16_global(const uint16_t* src, float (&v)[N]) {
   if constexpr (N == 4) {
-    const uint2 raw = __ldg(reinterpret_cast<const uint2*>(src));
+    const uint2 raw = *reinterpret_cast<const uint2*>(src);
     v[0] = bf16_lo(raw.x);
     v[1] = bf16_hi(raw.x);
     v[2] = bf16_lo(raw.y);
     v[3] = bf16_hi(raw.y);
   } else {
-    const uint32_t raw = __ldg(reinterpret_cast<const uint32_t*>(src));
+    const uint32_t raw = *reinterpret_cast<const uint32_t*>(src);
     v[0] = bf16_lo(raw);
     v[1] = bf16_hi(raw);
   }
@@ -254,7 +254,7 @@ __device__ float raw_threshold(float tv, float s) {
 template <int NP>
 __device__ __forceinline__ float load_tau(int et, const SplitParams& p, int b, int j0, bool compare) {
   float tv = INFINITY;
-  if (compare && et < p.G) tv = p.tau != nullptr ? __ldg(p.tau + (size_t)b * p.h_q + j0 + et) : -INFINITY;
+  if (compare && et < p.G) tv = p.tau != nullptr ? p.tau[(size_t)b * p.h_q + j0 + et] : -INFINITY;
   return tv;
 }
 
@@ -896,10 +896,10 @@ __global__ void __launch_bounds__(192, SplitSmem<D, NP, UMMA>::CTAS_PER_SM)
       }
       qv[k] = make_uint4(0, 0, 0, 0);
       if (i < QCH && n < p.G)
-        qv[k] = __ldg(reinterpret_cast<const uint4*>(p.q + ((size_t)b * p.h_q + j0 + n) * D + col));
+        qv[k] = *reinterpret_cast<const uint4*>(p.q + ((size_t)b * p.h_q + j0 + n) * D + col);
     }
     tv = load_tau<NP>(eth, p, b, j0, !DUMP);
-    if (DHIST && p.hist_out != nullptr && p.tau != nullptr && eth < p.G) tv = __ldg(p.tau + (size_t)b * p.h_q + j0 + eth);
+    if (DHIST && p.hist_out != nullptr && p.tau != nullptr && eth < p.G) tv = p.tau[(size_t)b * p.h_q + j0 + eth];
   }
   // the epilogue compares raw dot products (scaled only once listed)
   if (!DUMP && warp >= 2 && eth < NP) tv = raw_threshold(tv, p.scale);
@@ -1104,7 +1104,7 @@ __global__ void __launch_bounds__(192, SplitSmem<D, NP, UMMA>::CTAS_PER_SM)
 template <int NP>
 __device__ __forceinline__ void load_scores(float (&dst)[NP], const float* srow, long long ld, int G, int tok, int end) {
 #pragma unroll
-  for (int jl = 0; jl < NP; ++jl) dst[jl] = (jl < G && tok < end) ? __ldg(srow + (size_t)jl * ld + tok) : -INFINITY;
+  for (int jl = 0; jl < NP; ++jl) dst[jl] = (jl < G && tok < end) ? srow[(size_t)jl * ld + tok] : -INFINITY;
 }
 
 // Value staging of the compare/gather pass: 4 KB per warp list buffer at
@@ -1325,7 +1325,7 @@ __global__ void __launch_bounds__(DenseSmem<D, NP>::THREADS, DenseSmem<D, NP>::C
       const int i = eth + k * kEpiThreads;
       const int n = (i / 8) % NPM, col = (i / (NPM * 8)) * 64 + (i % 8) * 8;
       qv[k] = make_uint4(0, 0, 0, 0);
-      if (i < QCH && n < p.G) qv[k] = __ldg(reinterpret_cast<const uint4*>(p.q + ((size_t)b * p.h_q + j0 + n) * D + col));
+      if (i < QCH && n < p.G) qv[k] = *reinterpret_cast<const uint4*>(p.q + ((size_t)b * p.h_q + j0 + n) * D + col);
     }
   }
   const int L = device_seq_len(p.seq_len_dev, p.seq_len, p.l_cap, (s == 0 && h == 0 && b == 0) ? p.status : nullptr);
@@ -1737,7 +1737,7 @@ __device__ __forceinline__ void scan_row(const float* row, int L, F&& f) {
 #pragma unroll
     for (int u = 0; u < kScanUnroll; ++u) {
       const int i = i0 + u * kSelectThreads;
-      v[u] = i < nvec ? __ldg(row4 + i) : make_float4(0.f, 0.f, 0.f, 0.f);
+      v[u] = i < nvec ? row4[i] : make_float4(0.f, 0.f, 0.f, 0.f);
     }
 #pragma unroll
     for (int u = 0; u < kScanUnroll; ++u) {
@@ -1902,7 +1902,7 @@ __device__ __forceinline__ void scan_range(const float* row, int begin, int end,
 #pragma unroll
     for (int u = 0; u < kScanUnroll; ++u) {
       const int i = i0 + u * nt;
-      v[u] = i < nvec ? __ldg(row4 + v0 + i) : make_float4(0.f, 0.f, 0.f, 0.f);
+      v[u] = i < nvec ? row4[v0 + i] : make_float4(0.f, 0.f, 0.f, 0.f);
     }
 #pragma unroll
     for (int u = 0; u < kScanUnroll; ++u) {
@@ -2160,7 +2160,7 @@ __global__ void __launch_bounds__(kQkvWarps * 32, NB == 1 ? 4 : 2) saga_qkv_kern
     for (int i = threadIdx.x; i < NB * (kn / 8); i += blockDim.x) {
       const int b = i / (kn / 8), c = i % (kn / 8);
       uint4 v = make_uint4(0u, 0u, 0u, 0u);
-      if (b < p.batch) v = __ldg(reinterpret_cast<const uint4*>(p.x + (size_t)b * p.hidden + k0) + c);
+      if (b < p.batch) v = reinterpret_cast<const uint4*>(p.x + (size_t)b * p.hidden + k0)[c];
       *reinterpret_cast<uint4*>(xs + b * kQkvChunk + c * 8) = v;
     }
     __syncthreads();
@@ -2272,7 +2272,7 @@ __global__ void __launch_bounds__(kQkvMmaThreads)
       for (int j = 0; j < 8; ++j) {
         const int k = (kb0 + kq + j) * kQkvTileK + c * 8;
         v[j] = make_uint4(0u, 0u, 0u, 0u);
-        if (row_live && kq + j < nkb && k < p.hidden) v[j] = __ldg(reinterpret_cast<const uint4*>(xrow + k));
+        if (row_live && kq + j < nkb && k < p.hidden) v[j] = *reinterpret_cast<const uint4*>(xrow + k);
       }
 #pragma unroll
       for (int j = 0; j < 8; ++j)

@@ -10,8 +10,8 @@ import pytest
 ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 CSRC = os.path.join(ROOT, "long_context_decoding_saga_b200", "csrc")
 
-# file: what its read-only loads may be of (the weights of the norms)
-WEIGHTS = {"saga_cache.cu": ("wp + c * 8",), "saga_tree.cu": ()}
+# file: what its read-only loads may be of (the weights of the norms and of the QKV projection)
+WEIGHTS = {"saga_cache.cu": ("wp + c * 8",), "saga_kernels.cu": ("wrow + k0",), "saga_tree.cu": ()}
 
 
 @pytest.mark.parametrize("name", sorted(WEIGHTS))
