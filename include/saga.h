@@ -397,12 +397,17 @@ SAGA_API int saga_kv_load(const saga_shape* s, const saga_cache* cache, int star
  *   q    bf16 [B, tokens, h_q, d], out fp32 or bf16 [B, tokens, h_q, d], dense;
  *   tree_mask uint64 [B, tokens]; bits at or past counts[b] are ignored;
  *   1 <= tokens <= SAGA_TREE_MAX_TOKENS.
- * Scores, softmax statistics and sums are fp32; the softmax weights are rounded
- * before the product with the values, to 8 significant bits or more (bf16
- * caches) or 9 (8-bit caches).  Rows of absent tokens of out are left as they
- * are.  Cache rows that no present token sees may hold
- * anything; a row that some token sees must be finite (a NaN in it
- * makes the outputs that it belongs to NaN).  A prefix outside
+ * Scores, softmax statistics and sums are fp32, so a score within rounding of
+ * its threshold may fall on either side.  The softmax weights are rounded before
+ * the product with the values.  bf16 caches: to 8 significant bits, or to 16
+ * where at most 8 query rows (heads times tokens) of a key head share a value
+ * head.  8-bit caches: to 9 significant bits, but off by up to 2^-27 of the
+ * largest (in the part of the cache that one CTA takes) where that is more; q
+ * there is rounded too, each element off by at most 2^-17 of its head's largest
+ * (exact for those above 2^-9 of it).
+ * Rows of absent tokens of out are left as they are.  Cache rows that no present
+ * token sees may hold anything; a row that some token sees must be finite (a NaN
+ * in it makes the outputs that it belongs to NaN).  A prefix outside
  * [0, l_cap - counts[b]] is clamped and flagged in the status word (word 0 of
  * the workspace, saga_get_status).  out overlaps no other argument.
  * workspace: saga_tree_workspace_bytes(s, tokens) bytes of device memory,

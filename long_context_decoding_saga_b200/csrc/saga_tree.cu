@@ -27,11 +27,15 @@
 //
 // 8-bit caches: the codes go to the tensor cores as they are (kind::f8f6f4), so
 // a tile is read once, by TMA, and nothing is widened.  The other operands are
-// given in pieces: q, scaled by a power of two, as the sum of two e4m3 numbers
-// (4 + 4 of bf16's 8 bits, exact for all elements but those 2^-14 below the
-// row's largest), whose products add up in the same accumulators; the weights as
-// the sum of three e5m2 numbers (each off by 2^-3 of what is left: 2^-9; with two
-// the error of an output over a long cache was twice that of rounding it).  With
+// given in pieces: q, scaled by a power of two that brings the row's largest
+// element into [128, 256), as the sum of two e4m3 numbers (4 + 4 of bf16's 8 bits:
+// exact down to 2^-9 of 128, smaller elements off by at most 2^-17 of it), whose
+// products add up in the same accumulators; the weights as the sum of three e5m2
+// numbers (each off by 2^-3 of what is left: 2^-9; with two the error of an output
+// over a long cache was twice that of rounding it).  e5m2 ends at 2^-16, and the
+// largest weight of a segment's first tile is put at 2^10: weights below 2^-18 of
+// it have fewer bits, and those below 2^-27 of it are left out of the products,
+// though not of the sum that they are divided by.  With
 // queries as columns the pieces are columns of one product, added at a segment's
 // end: a product of 48 columns takes little longer than one of 16 (one token
 // over 128K rows 34.9 -> 30.7 us).
