@@ -248,14 +248,15 @@ SAGA_API int saga_noalloc_get_status(void* stream, unsigned* status);
 SAGA_API const char* saga_noalloc_last_error(void);
 
 /* Test hook for failure detection (no counterpart in the paper).  The next
- * saga_decode_attn / saga_decode_step call on this host thread, if it is a
- * reuse step (step % R != 0) run by the context-split attention kernel,
- * makes that kernel's epilogue wait, for at most limit_ns, on a barrier
- * that nothing arrives at, instead of running.  The wait gives up, the
- * kernel's pipeline unwinds (in-flight copies drained, TMEM freed) and
- * SAGA_STATUS_TIMEOUT is set in the status word; the call's results are then
- * invalid and the context stays usable.  One-shot: consumed by that next
- * call whatever its kind; limit_ns = 0 cancels a pending request. */
+ * saga_decode_attn / saga_decode_step / saga_tree_attn call on this host
+ * thread, if it is a reuse step (step % R != 0) run by the context-split
+ * attention kernel, or attention of drafted tokens, makes that kernel's epilogue
+ * (drafted tokens: the warp that issues the products) wait, for at most limit_ns,
+ * on a barrier that nothing arrives at, instead of running.  The wait gives up, the kernel's pipeline unwinds (in-flight copies
+ * drained, TMEM freed) and SAGA_STATUS_TIMEOUT is set in the status word; the
+ * call's results are then invalid and the context stays usable.  One-shot:
+ * consumed by that next call whatever its kind; limit_ns = 0 cancels a pending
+ * request. */
 SAGA_API int saga_test_expire_next_wait(unsigned limit_ns);
 
 /* ---------------------------------------------------------------------------
@@ -393,7 +394,7 @@ SAGA_API int saga_kv_load(const saga_shape* s, const saga_cache* cache, int star
  *   A[i] = q[b, t, j] . K[i] / sqrt(d) over the visible rows i,
  *   kept: all of them, or with tau (fp32 [B, h_q], the thresholds of the last
  *         refresh) those with A[i] >= tau[b, j], as a reuse step keeps them,
- *   out[b, t, j] = softmax(A)[kept] V[kept];  0 where nothing is kept.
+ *   out[b, t, j] = softmax(A[kept]) V[kept];  0 where nothing is kept.
  *   q    bf16 [B, tokens, h_q, d], out fp32 or bf16 [B, tokens, h_q, d], dense;
  *   tree_mask uint64 [B, tokens]; bits at or past counts[b] are ignored;
  *   1 <= tokens <= SAGA_TREE_MAX_TOKENS.

@@ -397,6 +397,11 @@ int api_ok() { return ok(); }
 int api_cuda_fail(cudaError_t e, const char* what) { return cuda_fail(e, what); }
 int api_validate_shape(const saga_shape* s) { return validate_shape(s); }
 int api_device_sms(int* sms) { return device_sms(sms); }
+unsigned api_take_test_wait() {
+  const unsigned ns = g_test_wait_ns;
+  g_test_wait_ns = 0;
+  return ns;
+}
 int api_rows_map(CUtensorMap* m, const void* base, long long rows, int d, bool e4m3) {
   EncodeTiledFn enc = get_encode();
   if (enc == nullptr) return fail(SAGA_ERR_CUDA, "cuTensorMapEncodeTiled unavailable from the driver");

@@ -19,6 +19,7 @@ int api_ok();
 int api_cuda_fail(cudaError_t e, const char* what);
 int api_validate_shape(const saga_shape* s);
 int api_device_sms(int* sms);
+unsigned api_take_test_wait();  // the limit of saga_test_expire_next_wait, once (0: none)
 // Tensor map over `rows` cache rows of d elements, kTreeTile rows a box: 64
 // columns of bf16 (one 128-byte swizzle row), or the whole row of e4m3 codes
 // (swizzled in its own 64 or 128 bytes).
@@ -90,6 +91,7 @@ struct TreeParams {
   TreePlan plan;
   TreeSmem smem;
   int ctas;        // of the attention kernel
+  unsigned test_wait_ns;  // saga_test_expire_next_wait: a wait in vain before the products, for so long (0: none)
   float* part_o;   // [slots, cols, d]: sums of weights times values
   float* part_m;   // [slots, cols]: the power of two that the weights are relative to
   float* part_l;   // [slots, cols]: sums of weights

@@ -675,6 +675,7 @@ __device__ __forceinline__ void block_end(const TreeParams& p, const Block& k, i
   tc_fence_before();
   __syncthreads();
   if (*k.abort_flag != 0) {
+    cp_async_wait_all();  // scales of a tile that is not taken any more
     if (threadIdx.x == 0) {
       flag_status(p.status, SAGA_STATUS_TIMEOUT);
       // loads still in flight land before the shared memory is given up
@@ -772,7 +773,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
   if (warp == 0) {
     if (any) issued = load_tiles<D, E4M3>(p, k, &kmap, &vmap, w);
   } else if (warp == 1) {
-    if (any) {
+    if (any && (p.test_wait_ns == 0u || mbar_wait(bar.drain, 0, abort_flag, p.test_wait_ns))) {
       const uint32_t id_s = E4M3 ? idesc(kE4m3, kE4m3, kTreeTile, cols, false) : idesc(kBf16, kBf16, kTreeTile, cols, false);
       const uint32_t id_o = E4M3 ? idesc(kE4m3, kE5m2, D, pcols, true) : idesc(kBf16, kBf16, 128, p.plan.nvp, true);
       const uint32_t id_l = idesc(kBf16, kBf16, 64, cols, true);
@@ -1399,7 +1400,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
   if (warp == 0) {
     if (any) issued = load_tiles<D, E4M3>(p, k, &kmap, &vmap, w);
   } else if (warp == 1) {
-    if (any) {
+    if (any && (p.test_wait_ns == 0u || mbar_wait(bar.drain, 0, abort_flag, p.test_wait_ns))) {
       const uint32_t id_s = E4M3 ? idesc(kE4m3, kE4m3, 128, kTreeTile, false) : idesc(kBf16, kBf16, 128, kTreeTile, false);
       // V as it lies: its rows are the inner dimension
       const uint32_t id_o = (E4M3 ? idesc(kE5m2, kE4m3, 128, D, false) : idesc(kBf16, kBf16, 128, D, false)) | 1u << 16;
@@ -1961,6 +1962,7 @@ int saga_tree_attn(const saga_shape* s, int tokens, const void* q, const saga_ca
   p.h_v = s->h_v;
   p.l_cap = s->l_cap;
   p.ctas = std::min(sms, kTreeMaxCtas);
+  p.test_wait_ns = api_take_test_wait();
   char* base = static_cast<char*>(workspace);
   p.part_o = reinterpret_cast<float*>(base + kTreeStatusBytes);
   p.part_m = reinterpret_cast<float*>(base + z.part_m);

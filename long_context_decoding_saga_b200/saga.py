@@ -389,8 +389,8 @@ def saga_noalloc_get_status(stream=None) -> int:
 
 
 def saga_test_expire_next_wait(limit_ns: int):
-    """Test hook: the next decode call's keep kernel (a sparse reuse step) waits on a barrier nothing arrives
-    at, for at most limit_ns, then unwinds and flags SAGA_STATUS_TIMEOUT (0 cancels)."""
+    """Test hook: the next decode call's keep kernel (a sparse reuse step), or the next drafted-token attention, waits
+    on a barrier nothing arrives at, for at most limit_ns, then unwinds and flags SAGA_STATUS_TIMEOUT (0 cancels)."""
     _check(load().saga_test_expire_next_wait(int(limit_ns)))
 
 

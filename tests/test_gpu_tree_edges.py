@@ -104,3 +104,32 @@ def test_a_nan_that_is_seen_shows(thresholds, heads, T, fmt, what, row):
             hit[b, :, :h_q // h_v, 5] = True
         assert torch.isnan(out[hit]).all(), (b, int(torch.isfinite(out[hit]).sum()))
         assert torch.equal(out[~hit], clean[~hit])
+
+
+@pytest.mark.parametrize("fmt", [BF16, E4M3])
+@pytest.mark.parametrize("heads,T", [((12, 1, 4, 128), 2), ((8, 1, 8, 64), 2), ((32, 2, 8, 64), 16), ((8, 1, 1, 128), 16)])
+def test_a_wait_that_runs_out_is_flagged_and_the_context_stays_usable(heads, T, fmt):
+    """The products of every CTA with tiles wait in vain for 2 ms; the CTA gives up and unwinds: the call returns, the
+    status word says so, and the next calls, on the same workspace and on a fresh one, are right."""
+    h_q, h_k, h_v, d = heads
+    shape = saga.SagaShape.of(2, *heads, 3000 + T)
+    g = torch.Generator().manual_seed(60 + T)
+    cache, K, V = tree._fill(shape, fmt, g)
+    q = torch.randn((2, T, h_q, d), generator=g).to(torch.bfloat16)
+    prefixes = [3000, 200]
+    ws = saga.alloc_tree_workspace(shape, T)
+    args = (shape, q.cuda(), cache, _i32(prefixes))
+    saga.saga_test_expire_next_wait(2_000_000)
+    saga.saga_tree_attn(*args, torch.empty((2, T, h_q, d), device="cuda"), ws)
+    torch.cuda.synchronize()
+    assert saga.saga_get_status(ws) == saga.SAGA_STATUS_TIMEOUT
+    ws2 = saga.alloc_tree_workspace(shape, T)
+    outs = []
+    for w in (ws, ws2):
+        outs.append(torch.empty((2, T, h_q, d), device="cuda"))
+        saga.saga_tree_attn(*args, outs[-1], w)
+    assert saga.saga_get_status(ws2) == 0
+    assert torch.equal(outs[0], outs[1])
+    for b, P in enumerate(prefixes):
+        exact, bound, _, _ = tree._bounds(q[b].double().numpy(), K[b], V[b], P, T, None, None, d, fmt)
+        assert (np.abs(outs[0][b].double().cpu().numpy() - exact) <= bound).all()
