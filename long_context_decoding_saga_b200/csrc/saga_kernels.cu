@@ -38,6 +38,7 @@
 #include <utility>
 
 #include "saga_device.cuh"
+#include "saga_launch.cuh"
 #include "saga_internal.h"
 
 namespace saga {
@@ -2357,59 +2358,17 @@ __global__ void __launch_bounds__(kQkvMmaThreads)
 // Every kernel is launched with programmatic stream serialization: it may
 // start while the previous kernel on the stream finishes, runs its
 // independent setup, and waits (pdl_wait) before touching shared data.
-// SAGA_PDL=0 in the environment turns this off (plain stream order).
-static bool pdl_enabled() {
-  static const bool on = [] {
-    const char* e = getenv("SAGA_PDL");
-    return !(e != nullptr && e[0] == '0');
-  }();
-  return on;
-}
-
-template <typename... KArgs, typename... Args>
-static cudaError_t launch_k(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t smem, cudaStream_t st,
-                            Args&&... args) {
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = grid;
-  cfg.blockDim = block;
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = st;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = pdl_enabled() ? 1 : 0;
-  return cudaLaunchKernelEx(&cfg, kernel, std::forward<Args>(args)...);
-}
-
-// cudaFuncSetAttribute holds per device: one bit per device ordinal.
-// Per kernel and device, once: the dynamic shared memory it may take, and
-// the largest shared-memory carveout.  Every kernel of the library asks for
-// the same carveout, so an SM running a small kernel (a combine) never has
-// to drain and reconfigure before a split CTA of the next call can join it.
-static cudaError_t ensure_smem(const void* fn, int bytes, std::atomic<uint64_t>& done) {
-  int dev = 0;
-  cudaError_t e = cudaGetDevice(&dev);
-  if (e != cudaSuccess) return e;
-  const uint64_t bit = 1ull << (dev & 63);
-  if (done.load(std::memory_order_acquire) & bit) return cudaSuccess;
-  if (bytes > 0) e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
-  if (e == cudaSuccess)
-    e = cudaFuncSetAttribute(fn, cudaFuncAttributePreferredSharedMemoryCarveout, cudaSharedmemCarveoutMaxShared);
-  if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_release);
-  return e;
-}
-
+// (launch_pdl and prepare_kernel: saga_launch.cuh.)
 template <int D, int NP, bool UMMA, bool DUMP>
 static cudaError_t run_split(const CUtensorMap& tf, const CUtensorMap& tp, const SplitParams& p, dim3 grid,
                              cudaStream_t st, int* occ) {
   using K = SplitSmem<D, NP, UMMA>;
   static std::atomic<uint64_t> prepared{0};
-  cudaError_t e = ensure_smem(reinterpret_cast<const void*>(saga_split_kernel<D, NP, UMMA, DUMP>), K::ALLOC, prepared);
+  cudaError_t e = prepare_kernel(reinterpret_cast<const void*>(saga_split_kernel<D, NP, UMMA, DUMP>), K::ALLOC, prepared);
   if (e != cudaSuccess) return e;
   if (occ != nullptr)
     return cudaOccupancyMaxActiveBlocksPerMultiprocessor(occ, saga_split_kernel<D, NP, UMMA, DUMP>, 192, K::ALLOC);
-  return launch_k(saga_split_kernel<D, NP, UMMA, DUMP>, grid, dim3(192), K::ALLOC, st, tf, tp, p);
+  return launch_pdl(saga_split_kernel<D, NP, UMMA, DUMP>, grid, dim3(192), K::ALLOC, st, tf, tp, p);
 }
 
 template <int D>
@@ -2445,11 +2404,11 @@ template <int D, int NP>
 static cudaError_t run_from_scores(const SplitParams& p, dim3 grid, cudaStream_t st, int* occ) {
   static std::atomic<uint64_t> prepared{0};
   const int bytes = FromScoresSmem<D, NP>::BYTES;
-  cudaError_t e = ensure_smem(reinterpret_cast<const void*>(saga_from_scores_kernel<D, NP>), bytes, prepared);
+  cudaError_t e = prepare_kernel(reinterpret_cast<const void*>(saga_from_scores_kernel<D, NP>), bytes, prepared);
   if (e != cudaSuccess) return e;
   if (occ != nullptr)
     return cudaOccupancyMaxActiveBlocksPerMultiprocessor(occ, saga_from_scores_kernel<D, NP>, kEpiThreads, bytes);
-  return launch_k(saga_from_scores_kernel<D, NP>, grid, dim3(kEpiThreads), bytes, st, p);
+  return launch_pdl(saga_from_scores_kernel<D, NP>, grid, dim3(kEpiThreads), bytes, st, p);
 }
 
 template <int D, int NP>
@@ -2457,11 +2416,11 @@ static cudaError_t run_dense(const CUtensorMap& kf, const CUtensorMap& kp, const
                              const SplitParams& p, dim3 grid, cudaStream_t st, int* occ) {
   using K = DenseSmem<D, NP>;
   static std::atomic<uint64_t> prepared{0};
-  cudaError_t e = ensure_smem(reinterpret_cast<const void*>(saga_dense_kernel<D, NP>), K::ALLOC, prepared);
+  cudaError_t e = prepare_kernel(reinterpret_cast<const void*>(saga_dense_kernel<D, NP>), K::ALLOC, prepared);
   if (e != cudaSuccess) return e;
   if (occ != nullptr)
     return cudaOccupancyMaxActiveBlocksPerMultiprocessor(occ, saga_dense_kernel<D, NP>, K::THREADS, K::ALLOC);
-  return launch_k(saga_dense_kernel<D, NP>, grid, dim3(K::THREADS), K::ALLOC, st, kf, kp, vf, vp, p);
+  return launch_pdl(saga_dense_kernel<D, NP>, grid, dim3(K::THREADS), K::ALLOC, st, kf, kp, vf, vp, p);
 }
 
 // Dense attention (every token kept) for groups whose query heads share one
@@ -2488,14 +2447,14 @@ cudaError_t launch_combine(int D, const CombineParams& p, cudaStream_t st) {
   static std::atomic<uint64_t> prepared64{0}, prepared128{0};
   cudaError_t e;
   if (D == 64) {
-    e = ensure_smem(reinterpret_cast<const void*>(saga_combine_kernel<64>), 0, prepared64);
+    e = prepare_kernel(reinterpret_cast<const void*>(saga_combine_kernel<64>), 0, prepared64);
     if (e != cudaSuccess) return e;
-    return launch_k(saga_combine_kernel<64>, dim3(p.rows, 2), dim3(kCombineThreads), 0, st, p);
+    return launch_pdl(saga_combine_kernel<64>, dim3(p.rows, 2), dim3(kCombineThreads), 0, st, p);
   }
   if (D == 128) {
-    e = ensure_smem(reinterpret_cast<const void*>(saga_combine_kernel<128>), 0, prepared128);
+    e = prepare_kernel(reinterpret_cast<const void*>(saga_combine_kernel<128>), 0, prepared128);
     if (e != cudaSuccess) return e;
-    return launch_k(saga_combine_kernel<128>, dim3(p.rows, 4), dim3(kCombineThreads), 0, st, p);
+    return launch_pdl(saga_combine_kernel<128>, dim3(p.rows, 4), dim3(kCombineThreads), 0, st, p);
   }
   return cudaErrorInvalidValue;
 }
@@ -2503,16 +2462,16 @@ cudaError_t launch_combine(int D, const CombineParams& p, cudaStream_t st) {
 cudaError_t launch_select(const SelectParams& p, int rows, cudaStream_t st) {
   static std::atomic<uint64_t> prepared{0};
   const int bytes = kSelectCap * 4;
-  cudaError_t e = ensure_smem(reinterpret_cast<const void*>(atopn_select_kernel), bytes, prepared);
+  cudaError_t e = prepare_kernel(reinterpret_cast<const void*>(atopn_select_kernel), bytes, prepared);
   if (e != cudaSuccess) return e;
-  return launch_k(atopn_select_kernel, dim3(rows), dim3(kSelectThreads), bytes, st, p);
+  return launch_pdl(atopn_select_kernel, dim3(rows), dim3(kSelectThreads), bytes, st, p);
 }
 
 // The refresh path's select for a few long rows: one cluster of CTAs per row.
 cudaError_t launch_select_cluster(const SelectParams& p, int rows, cudaStream_t st) {
   static std::atomic<uint64_t> prepared{0};
   const int bytes = kSelectCap * 4;
-  cudaError_t e = ensure_smem(reinterpret_cast<const void*>(atopn_cluster_select_kernel), bytes, prepared);
+  cudaError_t e = prepare_kernel(reinterpret_cast<const void*>(atopn_cluster_select_kernel), bytes, prepared);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(kSelCluster, rows);
@@ -2535,9 +2494,9 @@ template <int NB>
 static cudaError_t run_qkv(const QkvParams& p, cudaStream_t st) {
   static std::atomic<uint64_t> prepared{0};
   const int bytes = NB * kQkvChunk * 2;
-  cudaError_t e = ensure_smem(reinterpret_cast<const void*>(saga_qkv_kernel<NB>), bytes, prepared);
+  cudaError_t e = prepare_kernel(reinterpret_cast<const void*>(saga_qkv_kernel<NB>), bytes, prepared);
   if (e != cudaSuccess) return e;
-  return launch_k(saga_qkv_kernel<NB>, dim3((p.n_cols + kQkvWarps - 1) / kQkvWarps), dim3(kQkvWarps * 32), bytes, st,
+  return launch_pdl(saga_qkv_kernel<NB>, dim3((p.n_cols + kQkvWarps - 1) / kQkvWarps), dim3(kQkvWarps * 32), bytes, st,
                   p);
 }
 
@@ -2552,7 +2511,7 @@ cudaError_t launch_qkv(const QkvParams& p, const CUtensorMap& tw, cudaStream_t s
   }
   static std::atomic<uint64_t> prepared{0};
   const int bytes = qkv_mma_smem_bytes(p.stages, p.kbs_max);
-  cudaError_t e = ensure_smem(reinterpret_cast<const void*>(saga_qkv_mma_kernel), qkv_mma_smem_bytes(kQkvMaxStages, kQkvMaxKb),
+  cudaError_t e = prepare_kernel(reinterpret_cast<const void*>(saga_qkv_mma_kernel), qkv_mma_smem_bytes(kQkvMaxStages, kQkvMaxKb),
                               prepared);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
@@ -2574,17 +2533,17 @@ cudaError_t launch_qkv(const QkvParams& p, const CUtensorMap& tw, cudaStream_t s
 
 cudaError_t launch_append(const AppendParams& p, cudaStream_t st) {
   static std::atomic<uint64_t> prepared{0};
-  cudaError_t e = ensure_smem(reinterpret_cast<const void*>(saga_append_kernel), 0, prepared);
+  cudaError_t e = prepare_kernel(reinterpret_cast<const void*>(saga_append_kernel), 0, prepared);
   if (e != cudaSuccess) return e;
   const int n = p.batch * (p.h_k + p.h_v) * (p.d / 8);
-  return launch_k(saga_append_kernel, dim3((n + 255) / 256), dim3(256), 0, st, p);
+  return launch_pdl(saga_append_kernel, dim3((n + 255) / 256), dim3(256), 0, st, p);
 }
 
 cudaError_t launch_fill(float* dst, float v, int n, cudaStream_t st) {
   static std::atomic<uint64_t> prepared{0};
-  cudaError_t e = ensure_smem(reinterpret_cast<const void*>(saga_fill_kernel), 0, prepared);
+  cudaError_t e = prepare_kernel(reinterpret_cast<const void*>(saga_fill_kernel), 0, prepared);
   if (e != cudaSuccess) return e;
-  return launch_k(saga_fill_kernel, dim3((n + 255) / 256), dim3(256), 0, st, dst, v, n);
+  return launch_pdl(saga_fill_kernel, dim3((n + 255) / 256), dim3(256), 0, st, dst, v, n);
 }
 
 }  // namespace saga

@@ -1,4 +1,4 @@
-// saga_launch.cuh - launch helpers of the serving operators' kernels.
+// saga_launch.cuh - launch helpers of the kernels.
 #pragma once
 
 #include <cuda_runtime.h>
@@ -9,14 +9,18 @@
 
 namespace saga {
 
-// Launch with programmatic stream serialization, as the decode kernels are
+// Whether kernels are launched with programmatic stream serialization
 // (SAGA_PDL=0 in the environment: plain stream order).
-template <typename... KArgs, typename... Args>
-cudaError_t launch_pdl(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t smem, cudaStream_t st, Args&&... args) {
+inline bool pdl_enabled() {
   static const bool on = [] {
     const char* e = getenv("SAGA_PDL");
     return !(e != nullptr && e[0] == '0');
   }();
+  return on;
+}
+
+template <typename... KArgs, typename... Args>
+cudaError_t launch_pdl(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t smem, cudaStream_t st, Args&&... args) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = grid;
   cfg.blockDim = block;
@@ -26,12 +30,15 @@ cudaError_t launch_pdl(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t s
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = on ? 1 : 0;
+  cfg.numAttrs = pdl_enabled() ? 1 : 0;
   return cudaLaunchKernelEx(&cfg, kernel, std::forward<Args>(args)...);
 }
 
-// Once per kernel and device: its dynamic shared memory and the largest
-// carveout, the same one that the decode kernels ask for.
+// cudaFuncSetAttribute holds per device.  Per kernel and device, once (device
+// ordinals from 64 on: every time): the dynamic shared memory it may take, and
+// the largest shared-memory carveout.  Every kernel of the library asks for the
+// same carveout, so an SM running a small kernel (a combine) never has to drain
+// and reconfigure before a split CTA of the next call can join it.
 inline cudaError_t prepare_kernel(const void* fn, int bytes, std::atomic<uint64_t>& done) {
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);

@@ -928,7 +928,7 @@ int saga_key_head_merge(const saga_merge_shape* s, const void* x, const void* q,
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return cuda_err(e, "cudaGetDevice");
-  const uint64_t bit = 1ull << (dev & 63);
+  const uint64_t bit = dev < 64 ? 1ull << dev : 0ull;  // ordinals from 64 on: every time
   if (!(g_smem_set.load() & bit)) {
     e = cudaFuncSetAttribute(merge_gemm_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, GemmSmem::ALLOC);
     if (e == cudaSuccess)
