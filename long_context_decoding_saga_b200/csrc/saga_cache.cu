@@ -214,10 +214,14 @@ __device__ __forceinline__ void rows_of(const RowParams& p, const Tokens& k, con
 // token into shared memory, while the first rows of each kind are on their way.
 // Rows are taken head by head, so neighbouring lanes write neighbouring cache
 // rows and scales.  For few tokens the time is that of one chain of loads (one
-// token: 3.3 us in a graph); for many it is bound by the instructions per row
-// before HBM (8191 tokens of 42 heads of 64 normed and rotated, 88 MB: 25 us,
-// 54 % of the copy rate; two prompts of up to 4097 tokens of 17 heads of 128,
-// half rotated, into an 8-bit cache, 56 MB: 18 us).
+// token: 3.1 us in a graph).  Calls on new rows each time: 8191 tokens of 42
+// heads of 64 normed and rotated, 88 MB, 25 us, 54 % of the copy rate; two prompts
+// of up to 4097 tokens of 17 heads of 128, half rotated, into an 8-bit cache,
+// 56 MB, 18 us, 47 %.  The same rows again and again, of which the L2 keeps some
+// or all: 22.5 and 12.5 us.  The first is bound by its instructions before HBM
+// (71 % of the issue slots while a CTA runs; a warp is mostly ready or in a
+// fixed-latency wait), the second waits for its loads as much (58 % of the issue
+// slots; a third of a warp's time in those waits).
 template <int D, bool E4M3>
 __global__ void __launch_bounds__(kRowThreads) saga_rows_kernel(const RowParams p) {
   constexpr int LPR = D / 8;
@@ -475,7 +479,9 @@ int run_rows(const saga_shape* s, int tokens, const saga_rows* q, const saga_row
   // Tokens of a CTA: its start takes about as long as two tokens, and an SM
   // holds 4 CTAs at a time.  17 heads of 128, normed and rotated: 2048 tokens in
   // 2048, 1024 and 512 CTAs 14.8, 10.2 and 7.8 us; 42 heads of 64: 8191 tokens in
-  // 2048, 1024 and 512 CTAs 25.5, 23.1 and 25.5 us.
+  // 2048, 1024 and 512 CTAs 25.5, 23.1 and 25.5 us (the same rows again and again,
+  // warm in the L2 as far as they fit).  Tokens of 2200 and 2700 elements; much
+  // smaller ones were not measured.
   const int most = q == nullptr ? 64 : kMaxRowTokens;
   int group = 1;
   long long least = 0;

@@ -69,16 +69,21 @@ __device__ __forceinline__ void load_bf16(const uint16_t* src, float (&v)[N]) {
   }
 }
 
+// From a cache: written in place, so that the load is issued where it stands
+// (0.05 us a layer faster than the compiler's placement; an ordinary load, since
+// the kernel before may have written the row while this one started).
 template <int N>
 __device__ __forceinline__ void load_bf16_global(const uint16_t* src, float (&v)[N]) {
   if constexpr (N == 4) {
-    const uint2 raw = *reinterpret_cast<const uint2*>(src);
+    uint2 raw;
+    asm volatile("ld.global.v2.u32 {%0, %1}, [%2];" : "=r"(raw.x), "=r"(raw.y) : "l"(src));
     v[0] = bf16_lo(raw.x);
     v[1] = bf16_hi(raw.x);
     v[2] = bf16_lo(raw.y);
     v[3] = bf16_hi(raw.y);
   } else {
-    const uint32_t raw = *reinterpret_cast<const uint32_t*>(src);
+    uint32_t raw;
+    asm volatile("ld.global.u32 %0, [%1];" : "=r"(raw) : "l"(src));
     v[0] = bf16_lo(raw);
     v[1] = bf16_hi(raw);
   }

@@ -739,8 +739,8 @@ __device__ __forceinline__ void put_q8(uint8_t* at, int count, int row, int c, c
 // A tile of few columns is bound by its loads and one chain (scores, weights,
 // products); about 8 us go before the first product and to the end of the
 // join.  12/1/4 heads of 128 over 128K rows: one token from an 8-bit cache
-// (87 MB) 31 us, 4 tokens under thresholds from a bf16 cache (168 MB) 40 us,
-// 4.1 TB/s; 4 tokens over 1K rows of 8/1/8 heads of 64 15 us.
+// (87 MB) 31 us, 4 tokens under thresholds from a bf16 cache (168 MB) 41 us,
+// 4.1 TB/s; 4 tokens over 1K rows of 8/1/8 heads of 64 16 us.
 template <int D, bool E4M3>
 __global__ void __launch_bounds__(kTreeThreads, 1)
     saga_tree_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
@@ -1224,7 +1224,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
 // slots, 41 % of the exponentials' pipe and 21 % of the tensor pipe.  Leaving out
 // the exponentials, the sums or the products changes it by less than 5 %; twice
 // the warps with half of the scores each take 8 % more (bf16; 8-bit ones spill).
-// 64 tokens over 8 ragged rows of up to 16K of 32/8/8 heads of 64: 105 us; 16
+// 64 tokens over 8 ragged rows of up to 16K of 32/8/8 heads of 64: 106 us; 16
 // tokens over 128K 8-bit rows of 12/1/4 heads of 128: 55 us.
 
 __device__ __forceinline__ void umma_bf16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc, uint32_t id, uint32_t accumulate) {
@@ -1887,12 +1887,12 @@ TreeSizes tree_sizes(const saga_shape* s, const TreePlan& plan, int ctas) {
   return z;
 }
 
-// Queries as rows from so many live rows a chunk on.  A tree of T tokens over
-// 32K rows of 32/2/8 heads of 64 (16 T live rows up to 128), as columns and as
-// rows: bf16 T = 4 20.3 and 20.8 us, T = 6 21.9 and 21.3; 8-bit T = 2 21.7 and
-// 25.5, T = 4 26.4 and 26.2.  Over 16K rows of 32/8/8 heads (4 T live rows):
-// bf16 T = 16 23.3 and 23.8, T = 24 29.0 and 26.9; 8-bit T = 12 32.3 and 32.8,
-// T = 16 37.2 and 33.4.
+// Queries as rows from so many live rows a chunk on.  On caches of up to 42 MB,
+// which stay in the L2 from call to call: a tree of T tokens over 32K rows of
+// 32/2/8 heads of 64 (16 T live rows up to 128), as columns and as rows: bf16
+// T = 4 20.3 and 20.8 us, T = 6 21.9 and 21.3; 8-bit T = 2 21.7 and 25.5, T = 4
+// 26.4 and 26.2.  Over 16K rows of 32/8/8 heads (4 T live rows): bf16 T = 16 23.3
+// and 23.8, T = 24 29.0 and 26.9; 8-bit T = 12 32.3 and 32.8, T = 16 37.2 and 33.4.
 constexpr int kTreeRowsBf16 = 80, kTreeRowsE4m3 = 56;
 bool by_rows(const TreePlan& rows, bool e4m3) { return tree_live_rows(rows) >= (e4m3 ? kTreeRowsE4m3 : kTreeRowsBf16); }
 
